@@ -394,6 +394,121 @@ srnl_status srnl_block_fwd(const void *x, int B, int H, int W, int C, int heads,
                            size_t workspace_bytes, void *out);
 
 /*
+ * Layers around the operator, each with its backward pass: what a residual
+ * block's training needs besides the operator's own [SUMMARY paragraph on
+ * 2-D maps; OVERVIEW Four-Directional Scanning and Spatial Chunking:
+ * projections, normalisation, a depthwise convolution and a feed-forward
+ * network]. Common to them:
+ *   - arrays are dense and row-major; sizes and alignment of rows are free
+ *     (any C, K, N >= 1), base pointers 16-byte aligned. Outputs must not
+ *     overlap inputs, except dx_add = dx, du_add = du and residual or an addend
+ *     = out (of the same type).
+ *   - parameters' gradients are fp32 and overwritten; sums are fp32 in a
+ *     fixed order (bitwise reproducible). Over no rows they are zero.
+ *   - all memory must belong to the device that is current at the call
+ *     (SRNL_ERR_PTR otherwise), and `stream` to it too.
+ */
+
+/*
+ * srnl_layer_norm_fwd -- layer norm over the last axis:
+ *   out[r][c] = (x[r][c] - mean_r) rstd_r gain[c] + bias[c],
+ *   rstd_r = 1 / sqrt(var_r + eps), var biased, taken about the mean.
+ *   x [rows][C] in in_dtype; out [rows][C] in out_dtype; gain, bias [C] fp32,
+ *   either NULL for 1 and 0; mean, rstd [rows] fp32, written unless NULL (the
+ *   backward pass reads them). eps > 0.
+ * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_HIP.
+ */
+srnl_status srnl_layer_norm_fwd(const void *x, long long rows, int C, srnl_dtype in_dtype,
+                                const float *gain, const float *bias, float eps,
+                                srnl_dtype out_dtype, void *out, float *mean, float *rstd,
+                                void *stream);
+
+/*
+ * srnl_layer_norm_bwd -- with n = (x - mean) rstd and g = dout gain, per row
+ *   dx = rstd (g - mean(g) - n mean(g n)) [+ dx_add],
+ *   dgain[c] = sum over rows of dout n,  dbias[c] = sum over rows of dout.
+ *   dout [rows][C] in out_dtype (the forward's); x, dx in in_dtype; dx_add
+ *   [rows][C] in add_dtype or NULL (a residual's gradient); dgain, dbias [C]
+ *   fp32, either NULL if not wanted. Workspace (only with dgain or dbias):
+ *   srnl_layer_norm_bwd_workspace_bytes.
+ * Errors: as the forward, plus SRNL_ERR_WORKSPACE.
+ */
+size_t srnl_layer_norm_bwd_workspace_bytes(long long rows, int C);
+srnl_status srnl_layer_norm_bwd(const void *dout, srnl_dtype out_dtype, const void *x,
+                                long long rows, int C, srnl_dtype in_dtype, const float *gain,
+                                const float *mean, const float *rstd, const void *dx_add,
+                                srnl_dtype add_dtype, void *dx, float *dgain, float *dbias,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+typedef enum { SRNL_ACT_NONE = 0, SRNL_ACT_GELU = 1, SRNL_ACT_SILU = 2 } srnl_act;
+
+/* The linear layer's parameters and types (forward and backward alike). */
+typedef struct {
+    const void *w;             /* [N][K] in w_dtype */
+    const float *bias;         /* [N] or NULL */
+    const void *residual;      /* [M][N] in residual_dtype or NULL; forward only */
+    srnl_dtype x_dtype, w_dtype, residual_dtype, out_dtype;
+    srnl_act act;              /* GELU is the exact (erf) form */
+    void *stream;
+} srnl_linear_params;
+
+/*
+ * srnl_linear_fwd -- z = x w^T + bias, out = act(z) + residual.
+ *   x [M][K]; out [M][N] in out_dtype; pre [M][N] fp32: z, written unless
+ *   NULL (the backward pass of an activation reads it).
+ * Products are exact for bf16 operands and within 2^-26 of each term for
+ * fp32 ones, summed in fp32. Rows with an infinite fp32 operand (or one that
+ * bf16 rounds to infinity, above 3.39e38) come out NaN.
+ * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_HIP.
+ */
+srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N,
+                            const srnl_linear_params *params, void *out, float *pre);
+
+/*
+ * srnl_linear_bwd -- with dz = dout act'(pre) in fp32 (dz = dout without an
+ * activation):
+ *   dx = dz w [+ dx_add],  dw = dz^T x,  db = sum over rows of dz.
+ *   dout [M][N] in out_dtype; dx, dx_add [M][K] in x_dtype, dx_add or NULL;
+ *   dw [N][K], db [N] fp32; any of dx, dw, db NULL if not wanted, db only
+ *   together with dw. pre: as the forward wrote it; ignored without an
+ *   activation. The residual's gradient is dout itself.
+ * Workspace: srnl_linear_bwd_workspace_bytes (may be 0).
+ * Errors: as the forward, plus SRNL_ERR_WORKSPACE.
+ */
+size_t srnl_linear_bwd_workspace_bytes(long long M, int K, int N, const srnl_linear_params *params);
+srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K, int N,
+                            const srnl_linear_params *params, const float *pre, const void *dx_add,
+                            void *dx, float *dw, float *db, void *workspace, size_t workspace_bytes);
+
+/*
+ * srnl_dwconv_fwd -- the depthwise 3x3 branch on an NHWC grid, zero padding:
+ *   out[b][i][j][c] = bias[c] + sum over a, e in 0..2 of
+ *                     w[c][a][e] u[b][i + a - 1][j + e - 1][c] + add1 + add2
+ *   u [B][H][W][C] in in_dtype; w [C][3][3], bias [C] (or NULL) fp32; add1,
+ *   add2 like out in their own types, or NULL (the block's residual and its
+ *   other branch); out in out_dtype.
+ * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_HIP.
+ */
+srnl_status srnl_dwconv_fwd(const void *u, int B, int H, int W, int C, srnl_dtype in_dtype,
+                            const float *w, const float *bias, const void *add1,
+                            srnl_dtype add1_dtype, const void *add2, srnl_dtype add2_dtype,
+                            srnl_dtype out_dtype, void *out, void *stream);
+
+/*
+ * srnl_dwconv_bwd -- du (in in_dtype), dw [C][3][3] and db [C] (fp32) of the
+ * branch from dout (in out_dtype); any NULL if not wanted. du_add, in
+ * in_dtype, or NULL: another gradient of u, added to du. The addends'
+ * gradient is dout itself. Workspace (only with dw or db):
+ * srnl_dwconv_bwd_workspace_bytes.
+ * Errors: as the forward, plus SRNL_ERR_WORKSPACE.
+ */
+size_t srnl_dwconv_bwd_workspace_bytes(int B, int H, int W, int C);
+srnl_status srnl_dwconv_bwd(const void *dout, srnl_dtype out_dtype, const void *u, int B, int H,
+                            int W, int C, srnl_dtype in_dtype, const float *w, const void *du_add,
+                            void *du, float *dw, float *db, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/*
  * srnl_route_gather -- the route traversal as a standalone copy [OVERVIEW
  * Four-Directional Scanning and Spatial Chunking]:
  *   out[slot(r)][b][t][c] = x[b][i][j][c],  (i, j) = route r's t-th cell.

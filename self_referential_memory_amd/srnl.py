@@ -8,6 +8,7 @@ fails loudly when it is missing. There is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -25,6 +26,8 @@ FLAG_HARD_CAP, FLAG_NO_CAP, FLAG_NO_CLAMP, FLAG_FIXED_ALPHA, FLAG_READ_BEFORE = 
 FLAG_FREEZE_KV = 0x20
 FLAG_CHECK_FINITE = 0x40
 FLAG_RECORD = 0x80
+ACT_NONE, ACT_GELU, ACT_SILU = 0, 1, 2
+ACTS = {"none": ACT_NONE, "gelu": ACT_GELU, "silu": ACT_SILU}
 
 EXPORTS = ("srnl_scan_fwd", "srnl_scan_workspace_bytes", "srnl_scan_1d",
            "srnl_scan_1d_workspace_bytes", "srnl_fuse", "srnl_scan_bwd",
@@ -33,6 +36,9 @@ EXPORTS = ("srnl_scan_fwd", "srnl_scan_workspace_bytes", "srnl_scan_1d",
            "srnl_scan_fuse_bwd", "srnl_scan_fuse_bwd_workspace_bytes",
            "srnl_route_gather", "srnl_init_states", "srnl_block_fwd",
            "srnl_block_workspace_bytes",
+           "srnl_layer_norm_fwd", "srnl_layer_norm_bwd", "srnl_layer_norm_bwd_workspace_bytes",
+           "srnl_linear_fwd", "srnl_linear_bwd", "srnl_linear_bwd_workspace_bytes",
+           "srnl_dwconv_fwd", "srnl_dwconv_bwd", "srnl_dwconv_bwd_workspace_bytes",
            "srnl_route_index", "srnl_chunk_len", "srnl_status_string",
            "srnl_last_error")
 
@@ -61,6 +67,14 @@ class BlockWeights(ctypes.Structure):
                 ("w2", ctypes.c_void_p), ("b2", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p), ("ffn_hidden", ctypes.c_int),
                 ("ln_eps", ctypes.c_float)]
+
+
+class LinearParams(ctypes.Structure):
+    """srnl_linear_params."""
+    _fields_ = [("w", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("x_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
+                ("residual_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("stream", ctypes.c_void_p)]
 
 
 _lib = None
@@ -106,6 +120,23 @@ def lib() -> ctypes.CDLL:
         L.srnl_block_workspace_bytes.restype = sz
         L.srnl_block_fwd.argtypes = [vp, i, i, i, i, i, i, u, ctypes.POINTER(Params),
                                      ctypes.POINTER(BlockWeights), vp, sz, vp]
+        ll, lp = ctypes.c_longlong, ctypes.POINTER(LinearParams)
+        L.srnl_layer_norm_fwd.argtypes = [vp, ll, i, i, vp, vp, ctypes.c_float, i, vp, vp, vp, vp]
+        L.srnl_layer_norm_bwd.argtypes = [vp, i, vp, ll, i, i, vp, vp, vp, vp, i, vp, vp, vp, vp,
+                                          sz, vp]
+        L.srnl_layer_norm_bwd_workspace_bytes.argtypes = [ll, i]
+        L.srnl_layer_norm_bwd_workspace_bytes.restype = sz
+        L.srnl_linear_fwd.argtypes = [vp, ll, i, i, lp, vp, vp]
+        L.srnl_linear_bwd.argtypes = [vp, vp, ll, i, i, lp, vp, vp, vp, vp, vp, vp, sz]
+        L.srnl_linear_bwd_workspace_bytes.argtypes = [ll, i, i, lp]
+        L.srnl_linear_bwd_workspace_bytes.restype = sz
+        L.srnl_dwconv_fwd.argtypes = [vp, i, i, i, i, i, vp, vp, vp, i, vp, i, i, vp, vp]
+        L.srnl_dwconv_bwd.argtypes = [vp, i, vp, i, i, i, i, i, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.srnl_dwconv_bwd_workspace_bytes.argtypes = [i, i, i, i]
+        L.srnl_dwconv_bwd_workspace_bytes.restype = sz
+        for f in ("srnl_layer_norm_fwd", "srnl_layer_norm_bwd", "srnl_linear_fwd",
+                  "srnl_linear_bwd", "srnl_dwconv_fwd", "srnl_dwconv_bwd"):
+            getattr(L, f).restype = ctypes.c_int
         for f in ("srnl_scan_fwd", "srnl_scan_1d", "srnl_fuse", "srnl_scan_bwd",
                   "srnl_scan_1d_bwd", "srnl_fuse_bwd", "srnl_fuse_bwd_noalloc",
                   "srnl_scan_fuse_bwd", "srnl_route_gather", "srnl_init_states", "srnl_block_fwd"):
@@ -592,3 +623,371 @@ def block_fwd(x: torch.Tensor, states: torch.Tensor, weights: BlockWeights, head
     if own:
         _keep_for_stream(p.stream, workspace)
     return out
+
+
+# ------------------------------------------------------------ layers
+
+def _on(x: torch.Tensor, *others: Optional[torch.Tensor]):
+    """The context in which x's device is current (the library launches on the
+    current device); every tensor must be on it."""
+    if not x.is_cuda:
+        raise ValueError("tensors must be on the GPU (there is no CPU path)")
+    for t in others:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"tensors on {x.device} and {t.device}")
+    if x.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(x.device)
+
+
+def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _new(out: Optional[torch.Tensor], shape, dtype, device, name: str = "out") -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _expect(out, shape, dtype, name)
+    if out.device != device:
+        raise ValueError(f"{name} is on {out.device}, expected {device}")
+    return out
+
+
+def layer_norm_fwd(x: torch.Tensor, gain: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+                   eps: float = 1e-5, *, out_dtype=None, stats: bool = False,
+                   out: Optional[torch.Tensor] = None, stream=None):
+    """srnl_layer_norm_fwd over the last axis of x [..., C] -> y in out_dtype
+    (x's when None); with stats also (mean, rstd) [...] fp32, which
+    layer_norm_bwd takes. gain, bias: [C] fp32 or None."""
+    C = x.shape[-1]
+    for t, name in ((gain, "gain"), (bias, "bias")):
+        _expect(t, (C,), torch.float32, name)
+    dtx = _dtype_code(x)
+    with _on(x, gain, bias):
+        out = _new(out, x.shape, x.dtype if out_dtype is None else out_dtype, x.device)
+        dto = _dtype_code(out)
+        mean = rstd = None
+        if stats:
+            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
+        _check(lib().srnl_layer_norm_fwd(_ptr(x), x.numel() // C, C, dtx, _ptr(gain), _ptr(bias),
+                                         eps, dto, _ptr(out), _ptr(mean), _ptr(rstd),
+                                         _stream(stream)), "srnl_layer_norm_fwd")
+    return (out, mean, rstd) if stats else out
+
+
+def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gain: Optional[torch.Tensor],
+                   mean: torch.Tensor, rstd: torch.Tensor, *,
+                   dx_add: Optional[torch.Tensor] = None, param_grads: bool = True,
+                   dx: Optional[torch.Tensor] = None, stream=None):
+    """srnl_layer_norm_bwd: dout [..., C] -> (dx in x's dtype, dgain, dbias
+    [C] fp32; the last two None without param_grads). dx_add: a gradient of
+    x's shape, fp32 or bf16, added to dx (the residual around the norm)."""
+    C = x.shape[-1]
+    _expect(gain, (C,), torch.float32, "gain")
+    _expect(dout, x.shape, None, "dout")
+    _expect(dx_add, x.shape, None, "dx_add")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _expect(t, x.shape[:-1], torch.float32, name)
+    rows = x.numel() // C
+    dtx, dto = _dtype_code(x), _dtype_code(dout)
+    dta = 0 if dx_add is None else _dtype_code(dx_add)
+    with _on(x, dout, gain, mean, rstd, dx_add):
+        dx = _new(dx, x.shape, x.dtype, x.device, "dx")
+        dgain = dbias = ws = None
+        if param_grads:
+            dgain = torch.empty(C, dtype=torch.float32, device=x.device)
+            dbias = torch.empty_like(dgain)
+            ws = _workspace(lib().srnl_layer_norm_bwd_workspace_bytes(rows, C), x.device)
+        sh = _stream(stream)
+        _check(lib().srnl_layer_norm_bwd(
+            _ptr(dout), dto, _ptr(x), rows, C, dtx, _ptr(gain), _ptr(mean), _ptr(rstd),
+            _ptr(dx_add), dta, _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(ws),
+            0 if ws is None else ws.numel(), sh), "srnl_layer_norm_bwd")
+        _keep_for_stream(sh, ws)
+    return dx, dgain, dbias
+
+
+def _act_code(act) -> int:
+    if act in ACTS:
+        return ACTS[act]
+    if isinstance(act, int) and act in ACTS.values():
+        return act
+    raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+
+
+def linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+               act="none", residual: Optional[torch.Tensor] = None, out_dtype=None,
+               keep_pre: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """srnl_linear_fwd: act(x w^T + bias) + residual, x [..., K], w [N, K],
+    bias [N] fp32, residual [..., N], each of x, w, residual and the output
+    (out_dtype, x's when None) fp32 or bf16. act: "none", "gelu" (erf) or
+    "silu". keep_pre: also return x w^T + bias in fp32, which linear_bwd
+    takes."""
+    N, K = w.shape
+    if x.shape[-1] != K:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., {K}]")
+    shape = x.shape[:-1] + (N,)
+    _expect(bias, (N,), torch.float32, "bias")
+    _expect(residual, shape, None, "residual")
+    code = _act_code(act)
+    dtr = 0 if residual is None else _dtype_code(residual)
+    with _on(x, w, bias, residual):
+        out = _new(out, shape, x.dtype if out_dtype is None else out_dtype, x.device)
+        pre = torch.empty(shape, dtype=torch.float32, device=x.device) if keep_pre else None
+        p = LinearParams(_ptr(w), _ptr(bias), _ptr(residual), _dtype_code(x), _dtype_code(w), dtr,
+                         _dtype_code(out), code, _stream(stream))
+        _check(lib().srnl_linear_fwd(_ptr(x), x.numel() // K, K, N, ctypes.byref(p), _ptr(out),
+                                     _ptr(pre)), "srnl_linear_fwd")
+    return (out, pre) if keep_pre else out
+
+
+def linear_bwd(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+               pre: Optional[torch.Tensor] = None, *, act="none",
+               dx_add: Optional[torch.Tensor] = None, need_dx: bool = True, need_dw: bool = True,
+               need_db: bool = True, stream=None):
+    """srnl_linear_bwd: dout [..., N] -> (dx [..., K] in x's dtype, dw [N, K]
+    fp32, db [N] fp32), None where not needed (db comes with dw). pre: from
+    linear_fwd(keep_pre=True), for an activation. dx_add: a gradient of x's
+    shape and dtype, added to dx."""
+    N, K = w.shape
+    if x.shape[-1] != K:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [..., {K}]")
+    shape = x.shape[:-1] + (N,)
+    code = _act_code(act)
+    _expect(dout, shape, None, "dout")
+    _expect(dx_add, x.shape, x.dtype, "dx_add")
+    if code == ACT_NONE:
+        pre = None
+    elif pre is None:
+        raise ValueError("an activation's backward needs pre (linear_fwd with keep_pre=True)")
+    _expect(pre, shape, torch.float32, "pre")
+    if need_db and not need_dw:
+        raise ValueError("need_db needs need_dw: the bias gradient is formed with the weight's")
+    M = x.numel() // K
+    with _on(x, dout, w, pre, dx_add):
+        sh = _stream(stream)
+        p = LinearParams(_ptr(w), None, None, _dtype_code(x), _dtype_code(w), 0,
+                         _dtype_code(dout), code, sh)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+        dw = torch.empty((N, K), dtype=torch.float32, device=x.device) if need_dw else None
+        db = torch.empty(N, dtype=torch.float32, device=x.device) if need_db else None
+        ws = _workspace(lib().srnl_linear_bwd_workspace_bytes(M, K, N, ctypes.byref(p)), x.device)
+        _check(lib().srnl_linear_bwd(_ptr(dout), _ptr(x), M, K, N, ctypes.byref(p), _ptr(pre),
+                                     _ptr(dx_add), _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws),
+                                     0 if ws is None else ws.numel()), "srnl_linear_bwd")
+        _keep_for_stream(sh, ws)
+    return dx, dw, db
+
+
+def dwconv_fwd(u: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               add1: Optional[torch.Tensor] = None, add2: Optional[torch.Tensor] = None, *,
+               out_dtype=None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """srnl_dwconv_fwd: the depthwise 3x3 convolution of u [B,H,W,C] (zero
+    padding) with w [C,3,3], bias [C] fp32, plus the addends of u's shape, in
+    out_dtype (u's when None)."""
+    B, H, W, C = u.shape
+    _expect(w, (C, 3, 3), torch.float32, "w")
+    _expect(bias, (C,), torch.float32, "bias")
+    for t, name in ((add1, "add1"), (add2, "add2")):
+        _expect(t, u.shape, None, name)
+    codes = [0 if t is None else _dtype_code(t) for t in (add1, add2)]
+    with _on(u, w, bias, add1, add2):
+        out = _new(out, u.shape, u.dtype if out_dtype is None else out_dtype, u.device)
+        _check(lib().srnl_dwconv_fwd(_ptr(u), B, H, W, C, _dtype_code(u), _ptr(w), _ptr(bias),
+                                     _ptr(add1), codes[0], _ptr(add2), codes[1], _dtype_code(out),
+                                     _ptr(out), _stream(stream)), "srnl_dwconv_fwd")
+    return out
+
+
+def dwconv_bwd(dout: torch.Tensor, u: torch.Tensor, w: torch.Tensor, *,
+               du_add: Optional[torch.Tensor] = None, need_du: bool = True,
+               param_grads: bool = True, stream=None):
+    """srnl_dwconv_bwd: dout [B,H,W,C] -> (du in u's dtype, dw [C,3,3], db [C]
+    fp32), None where not needed. du_add: another gradient of u, of its shape
+    and dtype, added to du."""
+    B, H, W, C = u.shape
+    _expect(w, (C, 3, 3), torch.float32, "w")
+    _expect(dout, u.shape, None, "dout")
+    _expect(du_add, u.shape, u.dtype, "du_add")
+    with _on(u, dout, w, du_add):
+        du = torch.empty(u.shape, dtype=u.dtype, device=u.device) if need_du else None
+        dw = db = ws = None
+        if param_grads:
+            dw = torch.empty((C, 3, 3), dtype=torch.float32, device=u.device)
+            db = torch.empty(C, dtype=torch.float32, device=u.device)
+            ws = _workspace(lib().srnl_dwconv_bwd_workspace_bytes(B, H, W, C), u.device)
+        sh = _stream(stream)
+        _check(lib().srnl_dwconv_bwd(_ptr(dout), _dtype_code(dout), _ptr(u), B, H, W, C,
+                                     _dtype_code(u), _ptr(w), _ptr(du_add), _ptr(du), _ptr(dw),
+                                     _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), sh),
+               "srnl_dwconv_bwd")
+        _keep_for_stream(sh, ws)
+    return du, dw, db
+
+
+# ---- the layers as autograd nodes (on the current stream)
+
+def _wants_grad(*tensors: Optional[torch.Tensor]) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class LayerNorm(torch.autograd.Function):
+    """srnl_layer_norm_fwd and srnl_layer_norm_bwd as an autograd node."""
+
+    @staticmethod
+    def forward(ctx, x, gain, bias, eps, out_dtype):
+        out, mean, rstd = layer_norm_fwd(x, gain, bias, eps, out_dtype=out_dtype, stats=True)
+        ctx.save_for_backward(x, gain, mean, rstd)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, gain, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dgain, dbias = layer_norm_bwd(dout.contiguous(), x, gain, mean, rstd,
+                                          param_grads=need[1] or need[2])
+        return dx, dgain if need[1] else None, dbias if need[2] else None, None, None
+
+
+def layer_norm(x: torch.Tensor, gain: Optional[torch.Tensor], bias: Optional[torch.Tensor],
+               eps: float = 1e-5, out_dtype=None) -> torch.Tensor:
+    """Differentiable layer norm over the last axis (layer_norm_fwd)."""
+    if not _wants_grad(x, gain, bias):
+        return layer_norm_fwd(x, gain, bias, eps, out_dtype=out_dtype)
+    return LayerNorm.apply(x, gain, bias, eps, out_dtype)
+
+
+class Linear(torch.autograd.Function):
+    """srnl_linear_fwd and srnl_linear_bwd as an autograd node. The gradient
+    of w comes back in w's dtype (rounded once from fp32)."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act, out_dtype):
+        keep = _act_code(act) != ACT_NONE
+        out = linear_fwd(x, w, bias, act=act, residual=residual, out_dtype=out_dtype,
+                         keep_pre=keep)
+        out, pre = out if keep else (out, None)
+        ctx.save_for_backward(x, w, pre)
+        ctx.cfg = (act, None if residual is None else residual.dtype)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, w, pre = ctx.saved_tensors
+        act, res_dtype = ctx.cfg
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            dx, dw, db = linear_bwd(dout.contiguous(), x, w, pre, act=act, need_dx=need[0],
+                                    need_dw=need[1] or need[2], need_db=need[2])
+        dw = dw.to(w.dtype) if need[1] else None
+        dres = dout.to(res_dtype) if need[3] else None
+        return dx, dw, db, dres, None, None
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act="none",
+           residual: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
+    """Differentiable act(x w^T + bias) + residual (linear_fwd)."""
+    if not _wants_grad(x, w, bias, residual):
+        return linear_fwd(x, w, bias, act=act, residual=residual, out_dtype=out_dtype)
+    return Linear.apply(x, w, bias, residual, act, out_dtype)
+
+
+class DWConv(torch.autograd.Function):
+    """srnl_dwconv_fwd and srnl_dwconv_bwd as an autograd node."""
+
+    @staticmethod
+    def forward(ctx, u, w, bias, add1, add2, out_dtype):
+        ctx.save_for_backward(u, w)
+        ctx.add_dtypes = [None if t is None else t.dtype for t in (add1, add2)]
+        return dwconv_fwd(u, w, bias, add1, add2, out_dtype=out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        u, w = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        du = dw = db = None
+        if any(need[:3]):
+            du, dw, db = dwconv_bwd(dout.contiguous(), u, w, need_du=need[0],
+                                    param_grads=need[1] or need[2])
+        adds = [dout.to(t) if n else None for n, t in zip(need[3:5], ctx.add_dtypes)]
+        return (du, dw if need[1] else None, db if need[2] else None, *adds, None)
+
+
+def dwconv(u: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
+           add1: Optional[torch.Tensor] = None, add2: Optional[torch.Tensor] = None, *,
+           out_dtype=None) -> torch.Tensor:
+    """Differentiable depthwise 3x3 branch with its addends (dwconv_fwd)."""
+    if not _wants_grad(u, w, bias, add1, add2):
+        return dwconv_fwd(u, w, bias, add1, add2, out_dtype=out_dtype)
+    return DWConv.apply(u, w, bias, add1, add2, out_dtype)
+
+
+BLOCK_KEYS = ("ln1_w", "ln1_b", "wq", "dw_w", "dw_b", "ln2_w", "ln2_b", "w1", "b1", "w2", "b2")
+
+
+class Block(torch.autograd.Function):
+    """The residual block of srnl_block_fwd in its training form: the layers'
+    and the operator's entry points in turn, every activation kept in fp32,
+    the gradients of shared inputs added inside the backward calls."""
+
+    @staticmethod
+    def forward(ctx, x, states, scales, heads, d, route_mask, ln_eps, kw, *weights):
+        ln1_w, ln1_b, wq, dw_w, dw_b, ln2_w, ln2_b, w1, b1, w2, b2 = weights
+        B, H, W, C = x.shape
+        f32 = torch.float32
+        u, m1, r1 = layer_norm_fwd(x, ln1_w, ln1_b, ln_eps, out_dtype=f32, stats=True)
+        q = linear_fwd(u, wq)
+        y, rec = scan_fwd_record(u, states, heads, d, route_mask, q, **kw)
+        s = fuse(y, B, H, W, C, route_mask, scales)
+        h = dwconv_fwd(u, dw_w, dw_b, x, s, out_dtype=f32)
+        v, m2, r2 = layer_norm_fwd(h, ln2_w, ln2_b, ln_eps, stats=True)
+        a, z = linear_fwd(v, w1, b1, act=ACT_GELU, keep_pre=True)
+        out = linear_fwd(a, w2, b2, residual=h, out_dtype=x.dtype)
+        ctx.save_for_backward(x, states, scales, u, m1, r1, q, y, rec, h, m2, r2, v, a, z, *weights)
+        ctx.cfg = (heads, d, route_mask, kw)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, states, scales, u, m1, r1, q, y, rec, h, m2, r2, v, a, z, *weights = ctx.saved_tensors
+        ln1_w, ln1_b, wq, dw_w, dw_b, ln2_w, ln2_b, w1, b1, w2, b2 = weights
+        heads, d, route_mask, kw = ctx.cfg
+        dout = dout.contiguous()
+        da, gw2, gb2 = linear_bwd(dout, a, w2)
+        dv, gw1, gb1 = linear_bwd(da, v, w1, z, act=ACT_GELU)
+        dh, gl2w, gl2b = layer_norm_bwd(dv, h, ln2_w, m2, r2, dx_add=dout)
+        du, dq, dst, dsc = scan_fuse_bwd(u, states, heads, d, y, scales, dh, route_mask, q,
+                                         record=rec, **kw)
+        du, gdw, gdb = dwconv_bwd(dh, u, dw_w, du_add=du)
+        du, gwq, _ = linear_bwd(dq, u, wq, dx_add=du, need_db=False)
+        dx, gl1w, gl1b = layer_norm_bwd(du, x, ln1_w, m1, r1, dx_add=dh)
+        grads = (gl1w, gl1b, gwq, gdw, gdb, gl2w, gl2b, gw1, gb1, gw2, gb2)
+        return (dx, dst, dsc, None, None, None, None, None,
+                *(g.to(t.dtype) for g, t in zip(grads, weights)))
+
+
+def block(x: torch.Tensor, states: torch.Tensor, scales: torch.Tensor, bw: dict, heads: int,
+          d: int, route_mask: int = 15, ln_eps: float = 1e-5, **kw) -> torch.Tensor:
+    """Differentiable residual block, x [B,H,W,C] -> [B,H,W,C] in x's dtype:
+    the block of block_fwd (any width C = heads * d, any ffn width), with
+    gradients for x, the initial states, the scales and every weight. bw: the
+    tensors of block_weights (wq, w1, w2 bf16 or fp32, the others fp32). ``kw``
+    are the srnl_params fields (alpha_max, eps, chunk_row, chunk_col, flags).
+    Runs on the current stream."""
+    if "stream" in kw or "q" in kw:
+        raise ValueError("block runs on the current stream and forms its own queries")
+    C, F = x.shape[-1], bw["w1"].shape[0]
+    shapes = {"ln1_w": (C,), "ln1_b": (C,), "wq": (C, C), "dw_w": (C, 3, 3), "dw_b": (C,),
+              "ln2_w": (C,), "ln2_b": (C,), "w1": (F, C), "b1": (F,), "w2": (C, F), "b2": (C,)}
+    for k, shp in shapes.items():
+        _expect(bw[k], shp, None if k in ("wq", "w1", "w2") else torch.float32, k)
+    _expect(scales, (4, C), torch.float32, "scales")
+    _expect(states, _state_shape(heads, d), torch.float32, "states")
+    return Block.apply(x, states, scales, heads, d, route_mask, ln_eps, kw,
+                       *(bw[k] for k in BLOCK_KEYS))
