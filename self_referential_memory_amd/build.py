@@ -10,7 +10,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "srnl.hip")
 # translation units, compiled side by side and linked into the one library
-UNITS = [SRC] + [os.path.join(PKG, "csrc", f) for f in ("srnl_linear.hip", "srnl_layers.hip")]
+UNITS = [os.path.join(PKG, "csrc", "layers", f)
+         for f in ("operator_unit.hip", "linear.hip", "layers.hip")]
 LIB = os.path.join(PKG, "libsrnl.so")
 # the same source with the scan kernel's phase clocks compiled in (a
 # measurement build, loaded only by bench.py --phase-clocks)

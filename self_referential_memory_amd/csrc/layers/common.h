@@ -1,15 +1,16 @@
-// srnl_internal.h -- what the layers' translation units share: argument
+// common.h -- what the layers' translation units share: argument
 // checks, and device helpers for fp32 and bf16 rows of any alignment.
-#ifndef SRNL_INTERNAL_H
-#define SRNL_INTERNAL_H
+#ifndef SRNL_LAYERS_COMMON_H
+#define SRNL_LAYERS_COMMON_H
 
 #include <hip/hip_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
-#include "srnl_error.h"
+#include "error.h"
 
 namespace srnl_i {
 

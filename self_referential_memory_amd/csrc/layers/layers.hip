@@ -1,14 +1,14 @@
-// srnl_layers.hip -- the layers around the operator with their backward
+// layers.hip -- the layers around the operator with their backward
 // passes: layer norm and the depthwise 3x3 branch (the linear layer is in
-// srnl_linear.hip). Entry points as declared in include/srnl.h.
-#include "srnl_internal.h"
+// linear.hip). Entry points as declared in include/srnl.h.
+#include "common.h"
 
 namespace {
 
 using namespace srnl_i;
 
-#include "srnl_norm.inc"
-#include "srnl_dwconv.inc"
+#include "norm.inc"
+#include "dwconv.inc"
 
 // rows x C elements of at most 4 bytes within the address range
 bool norm_sizes_ok(long long rows, int C)
@@ -178,7 +178,7 @@ size_t srnl_dwconv_bwd_workspace_bytes(int B, int H, int W, int C)
 {
     if (check_dwconv(B, H, W, C) != SRNL_OK || B == 0 || H == 0 || W == 0)
         return 0;
-    const DwShape d = dw_shape(B, H, W, C, true);
+    const DwShape d = dw_shape(B, H, W, C);
     return static_cast<size_t>(d.gy) * d.jgroups * 10 * C * sizeof(float);
 }
 
@@ -230,7 +230,7 @@ srnl_status srnl_dwconv_bwd(const void *dout, srnl_dtype out_dtype, const void *
     s = launch_dwconv(a, true, st);
     if (s != SRNL_OK || !params)
         return s;
-    const DwShape d = dw_shape(B, H, W, C, true);
+    const DwShape d = dw_shape(B, H, W, C);
     return sum_rows(a.part, d.gy * d.jgroups, 10LL * C, 10LL * C, 9LL * C, dw, db, st);
 }
 

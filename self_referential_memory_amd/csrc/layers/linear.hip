@@ -1,4 +1,4 @@
-// srnl_linear.hip -- the linear layer with bias, activation and residual in
+// linear.hip -- the linear layer with bias, activation and residual in
 // its epilogue, forward and backward. Entry points as declared in
 // include/srnl.h.
 //
@@ -18,7 +18,7 @@
 //
 // A few rows (or few output tiles) go to linear_few_kernel, which splits the
 // reduction over the waves of a block and joins them in LDS.
-#include "srnl_internal.h"
+#include "common.h"
 
 namespace {
 

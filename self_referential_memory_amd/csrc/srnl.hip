@@ -47,7 +47,6 @@
 #include <type_traits>
 
 #include "srnl.h"
-#include "srnl_error.h"
 
 namespace {
 
@@ -2710,15 +2709,6 @@ srnl_params params_1d(const srnl_params *p)
 }
 
 }  // namespace
-
-srnl_status srnl_set_error(srnl_status s, const char *msg) noexcept
-{
-    try {
-        g_last_error = msg;
-    } catch (...) {      // no memory for the text: the status still stands
-    }
-    return s;
-}
 
 // ------------------------------------------------------------ C ABI
 

@@ -171,7 +171,7 @@ def _expect(t: Optional[torch.Tensor], shape, dtype, name: str) -> None:
     """The library sees only pointers: buffer shapes and dtypes are checked here."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != (shape if isinstance(shape, tuple) else tuple(shape)):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -183,7 +183,7 @@ def _state_shape(heads: int, d: int):
 
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -192,8 +192,7 @@ def _keep_for_stream(handle, *tensors) -> None:
     on return, but whose kernels run on the stream ``handle``: record that
     stream on them, so the caching allocator does not hand their memory out
     again before that stream's work is done."""
-    cur = torch.cuda.current_stream()
-    if (handle or 0) == (cur.cuda_stream or 0):
+    if (handle or 0) == (_stream(None) or 0):
         return
     s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
     for t in tensors:
@@ -201,12 +200,14 @@ def _keep_for_stream(handle, *tensors) -> None:
             t.record_stream(s)
 
 
+_DTYPE_CODES = {torch.float32: SRNL_F32, torch.bfloat16: SRNL_BF16}
+
+
 def _dtype_code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return SRNL_F32
-    if t.dtype == torch.bfloat16:
-        return SRNL_BF16
-    raise ValueError(f"unsupported dtype {t.dtype}")
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def route_index(r: int, H: int, W: int, t: int):
@@ -627,17 +628,19 @@ def block_fwd(x: torch.Tensor, states: torch.Tensor, weights: BlockWeights, head
 
 # ------------------------------------------------------------ layers
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(x: torch.Tensor, *others: Optional[torch.Tensor]):
     """The context in which x's device is current (the library launches on the
     current device); every tensor must be on it."""
-    if not x.is_cuda:
+    i = x.get_device()
+    if i < 0:
         raise ValueError("tensors must be on the GPU (there is no CPU path)")
     for t in others:
-        if t is not None and t.device != x.device:
+        if t is not None and t.get_device() != i:
             raise ValueError(f"tensors on {x.device} and {t.device}")
-    if x.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(x.device)
+    return _HERE if i == torch.cuda.current_device() else torch.cuda.device(i)
 
 
 def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
