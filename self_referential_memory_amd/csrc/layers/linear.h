@@ -1,0 +1,181 @@
+// linear.h -- what the linear layer's translation units share: activations,
+// the split of fp32 values into bf16 parts, operands, the epilogue.
+#ifndef SRNL_LAYERS_LINEAR_H
+#define SRNL_LAYERS_LINEAR_H
+
+#include "common.h"
+
+namespace srnl_i {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// ------------------------------------------------------------ activations
+
+// 1 - Phi(|z|) of the standard normal, from formula 7.1.26 of Abramowitz and
+// Stegun (Handbook of Mathematical Functions), |error| <= 0.75e-7:
+// erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-x^2),
+// t = 1 / (1 + p x), x = |z| / sqrt 2. ex returns exp(-z^2 / 2).
+__device__ __forceinline__ float normal_tail(float z, float &ex)
+{
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
+    float p = fmaf(t, 1.061405429f, -1.453152027f);
+    p = fmaf(t, p, 1.421413741f);
+    p = fmaf(t, p, -0.284496736f);
+    p = fmaf(t, p, 0.254829592f);
+    ex = __expf(-0.5f * z * z);
+    return 0.5f * t * p * ex;
+}
+// Phi(z) in [0, 1] as 1/2 + c P(c^2), c = z held to +-5.3, where Phi is 6e-8
+// from its limit: P is the degree-13 polynomial of least largest error in Phi,
+// found by weighted least squares on a Chebyshev basis and written in
+// t = 2 c^2 / 5.3^2 - 1 (coefficients below 0.14 on |t| <= 1, so Horner's rule
+// loses nothing). |error| <= 1.9e-7 in fp32; 0 and 1 are exact past 5.3. 17
+// plain operations, against 26 issue slots for erf through exp and a
+// reciprocal, which in an epilogue of a short reduction set the time.
+__device__ __forceinline__ float normal_cdf(float z)
+{
+    const float c = __builtin_amdgcn_fmed3f(z, -5.3f, 5.3f);
+    const float t = fmaf(c * 0.071199715f, c, -1.0f);
+    float p = fmaf(t, -0.000618251623f, 0.00166963739f);
+    p = fmaf(t, p, -0.00153595686f);
+    p = fmaf(t, p, 0.00192110776f);
+    p = fmaf(t, p, -0.00534413708f);
+    p = fmaf(t, p, 0.0096047828f);
+    p = fmaf(t, p, -0.0134618329f);
+    p = fmaf(t, p, 0.0186717361f);
+    p = fmaf(t, p, -0.0252255779f);
+    p = fmaf(t, p, 0.0321189426f);
+    p = fmaf(t, p, -0.0395970307f);
+    p = fmaf(t, p, 0.0492618792f);
+    p = fmaf(t, p, -0.0665182546f);
+    p = fmaf(t, p, 0.133392587f);
+    return __builtin_amdgcn_fmed3f(fmaf(c, p, 0.5f), 0.0f, 1.0f);
+}
+__device__ __forceinline__ float gelu(float z) { return z * normal_cdf(z); }
+__device__ __forceinline__ float gelu_slope(float z)
+{
+    float ex;
+    const float q = normal_tail(z, ex);
+    return fmaf(z * 0.39894228040143268f, ex, z >= 0.0f ? 1.0f - q : q);
+}
+__device__ __forceinline__ float logistic(float z)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+}
+__device__ __forceinline__ void act_values(float (&v)[8], int act)
+{
+    if (act == SRNL_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = gelu(v[e]);
+    } else if (act == SRNL_ACT_SILU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] *= logistic(v[e]);
+    }
+}
+// d *= act'(z)
+__device__ __forceinline__ void act_slopes(const float (&z)[8], int act, float (&d)[8])
+{
+    if (act == SRNL_ACT_GELU) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            d[e] *= gelu_slope(z[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = logistic(z[e]);
+            d[e] *= s * fmaf(z[e], 1.0f - s, 1.0f);
+        }
+    }
+}
+
+// ------------------------------------------------------------ operands
+
+// 8 fp32 values to PARTS planes of bf16 words
+__device__ __forceinline__ void split_parts(const float (&v)[8], u32x4 (&w)[3])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float a = v[2 * k], b = v[2 * k + 1];
+        const uint32_t h = pack_bf16(a, b);
+        const float ra = a - bf16_lo(h), rb = b - bf16_hi(h);
+        const uint32_t m = pack_bf16(ra, rb);
+        w[0][k] = h;
+        w[1][k] = m;
+        w[2][k] = pack_bf16(ra - bf16_lo(m), rb - bf16_hi(m));
+    }
+}
+
+// One operand as memory: element (row, r) is at row * ld + r (reduction
+// contiguous, RC) or r * ld + row.
+struct Operand {
+    const void *p;
+    long long ld;
+    long long rows;       // output rows (or columns) of this operand
+    const float *z;       // SLOPE: pre-activations laid out like p
+    int act;
+};
+
+// What an operand is made of: bf16 words, fp32 values, or dy act'(z) formed
+// while it is staged, with dy in bf16 or fp32.
+enum Source { BF16, FP32, SLOPE_BF16, SLOPE_FP32 };
+
+// ------------------------------------------------------------ epilogue
+
+struct Epilogue {
+    void *out;             // [I][J]
+    bool obf;
+    const float *bias;     // [J] or NULL
+    int act;
+    const void *add;       // [I][J] or NULL: added after the activation
+    bool abf;
+    float *pre;            // [I][J] or NULL: z before the activation
+};
+
+// eight neighbouring outputs (i, j .. j + 7) from their sums; n are inside
+template <bool ALIGNED>
+__device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, int n, float (&v)[8])
+{
+    if (n <= 0)
+        return;
+    if (e.bias) {
+        float b[8];
+        load_row<8, ALIGNED>(e.bias, false, j, n, b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] += b[k];
+    }
+    if (e.pre)
+        store_row<8, ALIGNED>(e.pre, false, o, n, v);
+    act_values(v, e.act);
+    if (e.add) {
+        float a[8];
+        load_row<8, ALIGNED>(e.add, e.abf, o, n, a);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] += a[k];
+    }
+    store_row<8, ALIGNED>(e.out, e.obf, o, n, v);
+}
+
+// ------------------------------------------------------------ narrow layers
+
+constexpr long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+
+// Both gradients of a layer whose weights fit in LDS beside a slice of rows
+// (narrow.hip). narrow_bwd_parts: how many partial weight and bias gradients
+// narrow_bwd leaves for the caller to join, 0 where it does not take the layer.
+#define SRNL_HIDDEN __attribute__((visibility("hidden")))
+SRNL_HIDDEN int narrow_bwd_parts(long long M, int K, int N, Source sz, Source sw, Source sx);
+SRNL_HIDDEN srnl_status narrow_bwd(const Operand &dz, const Operand &w, const Operand &x, int K, int N, Source sz,
+                                   Source sw, Source sx, const Epilogue &dx, float *dw_parts, float *db_parts,
+                                   int parts, hipStream_t st);
+
+}  // namespace srnl_i
+
+#endif

@@ -18,77 +18,11 @@
 //
 // A few rows (or few output tiles) go to linear_few_kernel, which splits the
 // reduction over the waves of a block and joins them in LDS.
-#include "common.h"
+#include "linear.h"
 
 namespace {
 
 using namespace srnl_i;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
-// ------------------------------------------------------------ activations
-
-// 1 - Phi(|z|) of the standard normal, from formula 7.1.26 of Abramowitz and
-// Stegun (Handbook of Mathematical Functions), |error| <= 0.75e-7:
-// erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-x^2),
-// t = 1 / (1 + p x), x = |z| / sqrt 2. ex returns exp(-z^2 / 2).
-__device__ __forceinline__ float normal_tail(float z, float &ex)
-{
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f, x, 1.0f));
-    float p = fmaf(t, 1.061405429f, -1.453152027f);
-    p = fmaf(t, p, 1.421413741f);
-    p = fmaf(t, p, -0.284496736f);
-    p = fmaf(t, p, 0.254829592f);
-    ex = __expf(-0.5f * z * z);
-    return 0.5f * t * p * ex;
-}
-__device__ __forceinline__ float gelu(float z)
-{
-    float ex;
-    const float q = normal_tail(z, ex);
-    return z * (z >= 0.0f ? 1.0f - q : q);
-}
-__device__ __forceinline__ float gelu_slope(float z)
-{
-    float ex;
-    const float q = normal_tail(z, ex);
-    return fmaf(z * 0.39894228040143268f, ex, z >= 0.0f ? 1.0f - q : q);
-}
-__device__ __forceinline__ float logistic(float z)
-{
-    return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
-}
-__device__ __forceinline__ void act_values(float (&v)[8], int act)
-{
-    if (act == SRNL_ACT_GELU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = gelu(v[e]);
-    } else if (act == SRNL_ACT_SILU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] *= logistic(v[e]);
-    }
-}
-// d *= act'(z)
-__device__ __forceinline__ void act_slopes(const float (&z)[8], int act, float (&d)[8])
-{
-    if (act == SRNL_ACT_GELU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            d[e] *= gelu_slope(z[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float s = logistic(z[e]);
-            d[e] *= s * fmaf(z[e], 1.0f - s, 1.0f);
-        }
-    }
-}
 
 // dz = dy act'(z), the pre-pass of the backward products
 __global__ __launch_bounds__(256) void act_slope_kernel(const void *__restrict__ dy, bool dybf,
@@ -105,33 +39,8 @@ __global__ __launch_bounds__(256) void act_slope_kernel(const void *__restrict__
     }
 }
 
-// ------------------------------------------------------------ operands
-
-// 8 fp32 values to PARTS planes of bf16 words
-__device__ __forceinline__ void split_parts(const float (&v)[8], u32x4 (&w)[3])
-{
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float a = v[2 * k], b = v[2 * k + 1];
-        const uint32_t h = pack_bf16(a, b);
-        const float ra = a - bf16_lo(h), rb = b - bf16_hi(h);
-        const uint32_t m = pack_bf16(ra, rb);
-        w[0][k] = h;
-        w[1][k] = m;
-        w[2][k] = pack_bf16(ra - bf16_lo(m), rb - bf16_hi(m));
-    }
-}
-
 // 16 bytes that lanes read in place of pieces outside an operand
 __device__ __align__(16) const uint32_t zero_piece[4] = {0, 0, 0, 0};
-
-// One operand as memory: element (row, r) is at row * ld + r (reduction
-// contiguous, RC) or r * ld + row.
-struct Operand {
-    const void *p;
-    long long ld;
-    long long rows;       // output rows (or columns) of this operand
-};
 
 // A tile of ROWS x BK of an operand, staged in LDS as PARTS planes of bf16.
 // RC: plane[row][BK], 16-byte pieces of a row permuted so that 16 consecutive
@@ -139,7 +48,9 @@ struct Operand {
 // in memory, the 64-byte blocks of a row permuted by r, read through the
 // transposing LDS read (ds_read_b64_tr_b16: of the 4 x 16 block that 16
 // lanes address, each lane gets a column).
-template <bool F32, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
+template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
+    static constexpr bool F32 = SRC != BF16, SLOPE = SRC == SLOPE_BF16 || SRC == SLOPE_FP32;
+    static constexpr bool VALUES = SRC == FP32 || SRC == SLOPE_FP32;
     static constexpr int PARTS = F32 ? 3 : 1;
     static constexpr bool ASYNC = ALIGNED && !F32;        // straight from memory into LDS
     static constexpr int PLANE = ROWS * BK;               // words
@@ -147,8 +58,9 @@ template <bool F32, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
     static_assert(PIECES >= 1 && PIECES * 256 * 8 == PLANE, "pieces divide evenly");
     static constexpr int PER = RC ? BK / 8 : ROWS / 8;    // pieces per stored row
 
-    float v[F32 ? PIECES : 1][8];
-    u32x4 raw[F32 ? 1 : PIECES];
+    float v[VALUES ? PIECES : 1][8];
+    u32x4 raw[VALUES ? 1 : PIECES];
+    float z[SLOPE ? PIECES : 1][8];
 
     static __device__ __forceinline__ int place(int major, int c)
     {
@@ -185,7 +97,9 @@ template <bool F32, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
                 const bool in = RC ? row < o.rows : r < rend;
                 const int n = !in || left <= 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
                 const long long at = RC ? row * o.ld + r : r * o.ld + row;
-                if constexpr (F32) {
+                if constexpr (SLOPE)
+                    load_row<8, ALIGNED>(o.z, false, at, n, z[q]);
+                if constexpr (VALUES) {
                     load_row<8, ALIGNED>(o.p, false, at, n, v[q]);
                 } else {
                     raw[q] = u32x4{0, 0, 0, 0};
@@ -203,7 +117,7 @@ template <bool F32, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
         }
     }
     // write what fetch holds in registers to buf
-    __device__ __forceinline__ void commit(uint16_t *buf) const
+    __device__ __forceinline__ void commit(const Operand &o, uint16_t *buf) const
     {
         if constexpr (!ASYNC) {
 #pragma unroll
@@ -213,7 +127,14 @@ template <bool F32, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
                 uint16_t *dst = buf + 8 * (major * PER + place(major, s % PER));
                 if constexpr (F32) {
                     u32x4 w[3];
-                    split_parts(v[q], w);
+                    float d[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        d[e] = VALUES ? v[VALUES ? q : 0][e]
+                                      : e & 1 ? bf16_hi(raw[VALUES ? 0 : q][e / 2]) : bf16_lo(raw[VALUES ? 0 : q][e / 2]);
+                    if constexpr (SLOPE)
+                        act_slopes(z[q], o.act, d);
+                    split_parts(d, w);
 #pragma unroll
                     for (int p = 0; p < 3; ++p)
                         *reinterpret_cast<u32x4 *>(dst + p * PLANE) = w[p];
@@ -248,50 +169,12 @@ template <bool F32, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
     }
 };
 
-// ------------------------------------------------------------ epilogue
-
-struct Epilogue {
-    void *out;             // [I][J]
-    bool obf;
-    const float *bias;     // [J] or NULL
-    int act;
-    const void *add;       // [I][J] or NULL: added after the activation
-    bool abf;
-    float *pre;            // [I][J] or NULL: z before the activation
-};
-
-// eight neighbouring outputs (i, j .. j + 7) from their sums; n are inside
-template <bool ALIGNED>
-__device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, int n, float (&v)[8])
-{
-    if (n <= 0)
-        return;
-    if (e.bias) {
-        float b[8];
-        load_row<8, ALIGNED>(e.bias, false, j, n, b);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] += b[k];
-    }
-    if (e.pre)
-        store_row<8, ALIGNED>(e.pre, false, o, n, v);
-    act_values(v, e.act);
-    if (e.add) {
-        float a[8];
-        load_row<8, ALIGNED>(e.add, e.abf, o, n, a);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] += a[k];
-    }
-    store_row<8, ALIGNED>(e.out, e.obf, o, n, v);
-}
-
 // ------------------------------------------------------------ tiled product
 
 struct TileArgs {
     Operand a, b;          // out[i][j] = sum over r of a(i, r) b(j, r)
     long long R;           // reduction length
-    long long slice;       // reduction length per split, a multiple of BK
+    long long slice;       // reduction length per split, a multiple of a step's
     int splits;
     int ti, tj;            // output tiles
     float *part;           // [splits][I][J] partial sums instead of the epilogue, or NULL
@@ -320,22 +203,31 @@ template <bool DIRECT> __device__ __forceinline__ void tile_barrier()
 // BI x BJ output tile per block of four waves (2 x 2), BI / 2 x BJ / 2 each,
 // in 32 x 32 MFMA tiles. An operand that goes straight to LDS is fetched one
 // step ahead into the other buffer; one that is converted waits in registers.
-template <bool AF, bool BF, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED, bool SUMS>
-__global__ __launch_bounds__(256) void linear_tile_kernel(TileArgs g)
-{
-    constexpr int BK = (AF || BF) ? 32 : 64;
-    using TA = Tile<AF, RCA, BI, BK, ALIGNED>;
-    using TB = Tile<BF, RCB, BJ, BK, ALIGNED>;
-    constexpr int NBUF = (TA::ASYNC || TB::ASYNC) ? 2 : 1;
-    constexpr int PA = TA::PARTS, PB = TB::PARTS;
-    constexpr int FI = BI / 64, FJ = BJ / 64;                   // 32 x 32 tiles per wave
-    constexpr int WORDS = NBUF * (PA * TA::PLANE + PB * TB::PLANE);
-    constexpr int OUTP = 32 * FJ + 4;                           // floats per staged output row
-    constexpr int OUT_WORDS = 4 * 32 * OUTP * 2;
-    __shared__ __align__(16) uint16_t lds[WORDS > OUT_WORDS ? WORDS : OUT_WORDS];
-    uint16_t *const la = lds, *const lb = lds + NBUF * PA * TA::PLANE;
+// Tiles of 64 are for small products, where a step is mostly the wait for its
+// loads: they take twice the reduction a step.
+template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED> struct TileCfg {
+    static constexpr int BK = (SA != BF16 || SB != BF16 ? 32 : 64) * (BI == 64 ? 2 : 1);
+    using TA = Tile<SA, RCA, BI, BK, ALIGNED>;
+    using TB = Tile<SB, RCB, BJ, BK, ALIGNED>;
+    static constexpr int NA = TA::ASYNC ? 2 : 1, NB = TB::ASYNC ? 2 : 1;    // buffers
+    static constexpr int PA = TA::PARTS, PB = TB::PARTS;
+    static constexpr int OUTP = 32 * (BJ / 64) + 4;             // floats per staged output row
+    static constexpr int WORDS = NA * PA * TA::PLANE + NB * PB * TB::PLANE;
+    static constexpr int OUT_WORDS = 4 * 32 * OUTP * 2;
+    static constexpr int LDS = WORDS > OUT_WORDS ? WORDS : OUT_WORDS;
+};
 
-    const unsigned t = die_order(blockIdx.x, gridDim.x);
+// tile t of g, in lds of TileCfg::LDS words
+template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED, bool SUMS>
+__device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint16_t *lds)
+{
+    using Cfg = TileCfg<SA, SB, RCA, RCB, BI, BJ, ALIGNED>;
+    using TA = typename Cfg::TA;
+    using TB = typename Cfg::TB;
+    constexpr int BK = Cfg::BK, NA = Cfg::NA, NB = Cfg::NB, PA = Cfg::PA, PB = Cfg::PB, OUTP = Cfg::OUTP;
+    constexpr int FI = BI / 64, FJ = BJ / 64;                   // 32 x 32 tiles per wave
+    uint16_t *const la = lds, *const lb = lds + NA * PA * TA::PLANE;
+
     const int tj = t % g.tj, ti = (t / g.tj) % g.ti, sp = t / (g.tj * g.ti);
     const long long i0 = static_cast<long long>(ti) * BI, j0 = static_cast<long long>(tj) * BJ;
     const long long rb = sp * g.slice, re = rb + g.slice < g.R ? rb + g.slice : g.R;
@@ -366,14 +258,14 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(TileArgs g)
 
     ta.fetch(g.a, i0, rb, re, la);
     tb.fetch(g.b, j0, rb, re, lb);
-    ta.commit(la);
-    tb.commit(lb);
+    ta.commit(g.a, la);
+    tb.commit(g.b, lb);
     int cur = 0;
-    tile_barrier<NBUF == 2>();
+    tile_barrier<NA == 2 || NB == 2>();
     for (long long r = rb; r < re; r += BK) {
-        uint16_t *const ca = la + cur * PA * TA::PLANE, *const cb = lb + cur * PB * TB::PLANE;
-        const int nxt = NBUF == 2 ? cur ^ 1 : 0;
-        uint16_t *const na = la + nxt * PA * TA::PLANE, *const nb = lb + nxt * PB * TB::PLANE;
+        const int nxt = cur ^ 1;
+        uint16_t *const ca = la + (NA == 2 ? cur : 0) * PA * TA::PLANE, *const na = la + (NA == 2 ? nxt : 0) * PA * TA::PLANE;
+        uint16_t *const cb = lb + (NB == 2 ? cur : 0) * PB * TB::PLANE, *const nb = lb + (NB == 2 ? nxt : 0) * PB * TB::PLANE;
         const bool more = r + BK < re;
         if (more) {
             ta.fetch(g.a, i0, r + BK, re, na);
@@ -415,14 +307,14 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(TileArgs g)
                         rs[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i][p], ones, rs[i], 0, 0, 0);
             }
         }
-        if (NBUF == 1)
+        if (NA == 1 || NB == 1)
             __syncthreads();                 // everyone has read the only buffer
         if (more) {
-            ta.commit(na);
-            tb.commit(nb);
+            ta.commit(g.a, na);
+            tb.commit(g.b, nb);
         }
         cur = nxt;
-        tile_barrier<NBUF == 2>();
+        tile_barrier<NA == 2 || NB == 2>();
     }
 
     if (SUMS && sums && (lane & 31) == 0) {  // every column of rs holds the sums
@@ -471,30 +363,106 @@ __global__ __launch_bounds__(256) void linear_tile_kernel(TileArgs g)
     }
 }
 
-// out = sum of the splits' partial products through the epilogue, in order
-__global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ part, int splits, long long n,
-                                                   Epilogue e)
+template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED, bool SUMS>
+__global__ __launch_bounds__(256) void linear_tile_kernel(TileArgs g)
 {
-    for (long long o = 8 * (blockIdx.x * 256LL + threadIdx.x); o < n; o += 8 * 256LL * gridDim.x) {
-        const int m = n - o < 8 ? static_cast<int>(n - o) : 8;
-        float v[8];
-        load_row<8, false>(part, false, o, m, v);
+    __shared__ __align__(16) uint16_t lds[TileCfg<SA, SB, RCA, RCB, BI, BJ, ALIGNED>::LDS];
+    tile_product<SA, SB, RCA, RCB, BI, BJ, ALIGNED, SUMS>(g, die_order(blockIdx.x, gridDim.x), lds);
+}
+
+// Both gradients of a small layer in one launch: the first nx blocks take the
+// input gradient's tiles, the others the weight gradient's, so that neither
+// waits for the other's last tiles. SZ, SW, SX: what dz, w and x are.
+template <Source SZ, Source SW, Source SX, bool ALIGNED>
+__global__ __launch_bounds__(256) void linear_grads_kernel(TileArgs gx, TileArgs gw, unsigned nx)
+{
+    constexpr int LX = TileCfg<SZ, SW, true, false, 64, 64, ALIGNED>::LDS;
+    constexpr int LW = TileCfg<SZ, SX, false, false, 64, 64, ALIGNED>::LDS;
+    __shared__ __align__(16) uint16_t lds[LX > LW ? LX : LW];
+    if (blockIdx.x < nx)
+        tile_product<SZ, SW, true, false, 64, 64, ALIGNED, false>(gx, die_order(blockIdx.x, nx), lds);
+    else
+        tile_product<SZ, SX, false, false, 64, 64, ALIGNED, true>(
+            gw, die_order(blockIdx.x - nx, gridDim.x - nx), lds);
+}
+
+// out = sum of the splits' partial products through the epilogue, in order:
+// one piece of eight outputs (few splits) or eight threads a piece, each an
+// eighth of the splits (many)
+struct Join {
+    const float *part;
+    int splits;
+    long long n;            // outputs; 0: nothing to join
+    long long blocks;
+    Epilogue e;
+};
+
+__device__ __forceinline__ void join_block(const Join &j, long long block)
+{
+    const bool wide = j.splits >= 16;
+    __shared__ float red[256][9];
+    const long long o = 8 * (block * (wide ? 32 : 256) + (wide ? threadIdx.x >> 3 : threadIdx.x));
+    const int m = o >= j.n ? 0 : j.n - o < 8 ? static_cast<int>(j.n - o) : 8;
+    const int s0 = wide ? static_cast<int>(threadIdx.x & 7) : 0, ds = wide ? 8 : 1;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        v[k] = 0.0f;
 #pragma unroll 4
-        for (int s = 1; s < splits; ++s) {
-            float w[8];
-            load_row<8, false>(part, false, s * n + o, m, w);
+    for (int s = s0; s < j.splits; s += ds) {
+        float w[8];
+        load_row<8, false>(j.part, false, s * j.n + o, m, w);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] += w[k];
+    }
+    if (wide) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            red[threadIdx.x][k] = v[k];
+        __syncthreads();
+        if (s0)
+            return;
+#pragma unroll
+        for (int t = 1; t < 8; ++t)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                v[k] += w[k];
-        }
-        finish8<false>(e, o, 0, m, v);
+                v[k] += red[threadIdx.x + t][k];
     }
+    finish8<false>(j.e, o, 0, m, v);
+}
+
+// the input gradient's, the weight gradient's and the bias gradient's partial
+// sums in one launch
+__global__ __launch_bounds__(256) void join_kernel(Join a, Join b, Join c)
+{
+    long long k = blockIdx.x;
+    if (k < a.blocks)
+        return join_block(a, k);
+    k -= a.blocks;
+    if (k < b.blocks)
+        return join_block(b, k);
+    join_block(c, k - b.blocks);
+}
+
+Join make_join(const float *part, int splits, long long n, const Epilogue &e)
+{
+    Join j = {};
+    if (splits > 1 && n > 0) {
+        const long long per = splits >= 16 ? 256 : 2048;
+        j.part = part;
+        j.splits = splits;
+        j.n = n;
+        j.blocks = (n + per - 1) / per;
+        j.e = e;
+    }
+    return j;
 }
 
 // ------------------------------------------------------------ few rows
 
 // 16 MI rows by 16 columns of the output per block; its eight waves take the
-// reduction in turns of 64 or 128 indices, straight from memory into MFMA operands
+// reduction 32 indices at a time in turn, straight from memory into MFMA operands
 // (v_mfma_f32_16x16x32_bf16), and join through LDS in wave order.
 constexpr int kFewWaves = 8;
 
@@ -540,14 +508,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
     for (int i = 0; i < MI; ++i)
         acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
     constexpr int U = MI == 1 ? 4 : 2;                          // pieces in flight
-    for (long long r = 32LL * U * wave; r < g.R; r += 32LL * U * kFewWaves) {
+    for (long long r = 32LL * wave; r < g.R; r += 32LL * U * kFewWaves) {
         u32x4 wb[U][3], wa[U][MI][3];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            few_load<BF, ALIGNED>(g.b, j0 + rl, r + 32 * u + g8, g.R, wb[u]);
+            const long long k = r + 32LL * kFewWaves * u + g8;
+            few_load<BF, ALIGNED>(g.b, j0 + rl, k, g.R, wb[u]);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
-                few_load<AF, ALIGNED>(g.a, i0 + 16 * i + rl, r + 32 * u + g8, g.R, wa[u][i]);
+                few_load<AF, ALIGNED>(g.a, i0 + 16 * i + rl, k, g.R, wa[u][i]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -591,8 +560,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
 
 // ------------------------------------------------------------ host
 
-long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-
 enum Form { FORWARD, GRAD_X, GRAD_W };     // which operands have the reduction contiguous
 
 struct Plan {
@@ -606,7 +573,7 @@ struct Plan {
 // Tile and split of out[I][J] over R. 128 x 128 tiles where they give every CU
 // one, else 64 x 64. The reduction is split where the tiles leave CUs idle
 // (the weight gradient over many tokens; an input gradient of few rows), as
-// long as a split keeps at least four staged steps.
+// long as a split keeps a few staged steps.
 Plan plan_tile(Form f, long long I, long long J, long long R, bool af, bool bf, bool aligned)
 {
     Plan p;
@@ -616,41 +583,85 @@ Plan plan_tile(Form f, long long I, long long J, long long R, bool af, bool bf, 
     p.bi = aligned && (big >= 256 || (f == GRAD_W && big * cdiv(R, 8 * bk) >= 256 && I >= 96 && J >= 96)) ? 128 : 64;
     p.ti = cdiv(I, p.bi);
     p.tj = cdiv(J, p.bi);
+    const int step = p.bi == 128 ? bk : 2 * bk;
     const long long tiles = p.ti * p.tj;
     long long s = f == FORWARD ? 1 : tiles >= 256 ? 1 : 256 / tiles;
-    const long long most = cdiv(R, 4 * bk);
+    const long long most = cdiv(R, (p.bi == 128 ? 4 : 2) * step);
     s = s < most ? s : most;
     s = s < 1 ? 1 : s;
-    p.slice = cdiv(cdiv(R, s), bk) * bk;
+    p.slice = cdiv(cdiv(R, s), step) * step;
     p.splits = static_cast<int>(cdiv(R, p.slice));
     return p;
 }
 
-template <bool AF, bool BF, Form F>
-void launch_tile(const TileArgs &g, const Plan &p, hipStream_t st)
-{
-    constexpr bool RCA = F != GRAD_W, RCB = F == FORWARD, SUMS = F == GRAD_W;
-    const dim3 grid(static_cast<unsigned>(p.ti * p.tj * p.splits)), block(256);
-    if (!p.aligned)
-        hipLaunchKernelGGL((linear_tile_kernel<AF, BF, RCA, RCB, 64, 64, false, SUMS>), grid, block, 0, st, g);
-    else if (p.bi == 128)
-        hipLaunchKernelGGL((linear_tile_kernel<AF, BF, RCA, RCB, 128, 128, true, SUMS>), grid, block, 0, st, g);
-    else
-        hipLaunchKernelGGL((linear_tile_kernel<AF, BF, RCA, RCB, 64, 64, true, SUMS>), grid, block, 0, st, g);
-}
+unsigned blocks_of(const Plan &p) { return static_cast<unsigned>(p.ti * p.tj * p.splits); }
 
-template <Form F>
-srnl_status run_tile(TileArgs g, const Plan &p, bool af, bool bf, hipStream_t st)
+void take_plan(TileArgs &g, const Plan &p)
 {
     g.slice = p.slice;
     g.splits = p.splits;
     g.ti = static_cast<int>(p.ti);
     g.tj = static_cast<int>(p.tj);
-    if (af && bf) launch_tile<true, true, F>(g, p, st);
-    else if (af) launch_tile<true, false, F>(g, p, st);
-    else if (bf) launch_tile<false, true, F>(g, p, st);
-    else launch_tile<false, false, F>(g, p, st);
+}
+
+// the forward pass, and the gradients' products of 128 x 128 tiles
+template <Source SA, Source SB, Form F>
+void launch_tile(const TileArgs &g, const Plan &p, hipStream_t st)
+{
+    constexpr bool RCA = F != GRAD_W, RCB = F == FORWARD, SUMS = F == GRAD_W;
+    const dim3 grid(blocks_of(p)), block(256);
+    if (p.bi == 128) {
+        hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 128, 128, true, SUMS>), grid, block, 0, st, g);
+    } else if constexpr (F == FORWARD) {
+        if (p.aligned)
+            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 64, 64, true, SUMS>), grid, block, 0, st, g);
+        else
+            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 64, 64, false, SUMS>), grid, block, 0, st, g);
+    }
+}
+
+template <Form F>
+srnl_status run_tile(const TileArgs &g, const Plan &p, bool af, bool bf, hipStream_t st)
+{
+    if (af && bf) launch_tile<FP32, FP32, F>(g, p, st);
+    else if (af) launch_tile<FP32, BF16, F>(g, p, st);
+    else if (bf) launch_tile<BF16, FP32, F>(g, p, st);
+    else launch_tile<BF16, BF16, F>(g, p, st);
     return launched("linear_tile_kernel");
+}
+
+struct GradsLaunch {
+    TileArgs gx, gw;
+    unsigned nx, nw;
+    bool wf, xf, aligned;
+};
+
+template <Source SZ, Source SW, Source SX> void launch_grads(const GradsLaunch &l, hipStream_t st)
+{
+    const dim3 grid(l.nx + l.nw), block(256);
+    if (l.aligned)
+        hipLaunchKernelGGL((linear_grads_kernel<SZ, SW, SX, true>), grid, block, 0, st, l.gx, l.gw, l.nx);
+    else
+        hipLaunchKernelGGL((linear_grads_kernel<SZ, SW, SX, false>), grid, block, 0, st, l.gx, l.gw, l.nx);
+}
+
+template <Source SZ> void launch_grads_of(const GradsLaunch &l, hipStream_t st)
+{
+    if (l.wf && l.xf) launch_grads<SZ, FP32, FP32>(l, st);
+    else if (l.wf) launch_grads<SZ, FP32, BF16>(l, st);
+    else if (l.xf) launch_grads<SZ, BF16, FP32>(l, st);
+    else launch_grads<SZ, BF16, BF16>(l, st);
+}
+
+srnl_status run_grads(const GradsLaunch &l, Source sz, hipStream_t st)
+{
+    switch (sz) {
+    case BF16: launch_grads_of<BF16>(l, st); break;
+    case FP32: launch_grads_of<FP32>(l, st); break;
+    case SLOPE_BF16: launch_grads_of<SLOPE_BF16>(l, st); break;
+    case SLOPE_FP32: launch_grads_of<SLOPE_FP32>(l, st); break;
+    }
+    return launched("linear_grads_kernel");
 }
 
 template <bool AF, bool BF>
@@ -669,30 +680,35 @@ void launch_few(const TileArgs &g, bool aligned, int mi, unsigned grid, hipStrea
 #undef FEW
 }
 
-// Workspace of the backward pass (floats, 64-float aligned parts): dz where an
-// activation makes it, then the larger of the input gradient's and the weight
-// gradient's partial products, then the partial bias gradient.
+// Workspace of the backward pass (floats, 64-float aligned parts): dz where a
+// pass of its own makes it, then the partial products of the input gradient and of
+// the weight gradient, and the partial bias gradient, where they are split.
 struct BwdLayout {
     Plan px, pw;
-    long long o_part = 0, o_sum = 0, total = 0;
+    bool fused = false;    // the activation's slope is applied while dz is staged
+    long long o_x = 0, o_w = 0, o_b = 0, total = 0;
 };
 long long up64(long long n) { return (n + 63) & ~63LL; }
 
 bool pieces_ok(long long a, long long b) { return a % 8 == 0 && b % 8 == 0; }
 
-BwdLayout bwd_layout(long long M, int K, int N, const srnl_linear_params *p, bool dx, bool dw)
+BwdLayout bwd_layout(long long M, int K, int N, const srnl_linear_params *p)
 {
     BwdLayout l;
     const bool zf = p->act != SRNL_ACT_NONE || p->out_dtype == SRNL_F32;     // dz is fp32
     const bool al = pieces_ok(K, N);
     l.px = plan_tile(GRAD_X, M, K, N, zf, p->w_dtype == SRNL_F32, al);
     l.pw = plan_tile(GRAD_W, N, K, M, zf, p->x_dtype == SRNL_F32, al);
-    l.o_part = p->act != SRNL_ACT_NONE ? up64(M * N) : 0;
-    long long part = dx && l.px.splits > 1 ? l.px.splits * M * K : 0;
-    const long long pw = dw && l.pw.splits > 1 ? static_cast<long long>(l.pw.splits) * N * K : 0;
-    part = part > pw ? part : pw;
-    l.o_sum = l.o_part + up64(part);
-    l.total = l.o_sum + (dw && l.pw.splits > 1 ? up64(static_cast<long long>(l.pw.splits) * N) : 0);
+    // dz = dy act'(z) is formed anew for every 64 columns of either product:
+    // up to 2 M values that costs less than a pass of its own (backward kernels
+    // with gelu less those without, fp32: 500 x 200 -> 300, 0.6 M values, 2 us;
+    // 1000 x 512 -> 512, 4 M, 5 us; the pass takes 4.6 us and a launch)
+    l.fused = p->act != SRNL_ACT_NONE && l.px.bi == 64 && l.pw.bi == 64 && M * N * cdiv(K, 64) <= (2LL << 20);
+    l.o_x = p->act != SRNL_ACT_NONE && !l.fused ? up64(M * N) : 0;
+    l.o_w = l.o_x + (l.px.splits > 1 ? up64(l.px.splits * M * K) : 0);
+    const bool split = l.pw.splits > 1;
+    l.o_b = l.o_w + (split ? up64(static_cast<long long>(l.pw.splits) * N * K) : 0);
+    l.total = l.o_b + (split ? up64(static_cast<long long>(l.pw.splits) * N) : 0);
     return l;
 }
 
@@ -737,17 +753,20 @@ srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N, const srnl
         return s;
     hipStream_t st = static_cast<hipStream_t>(p->stream);
     TileArgs g = {};
-    g.a = {x, K, M};
-    g.b = {p->w, K, N};
+    g.a = {x, K, M, nullptr, 0};
+    g.b = {p->w, K, N, nullptr, 0};
     g.R = K;
     g.e = {out, p->out_dtype == SRNL_BF16, p->bias, p->act, p->residual,
            p->residual_dtype == SRNL_BF16, pre};
     const bool af = p->x_dtype == SRNL_F32, bf = p->w_dtype == SRNL_F32;
     const bool al = pieces_ok(K, N);
-    // few rows, or fewer 64 x 64 tiles than half the CUs
-    if (M <= 64 || cdiv(M, 64) * cdiv(N, 64) < 128) {
-        g.tj = static_cast<int>(cdiv(N, 16));
-        const int mi = M <= 16 || cdiv(M, 16) * g.tj <= 512 ? 1 : cdiv(M, 32) * g.tj <= 512 ? 2 : 4;
+    // The few-rows kernel where 64 x 16 pieces of the output are no more than
+    // the CUs, in the smallest pieces for which that holds. Measured (us, few
+    // rows / 64 x 64 tiles): 49 x 2048 -> 512 bf16 5.9 / 11.7, 512 x 512 -> 512
+    // bf16 5.0 / 5.4, fp32 8.2 / 13.6; past it 1000 x 336 -> 776 bf16 6.3 / 5.0.
+    g.tj = static_cast<int>(cdiv(N, 16));
+    if (cdiv(M, 64) * g.tj <= 256) {
+        const int mi = cdiv(M, 16) * g.tj <= 256 ? 1 : cdiv(M, 32) * g.tj <= 256 ? 2 : 4;
         const unsigned grid = static_cast<unsigned>(cdiv(M, 16 * mi) * g.tj);
         if (af && bf) launch_few<true, true>(g, al, mi, grid, st);
         else if (af) launch_few<true, false>(g, al, mi, grid, st);
@@ -755,14 +774,16 @@ srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N, const srnl
         else launch_few<false, false>(g, al, mi, grid, st);
         return launched("linear_few_kernel");
     }
-    return run_tile<FORWARD>(g, plan_tile(FORWARD, M, N, K, af, bf, al), af, bf, st);
+    const Plan plan = plan_tile(FORWARD, M, N, K, af, bf, al);
+    take_plan(g, plan);
+    return run_tile<FORWARD>(g, plan, af, bf, st);
 }
 
 size_t srnl_linear_bwd_workspace_bytes(long long M, int K, int N, const srnl_linear_params *p)
 {
     if (check_linear(M, K, N, p) != SRNL_OK || M == 0)
         return 0;
-    return static_cast<size_t>(bwd_layout(M, K, N, p, true, true).total) * sizeof(float);
+    return static_cast<size_t>(bwd_layout(M, K, N, p).total) * sizeof(float);
 }
 
 srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K, int N,
@@ -795,11 +816,11 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
     s = check_ptrs(ptrs, 9);
     if (s != SRNL_OK)
         return s;
-    const BwdLayout l = bwd_layout(M, K, N, p, true, true);
+    const BwdLayout l = bwd_layout(M, K, N, p);
     float *const ws = static_cast<float *>(workspace);
     const void *dz = dout;
     bool zf = p->out_dtype == SRNL_F32;
-    if (act) {
+    if (act && !l.fused) {
         const long long n = M * N, blocks = cdiv(n, 2048);
         hipLaunchKernelGGL(act_slope_kernel, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)),
                            dim3(256), 0, st, dout, p->out_dtype == SRNL_BF16, pre, p->act, n, ws);
@@ -809,55 +830,47 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
         dz = ws;
         zf = true;
     }
-    float *const part = ws + l.o_part;
-    if (dx) {
-        TileArgs g = {};
-        g.a = {dz, N, M};
-        g.b = {p->w, K, K};
-        g.R = N;
-        g.e.out = dx;
-        g.e.obf = p->x_dtype == SRNL_BF16;
-        g.e.add = dx_add;
-        g.e.abf = g.e.obf;
-        g.part = l.px.splits > 1 ? part : nullptr;
-        s = run_tile<GRAD_X>(g, l.px, zf, p->w_dtype == SRNL_F32, st);
-        if (s != SRNL_OK)
-            return s;
-        if (g.part) {
-            const long long n = M * K, blocks = cdiv(n, 2048);
-            hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)),
-                               dim3(256), 0, st, part, l.px.splits, n, g.e);
-            s = launched("join_kernel");
-            if (s != SRNL_OK)
-                return s;
-        }
+    const bool wf = p->w_dtype == SRNL_F32, xf = p->x_dtype == SRNL_F32;
+    TileArgs gx = {}, gw = {};
+    gx.a = {dz, N, M, pre, p->act};
+    gx.b = {p->w, K, K, nullptr, 0};
+    gx.R = N;
+    gx.e.out = dx;
+    gx.e.obf = !xf;
+    gx.e.add = dx_add;
+    gx.e.abf = !xf;
+    gx.part = l.px.splits > 1 ? ws + l.o_x : nullptr;
+    take_plan(gx, l.px);
+    gw.a = {dz, N, N, pre, p->act};
+    gw.b = {x, K, K, nullptr, 0};
+    gw.R = M;
+    gw.e.out = dw;
+    const bool split = l.pw.splits > 1;
+    gw.part = split ? ws + l.o_w : nullptr;
+    gw.rowsum = db ? (split ? ws + l.o_b : db) : nullptr;
+    take_plan(gw, l.pw);
+    const bool bigx = dx && l.px.bi == 128, bigw = dw && l.pw.bi == 128;
+    const unsigned nx = dx && !bigx ? blocks_of(l.px) : 0, nw = dw && !bigw ? blocks_of(l.pw) : 0;
+    if (bigx)
+        s = run_tile<GRAD_X>(gx, l.px, zf, wf, st);
+    if (s == SRNL_OK && bigw)
+        s = run_tile<GRAD_W>(gw, l.pw, zf, xf, st);
+    if (s == SRNL_OK && nx + nw) {
+        const Source sz = l.fused ? (zf ? SLOPE_FP32 : SLOPE_BF16) : zf ? FP32 : BF16;
+        s = run_grads({gx, gw, nx, nw, wf, xf, l.px.aligned}, sz, st);
     }
-    if (dw) {
-        TileArgs g = {};
-        g.a = {dz, N, N};
-        g.b = {x, K, K};
-        g.R = M;
-        g.e.out = dw;
-        const bool split = l.pw.splits > 1;
-        g.part = split ? part : nullptr;
-        g.rowsum = db ? (split ? ws + l.o_sum : db) : nullptr;
-        s = run_tile<GRAD_W>(g, l.pw, zf, p->x_dtype == SRNL_F32, st);
-        if (s != SRNL_OK || !split)
-            return s;
-        const long long n = static_cast<long long>(N) * K;
-        if (l.pw.splits >= 16) {
-            s = sum_rows(part, l.pw.splits, n, n, n, dw, nullptr, st);
-        } else {
-            const long long blocks = cdiv(n, 2048);
-            hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)),
-                               dim3(256), 0, st, part, l.pw.splits, n, g.e);
-            s = launched("join_kernel");
-        }
-        if (s == SRNL_OK && db)
-            s = sum_rows(g.rowsum, l.pw.splits, N, N, N, db, nullptr, st);
+    if (s != SRNL_OK)
         return s;
-    }
-    return SRNL_OK;
+    Epilogue eb = {};
+    eb.out = db;
+    const Join jx = make_join(gx.part, dx ? l.px.splits : 1, M * K, gx.e);
+    const Join jw = make_join(gw.part, dw ? l.pw.splits : 1, static_cast<long long>(N) * K, gw.e);
+    const Join jb = make_join(gw.rowsum, db ? l.pw.splits : 1, N, eb);
+    const long long blocks = jx.blocks + jw.blocks + jb.blocks;
+    if (blocks == 0)
+        return SRNL_OK;
+    hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, jx, jw, jb);
+    return launched("join_kernel");
 }
 
 }  // extern "C"

@@ -183,7 +183,7 @@ def _state_shape(heads: int, d: int):
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -640,7 +640,7 @@ def _on(x: torch.Tensor, *others: Optional[torch.Tensor]):
     for t in others:
         if t is not None and t.get_device() != i:
             raise ValueError(f"tensors on {x.device} and {t.device}")
-    return _HERE if i == torch.cuda.current_device() else torch.cuda.device(i)
+    return _HERE if i == torch._C._cuda_getDevice() else torch.cuda.device(i)
 
 
 def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
