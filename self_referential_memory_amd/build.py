@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 SRC = os.path.join(PKG, "csrc", "srnl.hip")
 # translation units, compiled side by side and linked into the one library
 UNITS = [os.path.join(PKG, "csrc", "layers", f)
-         for f in ("operator_unit.hip", "linear.hip", "narrow.hip", "layers.hip")]
+         for f in ("operator_unit.hip", "linear.hip", "narrow_bf16.hip", "narrow_fp32.hip",
+                   "narrow_slope_bf16.hip", "narrow_slope_fp32.hip", "layers.hip")]
 LIB = os.path.join(PKG, "libsrnl.so")
 # the same source with the scan kernel's phase clocks compiled in (a
 # measurement build, loaded only by bench.py --phase-clocks)

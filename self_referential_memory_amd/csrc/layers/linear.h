@@ -163,18 +163,7 @@ __device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, i
     store_row<8, ALIGNED>(e.out, e.obf, o, n, v);
 }
 
-// ------------------------------------------------------------ narrow layers
-
 constexpr long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
-
-// Both gradients of a layer whose weights fit in LDS beside a slice of rows
-// (narrow.hip). narrow_bwd_parts: how many partial weight and bias gradients
-// narrow_bwd leaves for the caller to join, 0 where it does not take the layer.
-#define SRNL_HIDDEN __attribute__((visibility("hidden")))
-SRNL_HIDDEN int narrow_bwd_parts(long long M, int K, int N, Source sz, Source sw, Source sx);
-SRNL_HIDDEN srnl_status narrow_bwd(const Operand &dz, const Operand &w, const Operand &x, int K, int N, Source sz,
-                                   Source sw, Source sx, const Epilogue &dx, float *dw_parts, float *db_parts,
-                                   int parts, hipStream_t st);
 
 }  // namespace srnl_i
 

@@ -18,7 +18,7 @@
 //
 // A few rows (or few output tiles) go to linear_few_kernel, which splits the
 // reduction over the waves of a block and joins them in LDS.
-#include "linear.h"
+#include "narrow.h"
 
 namespace {
 
@@ -459,6 +459,15 @@ Join make_join(const float *part, int splits, long long n, const Epilogue &e)
     return j;
 }
 
+srnl_status join(const Join &a, const Join &b, const Join &c, hipStream_t st)
+{
+    const long long blocks = a.blocks + b.blocks + c.blocks;
+    if (blocks == 0)
+        return SRNL_OK;
+    hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, b, c);
+    return launched("join_kernel");
+}
+
 // ------------------------------------------------------------ few rows
 
 // 16 MI rows by 16 columns of the output per block; its eight waves take the
@@ -686,7 +695,9 @@ void launch_few(const TileArgs &g, bool aligned, int mi, unsigned grid, hipStrea
 struct BwdLayout {
     Plan px, pw;
     bool fused = false;    // the activation's slope is applied while dz is staged
-    long long o_x = 0, o_w = 0, o_b = 0, total = 0;
+    int narrow = 0;        // partial gradients of the narrow form (both gradients wanted), or 0
+    Source sz = BF16, sw = BF16, sx = BF16;      // dz as the staging kernels form it, w, x
+    long long o_x = 0, o_w = 0, o_b = 0, o_nb = 0, total = 0;
 };
 long long up64(long long n) { return (n + 63) & ~63LL; }
 
@@ -709,6 +720,16 @@ BwdLayout bwd_layout(long long M, int K, int N, const srnl_linear_params *p)
     const bool split = l.pw.splits > 1;
     l.o_b = l.o_w + (split ? up64(static_cast<long long>(l.pw.splits) * N * K) : 0);
     l.total = l.o_b + (split ? up64(static_cast<long long>(l.pw.splits) * N) : 0);
+    const Source wide = p->out_dtype == SRNL_F32 ? FP32 : BF16;
+    l.sz = p->act == SRNL_ACT_NONE ? wide : wide == FP32 ? SLOPE_FP32 : SLOPE_BF16;
+    l.sw = p->w_dtype == SRNL_F32 ? FP32 : BF16;
+    l.sx = p->x_dtype == SRNL_F32 ? FP32 : BF16;
+    l.narrow = narrow_bwd_parts(M, K, N, l.sz, l.sw, l.sx);
+    if (l.narrow) {
+        l.o_nb = up64(static_cast<long long>(l.narrow) * N * K);
+        const long long all = l.o_nb + up64(static_cast<long long>(l.narrow) * N);
+        l.total = l.total > all ? l.total : all;
+    }
     return l;
 }
 
@@ -818,6 +839,24 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
         return s;
     const BwdLayout l = bwd_layout(M, K, N, p);
     float *const ws = static_cast<float *>(workspace);
+    Epilogue ew = {}, eb = {};
+    ew.out = dw;
+    eb.out = db;
+    if (dx && dw && l.narrow) {
+        const Operand oz = {dout, N, M, pre, p->act}, ow = {p->w, K, N, nullptr, 0}, ox = {x, K, M, nullptr, 0};
+        const bool xb = p->x_dtype == SRNL_BF16;
+        const Epilogue ex = {dx, xb, nullptr, SRNL_ACT_NONE, dx_add, xb, nullptr};
+        float *const nb = db ? ws + l.o_nb : nullptr;
+        const NarrowArgs g = {oz, ow, ox, M, K, N, ex, ws, nb};
+        switch (l.sz) {
+        case BF16: s = narrow_launch<BF16>(g, l.narrow, l.sw, l.sx, st); break;
+        case FP32: s = narrow_launch<FP32>(g, l.narrow, l.sw, l.sx, st); break;
+        case SLOPE_BF16: s = narrow_launch<SLOPE_BF16>(g, l.narrow, l.sw, l.sx, st); break;
+        case SLOPE_FP32: s = narrow_launch<SLOPE_FP32>(g, l.narrow, l.sw, l.sx, st); break;
+        }
+        return s == SRNL_OK ? join({}, make_join(ws, l.narrow, static_cast<long long>(N) * K, ew),
+                                   make_join(nb, db ? l.narrow : 1, N, eb), st) : s;
+    }
     const void *dz = dout;
     bool zf = p->out_dtype == SRNL_F32;
     if (act && !l.fused) {
@@ -844,7 +883,7 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
     gw.a = {dz, N, N, pre, p->act};
     gw.b = {x, K, K, nullptr, 0};
     gw.R = M;
-    gw.e.out = dw;
+    gw.e = ew;
     const bool split = l.pw.splits > 1;
     gw.part = split ? ws + l.o_w : nullptr;
     gw.rowsum = db ? (split ? ws + l.o_b : db) : nullptr;
@@ -856,21 +895,13 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
     if (s == SRNL_OK && bigw)
         s = run_tile<GRAD_W>(gw, l.pw, zf, xf, st);
     if (s == SRNL_OK && nx + nw) {
-        const Source sz = l.fused ? (zf ? SLOPE_FP32 : SLOPE_BF16) : zf ? FP32 : BF16;
-        s = run_grads({gx, gw, nx, nw, wf, xf, l.px.aligned}, sz, st);
+        s = run_grads({gx, gw, nx, nw, wf, xf, l.px.aligned}, l.fused ? l.sz : zf ? FP32 : BF16, st);
     }
     if (s != SRNL_OK)
         return s;
-    Epilogue eb = {};
-    eb.out = db;
-    const Join jx = make_join(gx.part, dx ? l.px.splits : 1, M * K, gx.e);
-    const Join jw = make_join(gw.part, dw ? l.pw.splits : 1, static_cast<long long>(N) * K, gw.e);
-    const Join jb = make_join(gw.rowsum, db ? l.pw.splits : 1, N, eb);
-    const long long blocks = jx.blocks + jw.blocks + jb.blocks;
-    if (blocks == 0)
-        return SRNL_OK;
-    hipLaunchKernelGGL(join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, jx, jw, jb);
-    return launched("join_kernel");
+    return join(make_join(gx.part, dx ? l.px.splits : 1, M * K, gx.e),
+                make_join(gw.part, dw ? l.pw.splits : 1, static_cast<long long>(N) * K, ew),
+                make_join(gw.rowsum, db ? l.pw.splits : 1, N, eb), st);
 }
 
 }  // extern "C"

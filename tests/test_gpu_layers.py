@@ -214,6 +214,32 @@ def test_linear_large_tiles_at_the_blocks_own_sizes():
     check_linear(3136, 512, 2048, F32, BF16, F32, act="gelu", seed=3)
 
 
+NARROW = [(64, 64), (40, 56), (64, 256), (256, 64), (128, 128), (72, 128), (64, 104), (16, 200), (248, 8)]
+
+
+@pytest.mark.parametrize("act", ["none", "gelu"])
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (F32, BF16, F32), (F32, F32, F32), (BF16, F32, F32),
+                                   (BF16, BF16, F32), (F32, BF16, BF16)])
+@pytest.mark.parametrize("K,N", NARROW)
+def test_linear_many_rows_of_narrow_layers(K, N, types, act):
+    """65536 rows and a ragged rest: the backward pass that keeps the weights
+    in LDS, at every width it has and between them."""
+    check_linear(65536 + 1237, K, N, *types, act=act, add=K == 64, bias=True, seed=4)
+
+
+def test_linear_narrow_backward_repeats_and_matches_its_parts():
+    x, w, dout = rnd(1, 70000, 64), rnd(2, 256, 64, dtype=BF16), rnd(3, 70000, 256)
+    pre = srnl.linear_fwd(x, w, act="gelu", keep_pre=True)[1]
+    dx, dw, db = srnl.linear_bwd(dout, x, w, pre, act="gelu")
+    again = srnl.linear_bwd(dout, x, w, pre, act="gelu")
+    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dw, db)))
+    nb = srnl.linear_bwd(dout, x, w, pre, act="gelu", need_db=False)
+    assert nb[2] is None and torch.equal(nb[0], dx) and torch.equal(nb[1], dw)
+    # one gradient alone takes the tiled kernels: the same sums in another order
+    only = srnl.linear_bwd(dout, x, w, pre, act="gelu", need_dw=False, need_db=False)[0]
+    assert (only - dx).abs().max() <= 2 * 264 * 2 * U * (dout.abs().max() * 1.13 * w.float().abs().sum(0).max())
+
+
 def test_linear_parts_of_the_gradient_and_repeats():
     x, w = rnd(1, 900, 72), rnd(2, 104, 72, dtype=BF16)
     dout = rnd(3, 900, 104)
