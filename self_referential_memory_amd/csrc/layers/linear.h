@@ -125,6 +125,15 @@ struct Operand {
 // while it is staged, with dy in bf16 or fp32.
 enum Source { BF16, FP32, SLOPE_BF16, SLOPE_FP32 };
 
+// Barrier for LDS alone: __syncthreads() would also wait for every load from
+// memory that is in flight, prefetched registers among them.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // ------------------------------------------------------------ epilogue
 
 struct Epilogue {
