@@ -48,19 +48,20 @@ __device__ __align__(16) const uint32_t zero_piece[4] = {0, 0, 0, 0};
 // in memory, the 64-byte blocks of a row permuted by r, read through the
 // transposing LDS read (ds_read_b64_tr_b16: of the 4 x 16 block that 16
 // lanes address, each lane gets a column).
-template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
+template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED, int NT = 256> struct Tile {
     static constexpr bool F32 = SRC != BF16, SLOPE = SRC == SLOPE_BF16 || SRC == SLOPE_FP32;
     static constexpr bool VALUES = SRC == FP32 || SRC == SLOPE_FP32;
     static constexpr int PARTS = F32 ? 3 : 1;
     static constexpr bool ASYNC = ALIGNED && !F32;        // straight from memory into LDS
     static constexpr int PLANE = ROWS * BK;               // words
-    static constexpr int PIECES = PLANE / 8 / 256;        // 8-element pieces per thread
-    static_assert(PIECES >= 1 && PIECES * 256 * 8 == PLANE, "pieces divide evenly");
+    static constexpr int PIECES = PLANE / 8 / NT;         // 8-element pieces per thread
+    static_assert(PIECES >= 1 && PIECES * NT * 8 == PLANE, "pieces divide evenly");
     static constexpr int PER = RC ? BK / 8 : ROWS / 8;    // pieces per stored row
 
     float v[VALUES ? PIECES : 1][8];
     u32x4 raw[VALUES ? 1 : PIECES];
     float z[SLOPE ? PIECES : 1][8];
+    const uint16_t *next[ASYNC ? PIECES : 1];             // ASYNC: where the next step's pieces are
 
     static __device__ __forceinline__ int place(int major, int c)
     {
@@ -68,31 +69,58 @@ template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
             constexpr int RP = 16 / PER;                  // rows per 256 bytes
             return c ^ ((major / RP) & (PER - 1));
         }
-        constexpr int NB = ROWS / 32, RPB = 4 / NB;       // 64-byte blocks a row, rows per 256 bytes
+        constexpr int NB = ROWS < 128 ? ROWS / 32 : 4, RPB = 4 / NB;    // 64-byte blocks of 256 bytes, rows in them
         return c ^ (4 * ((major / RPB) & (NB - 1)));
     }
 
-    // start fetching the tile at (row0, r0); ASYNC: into buf
+    // before the first fetch, at (row0, r0). ASYNC: pieces of rows outside the
+    // operand take the last row's (or first columns'), whose products are not
+    // stored.
+    __device__ __forceinline__ void start(const Operand &o, long long row0, long long r0)
+    {
+        if constexpr (ASYNC) {
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) {
+                const int s = threadIdx.x + NT * q, major = s / PER, c = place(major, s % PER);
+                const long long row = row0 + (RC ? major : 8 * c), r = r0 + (RC ? 8 * c : major);
+                const long long in = row < o.rows ? row : RC ? o.rows - 1 : 0;
+                next[q] = static_cast<const uint16_t *>(o.p) + (RC ? in * o.ld + r : r * o.ld + in);
+            }
+        }
+    }
+    // start fetching the tile at (row0, r0); ASYNC: into buf, step by step from
+    // where start() was
     __device__ __forceinline__ void fetch(const Operand &o, long long row0, long long r0, long long rend,
                                           uint16_t *buf)
     {
         const int tid = threadIdx.x;
+        if constexpr (ASYNC) {
+            const bool tail = r0 + BK > rend;
+            const long long stride = RC ? BK : BK * o.ld;
 #pragma unroll
-        for (int q = 0; q < PIECES; ++q) {
-            const int s = tid + 256 * q;
-            const int major = s / PER, c = ASYNC ? place(major, s % PER) : s % PER;
-            const long long row = row0 + (RC ? major : 8 * c), r = r0 + (RC ? 8 * c : major);
-            if constexpr (ASYNC) {
-                const uint16_t *src = reinterpret_cast<const uint16_t *>(zero_piece);
-                if (row < o.rows && r < rend)
-                    src = static_cast<const uint16_t *>(o.p) + (RC ? row * o.ld + r : r * o.ld + row);
+            for (int q = 0; q < PIECES; ++q) {
+                const uint16_t *src = next[q];
+                if (tail) {
+                    const int s = tid + NT * q, major = s / PER;
+                    if (r0 + (RC ? 8 * place(major, s % PER) : major) >= rend)
+                        src = reinterpret_cast<const uint16_t *>(zero_piece);
+                }
+                next[q] += stride;
                 // lane l of the wave writes base + 16 l
-                uint16_t *dst = buf + 8 * (256 * q + (tid & ~63));
+                uint16_t *dst = buf + 8 * (NT * q + (tid & ~63));
                 __builtin_amdgcn_global_load_lds(
                     reinterpret_cast<const __attribute__((address_space(1))) void *>(
                         reinterpret_cast<uintptr_t>(src)),
                     (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
-            } else {
+            }
+            return;
+        }
+#pragma unroll
+        for (int q = 0; q < PIECES; ++q) {
+            const int s = tid + NT * q;
+            const int major = s / PER, c = s % PER;
+            const long long row = row0 + (RC ? major : 8 * c), r = r0 + (RC ? 8 * c : major);
+            {
                 const long long left = RC ? rend - r : o.rows - row;
                 const bool in = RC ? row < o.rows : r < rend;
                 const int n = !in || left <= 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
@@ -122,7 +150,7 @@ template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED> struct Tile {
         if constexpr (!ASYNC) {
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
-                const int s = threadIdx.x + 256 * q;
+                const int s = threadIdx.x + NT * q;
                 const int major = s / PER;
                 uint16_t *dst = buf + 8 * (major * PER + place(major, s % PER));
                 if constexpr (F32) {
@@ -205,15 +233,19 @@ template <bool DIRECT> __device__ __forceinline__ void tile_barrier()
 // step ahead into the other buffer; one that is converted waits in registers.
 // Tiles of 64 are for small products, where a step is mostly the wait for its
 // loads: they take twice the reduction a step.
+constexpr int tile_waves(int bi) { return bi == 256 ? 8 : 4; }
+
 template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED> struct TileCfg {
     static constexpr int BK = (SA != BF16 || SB != BF16 ? 32 : 64) * (BI == 64 ? 2 : 1);
-    using TA = Tile<SA, RCA, BI, BK, ALIGNED>;
-    using TB = Tile<SB, RCB, BJ, BK, ALIGNED>;
+    static constexpr int NW = tile_waves(BI), WI = 2, WJ = NW / WI;      // waves, down and across
+    using TA = Tile<SA, RCA, BI, BK, ALIGNED, 64 * NW>;
+    using TB = Tile<SB, RCB, BJ, BK, ALIGNED, 64 * NW>;
     static constexpr int NA = TA::ASYNC ? 2 : 1, NB = TB::ASYNC ? 2 : 1;    // buffers
     static constexpr int PA = TA::PARTS, PB = TB::PARTS;
-    static constexpr int OUTP = 32 * (BJ / 64) + 4;             // floats per staged output row
+    static constexpr int FI = BI / 32 / WI, FJ = BJ / 32 / WJ;  // 32 x 32 tiles per wave
+    static constexpr int OUTP = 32 * FJ + 4;                    // floats per staged output row
     static constexpr int WORDS = NA * PA * TA::PLANE + NB * PB * TB::PLANE;
-    static constexpr int OUT_WORDS = 4 * 32 * OUTP * 2;
+    static constexpr int OUT_WORDS = NW * 32 * OUTP * 2;
     static constexpr int LDS = WORDS > OUT_WORDS ? WORDS : OUT_WORDS;
 };
 
@@ -225,14 +257,14 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
     using TA = typename Cfg::TA;
     using TB = typename Cfg::TB;
     constexpr int BK = Cfg::BK, NA = Cfg::NA, NB = Cfg::NB, PA = Cfg::PA, PB = Cfg::PB, OUTP = Cfg::OUTP;
-    constexpr int FI = BI / 64, FJ = BJ / 64;                   // 32 x 32 tiles per wave
+    constexpr int FI = Cfg::FI, FJ = Cfg::FJ;
     uint16_t *const la = lds, *const lb = lds + NA * PA * TA::PLANE;
 
     const int tj = t % g.tj, ti = (t / g.tj) % g.ti, sp = t / (g.tj * g.ti);
     const long long i0 = static_cast<long long>(ti) * BI, j0 = static_cast<long long>(tj) * BJ;
     const long long rb = sp * g.slice, re = rb + g.slice < g.R ? rb + g.slice : g.R;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int wi = (wave >> 1) * 32 * FI, wj = (wave & 1) * 32 * FJ;
+    const int wi = (wave / Cfg::WJ) * 32 * FI, wj = (wave % Cfg::WJ) * 32 * FJ;
     const bool sums = SUMS && g.rowsum && tj == 0 && wj == 0;
 
     TA ta;
@@ -256,6 +288,8 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
         ones = __builtin_bit_cast(bf16x8, w);
     }
 
+    ta.start(g.a, i0, rb);
+    tb.start(g.b, j0, rb);
     ta.fetch(g.a, i0, rb, re, la);
     tb.fetch(g.b, j0, rb, re, lb);
     ta.commit(g.a, la);
@@ -364,7 +398,7 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
 }
 
 template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED, bool SUMS>
-__global__ __launch_bounds__(256) void linear_tile_kernel(TileArgs g)
+__global__ __launch_bounds__(64 * tile_waves(BI)) void linear_tile_kernel(TileArgs g)
 {
     __shared__ __align__(16) uint16_t lds[TileCfg<SA, SB, RCA, RCB, BI, BJ, ALIGNED>::LDS];
     tile_product<SA, SB, RCA, RCB, BI, BJ, ALIGNED, SUMS>(g, die_order(blockIdx.x, gridDim.x), lds);
@@ -408,7 +442,7 @@ __device__ __forceinline__ void join_block(const Join &j, long long block)
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         v[k] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = s0; s < j.splits; s += ds) {
         float w[8];
         load_row<8, false>(j.part, false, s * j.n + o, m, w);
@@ -579,8 +613,10 @@ struct Plan {
     long long ti, tj;
 };
 
-// Tile and split of out[I][J] over R. 128 x 128 tiles where they give every CU
-// one, else 64 x 64. The reduction is split where the tiles leave CUs idle
+// Tile and split of out[I][J] over R. 256 x 256 (bf16 operands) or 128 x 128
+// tiles where they give every CU one, else 64 x 64: 16384 x 2048 -> 2048 bf16
+// takes 156 us in the largest and 182 us in 128 x 128, whose waves read twice
+// the LDS bytes a product (31 and 23 bytes a cycle and wave). The reduction is split where the tiles leave CUs idle
 // (the weight gradient over many tokens; an input gradient of few rows), as
 // long as a split keeps a few staged steps.
 Plan plan_tile(Form f, long long I, long long J, long long R, bool af, bool bf, bool aligned)
@@ -590,12 +626,14 @@ Plan plan_tile(Form f, long long I, long long J, long long R, bool af, bool bf, 
     const int bk = af || bf ? 32 : 64;
     const long long big = cdiv(I, 128) * cdiv(J, 128);
     p.bi = aligned && (big >= 256 || (f == GRAD_W && big * cdiv(R, 8 * bk) >= 256 && I >= 96 && J >= 96)) ? 128 : 64;
+    if (aligned && !af && !bf && f != GRAD_W && cdiv(I, 256) * cdiv(J, 256) >= 256 && R >= 256)
+        p.bi = 256;
     p.ti = cdiv(I, p.bi);
     p.tj = cdiv(J, p.bi);
-    const int step = p.bi == 128 ? bk : 2 * bk;
+    const int step = p.bi >= 128 ? bk : 2 * bk;
     const long long tiles = p.ti * p.tj;
     long long s = f == FORWARD ? 1 : tiles >= 256 ? 1 : 256 / tiles;
-    const long long most = cdiv(R, (p.bi == 128 ? 4 : 2) * step);
+    const long long most = cdiv(R, (p.bi >= 128 ? 4 : 2) * step);
     s = s < most ? s : most;
     s = s < 1 ? 1 : s;
     p.slice = cdiv(cdiv(R, s), step) * step;
@@ -619,7 +657,10 @@ void launch_tile(const TileArgs &g, const Plan &p, hipStream_t st)
 {
     constexpr bool RCA = F != GRAD_W, RCB = F == FORWARD, SUMS = F == GRAD_W;
     const dim3 grid(blocks_of(p)), block(256);
-    if (p.bi == 128) {
+    if (p.bi == 256) {
+        if constexpr (SA == BF16 && SB == BF16 && F != GRAD_W)
+            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 256, 256, true, SUMS>), grid, dim3(512), 0, st, g);
+    } else if (p.bi == 128) {
         hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 128, 128, true, SUMS>), grid, block, 0, st, g);
     } else if constexpr (F == FORWARD) {
         if (p.aligned)
@@ -888,7 +929,7 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
     gw.part = split ? ws + l.o_w : nullptr;
     gw.rowsum = db ? (split ? ws + l.o_b : db) : nullptr;
     take_plan(gw, l.pw);
-    const bool bigx = dx && l.px.bi == 128, bigw = dw && l.pw.bi == 128;
+    const bool bigx = dx && l.px.bi >= 128, bigw = dw && l.pw.bi >= 128;
     const unsigned nx = dx && !bigx ? blocks_of(l.px) : 0, nw = dw && !bigw ? blocks_of(l.pw) : 0;
     if (bigx)
         s = run_tile<GRAD_X>(gx, l.px, zf, wf, st);
