@@ -430,7 +430,7 @@ srnl_status srnl_layer_norm_fwd(const void *x, long long rows, int C, srnl_dtype
  *   dout [rows][C] in out_dtype (the forward's); x, dx in in_dtype; dx_add
  *   [rows][C] in add_dtype or NULL (a residual's gradient); dgain, dbias [C]
  *   fp32, either NULL if not wanted. Workspace (only with dgain or dbias):
- *   srnl_layer_norm_bwd_workspace_bytes.
+ *   srnl_layer_norm_bwd_workspace_bytes (may be 0).
  * Errors: as the forward, plus SRNL_ERR_WORKSPACE.
  */
 size_t srnl_layer_norm_bwd_workspace_bytes(long long rows, int C);

@@ -84,7 +84,8 @@ size_t srnl_layer_norm_bwd_workspace_bytes(long long rows, int C)
 {
     if (rows <= 0 || C < 1 || !norm_sizes_ok(rows, C))
         return 0;
-    return static_cast<size_t>(norm_bwd_blocks(rows, C)) * 2 * C * sizeof(float);
+    const int blocks = norm_bwd_blocks(rows, C);
+    return norm_direct(blocks, C) ? 0 : static_cast<size_t>(blocks) * 2 * C * sizeof(float);
 }
 
 srnl_status srnl_layer_norm_bwd(const void *dout, srnl_dtype out_dtype, const void *x,
@@ -108,12 +109,13 @@ srnl_status srnl_layer_norm_bwd(const void *dout, srnl_dtype out_dtype, const vo
             s = zero_fill(dgain, C, st);
         return s == SRNL_OK ? zero_fill(dbias, C, st) : s;
     }
-    if (params && (!workspace || workspace_bytes < srnl_layer_norm_bwd_workspace_bytes(rows, C)))
+    const bool join = params && !norm_direct(norm_bwd_blocks(rows, C), C);
+    if (join && (!workspace || workspace_bytes < srnl_layer_norm_bwd_workspace_bytes(rows, C)))
         return fail(SRNL_ERR_WORKSPACE, "workspace smaller than srnl_layer_norm_bwd_workspace_bytes");
     const PtrArg ptrs[] = {{dout, "dout", false},     {x, "x", false},         {dx, "dx", false},
                            {mean, "mean", false},     {rstd, "rstd", false},   {gain, "gain", true},
                            {dx_add, "dx_add", true},  {dgain, "dgain", true},  {dbias, "dbias", true},
-                           {params ? workspace : nullptr, "workspace", true}};
+                           {join ? workspace : nullptr, "workspace", true}};
     s = check_ptrs(ptrs, 10);
     if (s != SRNL_OK)
         return s;
@@ -130,9 +132,11 @@ srnl_status srnl_layer_norm_bwd(const void *dout, srnl_dtype out_dtype, const vo
     a.dbf = out_dtype == SRNL_BF16;
     a.add = dx_add;
     a.abf = add_dtype == SRNL_BF16;
-    a.part = params ? static_cast<float *>(workspace) : nullptr;
+    a.part = join ? static_cast<float *>(workspace) : nullptr;
+    a.dgain = dgain;
+    a.dbias = dbias;
     s = launch_norm(a, true, st);
-    if (s != SRNL_OK || !params)
+    if (s != SRNL_OK || !join)
         return s;
     return sum_rows(a.part, norm_bwd_blocks(rows, C), 2LL * C, 2LL * C, C, dgain, dbias, st);
 }

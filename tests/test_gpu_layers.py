@@ -131,6 +131,20 @@ def test_norm_constant_rows_large_offsets_and_masked_extremes(C):
     assert torch.isfinite(dx[keep]).all()
 
 
+@pytest.mark.parametrize("C", [8, 100, 640, 2100])
+@pytest.mark.parametrize("rows", [1, 2, 5, 33])
+def test_norm_backward_of_few_rows(rows, C):
+    """A few rows' parameter gradients come from one block, without a workspace."""
+    x, dout, gain = rnd(1, rows, C, dtype=BF16), rnd(2, rows, C), rnd(3, C)
+    _, n, rm, rr = norm_ref(x, gain, None, 1e-5)
+    mean, rstd = rm[:, 0].float(), rr[:, 0].float()
+    _, dg, db = srnl.layer_norm_bwd(dout, x, gain, mean, rstd)
+    nn = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    t = dout.double() * nn
+    within(dg, t.sum(0), 2 * (rows + 8) * U * t.abs().sum(0), "dgain")
+    within(db, dout.double().sum(0), 2 * (rows + 8) * U * dout.double().abs().sum(0), "dbias")
+
+
 def test_norm_no_rows():
     x = torch.empty(0, 64, device=DEV)
     gain = torch.ones(64, device=DEV)

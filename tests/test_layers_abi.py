@@ -32,7 +32,7 @@ def norm_bwd(rows=2, C=8, i=0, o=0, add=None, add_t=0, dgain=None, ws=None, nws=
 
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), ARG), (dict(C=0), ARG), (dict(i=9), DTYPE), (dict(add=16, add_t=5), DTYPE),
-    (dict(dgain=16), WS), (dict(dgain=16, ws=16, nws=8), WS), (dict(), PTR), (dict(rows=0), OK)])
+    (dict(rows=999, dgain=16), WS), (dict(rows=999, dgain=16, ws=16, nws=8), WS), (dict(), PTR), (dict(rows=0), OK)])
 def test_norm_backward_errors(kw, status):
     assert norm_bwd(**kw) == status
 
@@ -59,11 +59,11 @@ def test_linear_pointer_and_workspace_errors():
     assert linear("fwd") == PTR
     assert linear("bwd") == OK                          # nothing wanted
     assert linear("bwd", db=16) == PTR                  # the bias gradient needs the weight's
-    assert linear("bwd", M=512, act=1, dw=16) == WS
+    assert linear("bwd", M=100000, K=64, N=64, act=1, dw=16) == WS
     L = srnl.lib()
     p = srnl.LinearParams(None, None, None, 0, 0, 0, 0, 1, None)
-    n = L.srnl_linear_bwd_workspace_bytes(1000, 64, 128, ctypes.byref(p))
-    assert n >= 4 * 1000 * 128                          # dz
+    n = L.srnl_linear_bwd_workspace_bytes(9000, 512, 1024, ctypes.byref(p))
+    assert n >= 4 * 9000 * 1024                         # dz
     assert L.srnl_linear_bwd_workspace_bytes(0, 64, 128, ctypes.byref(p)) == 0
     assert L.srnl_linear_bwd_workspace_bytes(5, 0, 128, ctypes.byref(p)) == 0
     assert L.srnl_linear_bwd_workspace_bytes(5, 8, 128, None) == 0
