@@ -121,9 +121,12 @@ struct Operand {
     int act;
 };
 
-// What an operand is made of: bf16 words, fp32 values, or dy act'(z) formed
-// while it is staged, with dy in bf16 or fp32.
-enum Source { BF16, FP32, SLOPE_BF16, SLOPE_FP32 };
+// What an operand is made of: bf16 words (in rows of whole 16-byte pieces, or
+// in rows of any length), fp32 values, or dy act'(z) formed while it is staged,
+// with dy in bf16 or fp32. The card takes wide loads at any element's address;
+// only the direct loads into LDS ask for whole pieces.
+enum Source { BF16, BF16_ANY, FP32, SLOPE_BF16, SLOPE_FP32 };
+constexpr bool is_bf16(Source s) { return s == BF16 || s == BF16_ANY; }
 
 // Barrier for LDS alone: __syncthreads() would also wait for every load from
 // memory that is in flight, prefetched registers among them.
@@ -146,30 +149,31 @@ struct Epilogue {
     float *pre;            // [I][J] or NULL: z before the activation
 };
 
-// eight neighbouring outputs (i, j .. j + 7) from their sums; n are inside
-template <bool ALIGNED>
+// eight neighbouring outputs (i, j .. j + 7) from their sums; n are inside. WHOLE: the
+// rows are whole pieces, so that n is 8 or nothing
+template <bool WHOLE>
 __device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, int n, float (&v)[8])
 {
     if (n <= 0)
         return;
     if (e.bias) {
         float b[8];
-        load_row<8, ALIGNED>(e.bias, false, j, n, b);
+        load_row<8, WHOLE>(e.bias, false, j, n, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             v[k] += b[k];
     }
     if (e.pre)
-        store_row<8, ALIGNED>(e.pre, false, o, n, v);
+        store_row<8, WHOLE>(e.pre, false, o, n, v);
     act_values(v, e.act);
     if (e.add) {
         float a[8];
-        load_row<8, ALIGNED>(e.add, e.abf, o, n, a);
+        load_row<8, WHOLE>(e.add, e.abf, o, n, a);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             v[k] += a[k];
     }
-    store_row<8, ALIGNED>(e.out, e.obf, o, n, v);
+    store_row<8, WHOLE>(e.out, e.obf, o, n, v);
 }
 
 constexpr long long cdiv(long long a, long long b) { return (a + b - 1) / b; }

@@ -48,11 +48,11 @@ __device__ __align__(16) const uint32_t zero_piece[4] = {0, 0, 0, 0};
 // in memory, the 64-byte blocks of a row permuted by r, read through the
 // transposing LDS read (ds_read_b64_tr_b16: of the 4 x 16 block that 16
 // lanes address, each lane gets a column).
-template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED, int NT = 256> struct Tile {
-    static constexpr bool F32 = SRC != BF16, SLOPE = SRC == SLOPE_BF16 || SRC == SLOPE_FP32;
+template <Source SRC, bool RC, int ROWS, int BK, int NT = 256> struct Tile {
+    static constexpr bool F32 = !is_bf16(SRC), SLOPE = SRC == SLOPE_BF16 || SRC == SLOPE_FP32;
     static constexpr bool VALUES = SRC == FP32 || SRC == SLOPE_FP32;
     static constexpr int PARTS = F32 ? 3 : 1;
-    static constexpr bool ASYNC = ALIGNED && !F32;        // straight from memory into LDS
+    static constexpr bool ASYNC = SRC == BF16;            // straight from memory into LDS
     static constexpr int PLANE = ROWS * BK;               // words
     static constexpr int PIECES = PLANE / 8 / NT;         // 8-element pieces per thread
     static_assert(PIECES >= 1 && PIECES * NT * 8 == PLANE, "pieces divide evenly");
@@ -62,6 +62,8 @@ template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED, int NT = 256> str
     u32x4 raw[VALUES ? 1 : PIECES];
     float z[SLOPE ? PIECES : 1][8];
     const uint16_t *next[ASYNC ? PIECES : 1];             // ASYNC: where the next step's pieces are
+    long long off;                                        // otherwise: the first one's offset
+    long long total;                                      // elements of the operand
 
     static __device__ __forceinline__ int place(int major, int c)
     {
@@ -73,10 +75,10 @@ template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED, int NT = 256> str
         return c ^ (4 * ((major / RPB) & (NB - 1)));
     }
 
-    // before the first fetch, at (row0, r0). ASYNC: pieces of rows outside the
-    // operand take the last row's (or first columns'), whose products are not
-    // stored.
-    __device__ __forceinline__ void start(const Operand &o, long long row0, long long r0)
+    // before the first fetch, at (row0, r0) of an operand with R reduction
+    // indices. ASYNC: pieces of rows outside the operand take the last row's (or
+    // first columns'), whose products are not stored.
+    __device__ __forceinline__ void start(const Operand &o, long long row0, long long r0, long long R)
     {
         if constexpr (ASYNC) {
 #pragma unroll
@@ -86,12 +88,19 @@ template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED, int NT = 256> str
                 const long long in = row < o.rows ? row : RC ? o.rows - 1 : 0;
                 next[q] = static_cast<const uint16_t *>(o.p) + (RC ? in * o.ld + r : r * o.ld + in);
             }
+        } else {
+            total = RC ? o.rows * o.ld : R * o.ld;
+            off = offset(o, row0, r0, 0);
         }
     }
-    // start fetching the tile at (row0, r0); ASYNC: into buf, step by step from
-    // where start() was
-    __device__ __forceinline__ void fetch(const Operand &o, long long row0, long long r0, long long rend,
-                                          uint16_t *buf)
+    static __device__ __forceinline__ long long offset(const Operand &o, long long row0, long long r0, int q)
+    {
+        const int s = threadIdx.x + NT * q, major = s / PER, c = s % PER;
+        return RC ? (row0 + major) * o.ld + r0 + 8 * c : (r0 + major) * o.ld + row0 + 8 * c;
+    }
+    // start fetching the tile at r0, step by step from where start() was; ASYNC:
+    // into buf
+    __device__ __forceinline__ void fetch(const Operand &o, long long r0, long long rend, uint16_t *buf)
     {
         const int tid = threadIdx.x;
         if constexpr (ASYNC) {
@@ -115,39 +124,72 @@ template <Source SRC, bool RC, int ROWS, int BK, bool ALIGNED, int NT = 256> str
             }
             return;
         }
+        // Every piece is one wide load without a condition, so that nothing waits
+        // for it here: what lies past the reduction, or past the operand's last
+        // eight elements, is put right by commit(). Rows (columns) past the last
+        // hold whatever is there; their products are not stored.
+        const long long last = total - 8;
+        if (last >= 0) {
+#pragma unroll
+            for (int q = 0; q < PIECES; ++q) {
+                static_assert(NT % PER == 0, "a thread's pieces are alike but for their row");
+                const long long my = off + q * (NT / PER) * o.ld, at = my < last ? my : last;
+                if constexpr (SLOPE)
+                    load_f32<8, false>(o.z + at, z[q]);
+                if constexpr (VALUES)
+                    load_f32<8, false>(static_cast<const float *>(o.p) + at, v[q]);
+                else
+                    __builtin_memcpy(&raw[q], static_cast<const uint16_t *>(o.p) + at, 16);
+            }
+            off += RC ? BK : BK * o.ld;
+        }
+    }
+    // the tile at (row0, r0) as fetched, where it reaches the operand's end:
+    // zeros past the reduction, and the last elements one by one
+    __device__ __forceinline__ void mend(const Operand &o, long long row0, long long r0, long long rend)
+    {
+        const long long wide = row0 + ROWS < o.rows ? row0 + ROWS : (o.rows + 7) & ~7LL;
+        if (r0 + BK <= rend && (RC || (r0 + BK - 1) * o.ld + wide <= total))
+            return;
 #pragma unroll
         for (int q = 0; q < PIECES; ++q) {
-            const int s = tid + NT * q;
-            const int major = s / PER, c = s % PER;
-            const long long row = row0 + (RC ? major : 8 * c), r = r0 + (RC ? 8 * c : major);
-            {
-                const long long left = RC ? rend - r : o.rows - row;
-                const bool in = RC ? row < o.rows : r < rend;
-                const int n = !in || left <= 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
-                const long long at = RC ? row * o.ld + r : r * o.ld + row;
-                if constexpr (SLOPE)
-                    load_row<8, ALIGNED>(o.z, false, at, n, z[q]);
-                if constexpr (VALUES) {
-                    load_row<8, ALIGNED>(o.p, false, at, n, v[q]);
-                } else {
-                    raw[q] = u32x4{0, 0, 0, 0};
-                    const uint16_t *src = static_cast<const uint16_t *>(o.p) + at;
-                    if (n == 8) {
-                        __builtin_memcpy(&raw[q], src, 16);
-                    } else {
+            const int s = threadIdx.x + NT * q, major = s / PER, c = s % PER;
+            const long long left = RC ? rend - r0 - 8 * c : r0 + major < rend ? 8 : 0;
+            const int n = left < 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
+            const long long at = offset(o, row0, r0, q);
+            const bool single = n > 0 && at > total - 8;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (e < n)
-                                raw[q][e / 2] |= static_cast<uint32_t>(src[e]) << (16 * (e & 1));
+            for (int e = 0; e < 8; ++e) {
+                const bool in = e < n;
+                if constexpr (SLOPE)
+                    z[q][e] = in ? z[q][e] : 0.0f;
+                if constexpr (VALUES)
+                    v[q][e] = in ? v[q][e] : 0.0f;
+                else
+                    raw[q][e / 2] = in ? raw[q][e / 2] : raw[q][e / 2] & (e & 1 ? 0xFFFFu : 0xFFFF0000u);
+            }
+            if (single) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const bool in = e < n && at + e < total;
+                    const long long x = in ? at + e : 0;
+                    if constexpr (SLOPE)
+                        z[q][e] = in ? o.z[x] : 0.0f;
+                    if constexpr (VALUES) {
+                        v[q][e] = in ? static_cast<const float *>(o.p)[x] : 0.0f;
+                    } else {
+                        const uint32_t w = in ? static_cast<const uint16_t *>(o.p)[x] : 0u;
+                        raw[q][e / 2] = e & 1 ? raw[q][e / 2] | w << 16 : w;
                     }
                 }
             }
         }
     }
     // write what fetch holds in registers to buf
-    __device__ __forceinline__ void commit(const Operand &o, uint16_t *buf) const
+    __device__ __forceinline__ void commit(const Operand &o, long long row0, long long r0, long long rend, uint16_t *buf)
     {
         if constexpr (!ASYNC) {
+            mend(o, row0, r0, rend);
 #pragma unroll
             for (int q = 0; q < PIECES; ++q) {
                 const int s = threadIdx.x + NT * q;
@@ -235,11 +277,11 @@ template <bool DIRECT> __device__ __forceinline__ void tile_barrier()
 // loads: they take twice the reduction a step.
 constexpr int tile_waves(int bi) { return bi == 256 ? 8 : 4; }
 
-template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED> struct TileCfg {
-    static constexpr int BK = (SA != BF16 || SB != BF16 ? 32 : 64) * (BI == 64 ? 2 : 1);
+template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ> struct TileCfg {
+    static constexpr int BK = (is_bf16(SA) && is_bf16(SB) ? 64 : 32) * (BI == 64 ? 2 : 1);
     static constexpr int NW = tile_waves(BI), WI = 2, WJ = NW / WI;      // waves, down and across
-    using TA = Tile<SA, RCA, BI, BK, ALIGNED, 64 * NW>;
-    using TB = Tile<SB, RCB, BJ, BK, ALIGNED, 64 * NW>;
+    using TA = Tile<SA, RCA, BI, BK, 64 * NW>;
+    using TB = Tile<SB, RCB, BJ, BK, 64 * NW>;
     static constexpr int NA = TA::ASYNC ? 2 : 1, NB = TB::ASYNC ? 2 : 1;    // buffers
     static constexpr int PA = TA::PARTS, PB = TB::PARTS;
     static constexpr int FI = BI / 32 / WI, FJ = BJ / 32 / WJ;  // 32 x 32 tiles per wave
@@ -247,13 +289,17 @@ template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED
     static constexpr int WORDS = NA * PA * TA::PLANE + NB * PB * TB::PLANE;
     static constexpr int OUT_WORDS = NW * 32 * OUTP * 2;
     static constexpr int LDS = WORDS > OUT_WORDS ? WORDS : OUT_WORDS;
+    // Blocks a CU that the registers are held to: as many as fit in LDS where
+    // that costs no spill (132 registers become 128, three blocks four:
+    // 200704 x 64 -> 256 fp32 with bf16 weights 78 -> 73 us).
+    static constexpr int BLOCKS = RCA && RCB && BI == 128 && SA == FP32 && SB != BF16_ANY ? 160 * 1024 / (2 * LDS) : 1;
 };
 
 // tile t of g, in lds of TileCfg::LDS words
-template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED, bool SUMS>
+template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool SUMS>
 __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint16_t *lds)
 {
-    using Cfg = TileCfg<SA, SB, RCA, RCB, BI, BJ, ALIGNED>;
+    using Cfg = TileCfg<SA, SB, RCA, RCB, BI, BJ>;
     using TA = typename Cfg::TA;
     using TB = typename Cfg::TB;
     constexpr int BK = Cfg::BK, NA = Cfg::NA, NB = Cfg::NB, PA = Cfg::PA, PB = Cfg::PB, OUTP = Cfg::OUTP;
@@ -288,12 +334,12 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
         ones = __builtin_bit_cast(bf16x8, w);
     }
 
-    ta.start(g.a, i0, rb);
-    tb.start(g.b, j0, rb);
-    ta.fetch(g.a, i0, rb, re, la);
-    tb.fetch(g.b, j0, rb, re, lb);
-    ta.commit(g.a, la);
-    tb.commit(g.b, lb);
+    ta.start(g.a, i0, rb, g.R);
+    tb.start(g.b, j0, rb, g.R);
+    ta.fetch(g.a, rb, re, la);
+    tb.fetch(g.b, rb, re, lb);
+    ta.commit(g.a, i0, rb, re, la);
+    tb.commit(g.b, j0, rb, re, lb);
     int cur = 0;
     tile_barrier<NA == 2 || NB == 2>();
     for (long long r = rb; r < re; r += BK) {
@@ -302,8 +348,8 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
         uint16_t *const cb = lb + (NB == 2 ? cur : 0) * PB * TB::PLANE, *const nb = lb + (NB == 2 ? nxt : 0) * PB * TB::PLANE;
         const bool more = r + BK < re;
         if (more) {
-            ta.fetch(g.a, i0, r + BK, re, na);
-            tb.fetch(g.b, j0, r + BK, re, nb);
+            ta.fetch(g.a, r + BK, re, na);
+            tb.fetch(g.b, r + BK, re, nb);
         }
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
@@ -344,8 +390,8 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
         if (NA == 1 || NB == 1)
             __syncthreads();                 // everyone has read the only buffer
         if (more) {
-            ta.commit(g.a, na);
-            tb.commit(g.b, nb);
+            ta.commit(g.a, i0, r + BK, re, na);
+            tb.commit(g.b, j0, r + BK, re, nb);
         }
         cur = nxt;
         tile_barrier<NA == 2 || NB == 2>();
@@ -388,35 +434,38 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
             const long long oi = i0 + wi + 32 * i + row;
             const long long oj = j0 + wj + c;
             const long long left = g.b.rows - oj;
-            if (oi < g.a.rows)
-                finish8<ALIGNED>(e, oi * g.b.rows + oj, static_cast<int>(oj),
-                                 left < 8 ? static_cast<int>(left) : 8, v);
+            const int n = oi >= g.a.rows || left <= 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
+            if (g.b.rows % 8 == 0)
+                finish8<true>(e, oi * g.b.rows + oj, static_cast<int>(oj), n, v);
+            else
+                finish8<false>(e, oi * g.b.rows + oj, static_cast<int>(oj), n, v);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
 }
 
-template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool ALIGNED, bool SUMS>
-__global__ __launch_bounds__(64 * tile_waves(BI)) void linear_tile_kernel(TileArgs g)
+template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool SUMS>
+__global__ __launch_bounds__(64 * tile_waves(BI), (TileCfg<SA, SB, RCA, RCB, BI, BJ>::BLOCKS))
+void linear_tile_kernel(TileArgs g)
 {
-    __shared__ __align__(16) uint16_t lds[TileCfg<SA, SB, RCA, RCB, BI, BJ, ALIGNED>::LDS];
-    tile_product<SA, SB, RCA, RCB, BI, BJ, ALIGNED, SUMS>(g, die_order(blockIdx.x, gridDim.x), lds);
+    __shared__ __align__(16) uint16_t lds[TileCfg<SA, SB, RCA, RCB, BI, BJ>::LDS];
+    tile_product<SA, SB, RCA, RCB, BI, BJ, SUMS>(g, die_order(blockIdx.x, gridDim.x), lds);
 }
 
 // Both gradients of a small layer in one launch: the first nx blocks take the
 // input gradient's tiles, the others the weight gradient's, so that neither
 // waits for the other's last tiles. SZ, SW, SX: what dz, w and x are.
-template <Source SZ, Source SW, Source SX, bool ALIGNED>
+template <Source SZ, Source SW, Source SX>
 __global__ __launch_bounds__(256) void linear_grads_kernel(TileArgs gx, TileArgs gw, unsigned nx)
 {
-    constexpr int LX = TileCfg<SZ, SW, true, false, 64, 64, ALIGNED>::LDS;
-    constexpr int LW = TileCfg<SZ, SX, false, false, 64, 64, ALIGNED>::LDS;
+    constexpr int LX = TileCfg<SZ, SW, true, false, 64, 64>::LDS;
+    constexpr int LW = TileCfg<SZ, SX, false, false, 64, 64>::LDS;
     __shared__ __align__(16) uint16_t lds[LX > LW ? LX : LW];
     if (blockIdx.x < nx)
-        tile_product<SZ, SW, true, false, 64, 64, ALIGNED, false>(gx, die_order(blockIdx.x, nx), lds);
+        tile_product<SZ, SW, true, false, 64, 64, false>(gx, die_order(blockIdx.x, nx), lds);
     else
-        tile_product<SZ, SX, false, false, 64, 64, ALIGNED, true>(
+        tile_product<SZ, SX, false, false, 64, 64, true>(
             gw, die_order(blockIdx.x - nx, gridDim.x - nx), lds);
 }
 
@@ -509,7 +558,7 @@ srnl_status join(const Join &a, const Join &b, const Join &c, hipStream_t st)
 // (v_mfma_f32_16x16x32_bf16), and join through LDS in wave order.
 constexpr int kFewWaves = 8;
 
-template <bool F32, bool ALIGNED>
+template <bool F32>
 __device__ __forceinline__ void few_load(const Operand &o, long long row, long long r, long long R,
                                          u32x4 (&w)[3])
 {
@@ -518,26 +567,26 @@ __device__ __forceinline__ void few_load(const Operand &o, long long row, long l
     const long long at = row * o.ld + r;
     if constexpr (F32) {
         float v[8];
-        load_row<8, ALIGNED>(o.p, false, at, n, v);
+        load_row<8, false>(o.p, false, at, n, v);
         split_parts(v, w);
     } else {
         w[0] = u32x4{0, 0, 0, 0};
         const uint16_t *src = static_cast<const uint16_t *>(o.p) + at;
-        if (ALIGNED ? n > 0 : n == 8) {
-            if (ALIGNED)
-                w[0] = *reinterpret_cast<const u32x4 *>(src);
-            else
-                __builtin_memcpy(&w[0], src, 16);
-        } else if (!ALIGNED) {
+        if (n == 8) {
+            __builtin_memcpy(&w[0], src, 16);
+        } else if (n > 0) {
+            uint16_t t[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (e < n)
-                    w[0][e / 2] |= static_cast<uint32_t>(src[e]) << (16 * (e & 1));
+                t[e] = src[e < n ? e : 0];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[0][e] = (2 * e < n ? t[2 * e] : 0u) | (2 * e + 1 < n ? static_cast<uint32_t>(t[2 * e + 1]) << 16 : 0u);
         }
     }
 }
 
-template <bool AF, bool BF, int MI, bool ALIGNED>
+template <bool AF, bool BF, int MI>
 __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
 {
     constexpr int PA = AF ? 3 : 1, PB = BF ? 3 : 1;
@@ -556,10 +605,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long k = r + 32LL * kFewWaves * u + g8;
-            few_load<BF, ALIGNED>(g.b, j0 + rl, k, g.R, wb[u]);
+            few_load<BF>(g.b, j0 + rl, k, g.R, wb[u]);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
-                few_load<AF, ALIGNED>(g.a, i0 + 16 * i + rl, k, g.R, wa[u][i]);
+                few_load<AF>(g.a, i0 + 16 * i + rl, k, g.R, wa[u][i]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -597,8 +646,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
             v[k] += t[k];
     }
     const long long left = g.b.rows - (j0 + c);
-    finish8<ALIGNED>(g.e, (i0 + row) * g.b.rows + j0 + c, static_cast<int>(j0 + c),
-                     left < 8 ? static_cast<int>(left) : 8, v);
+    finish8<false>(g.e, (i0 + row) * g.b.rows + j0 + c, static_cast<int>(j0 + c),
+                   left < 8 ? static_cast<int>(left) : 8, v);
 }
 
 // ------------------------------------------------------------ host
@@ -606,7 +655,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
 enum Form { FORWARD, GRAD_X, GRAD_W };     // which operands have the reduction contiguous
 
 struct Plan {
-    bool aligned;
     int bi;                // tile side
     int splits;
     long long slice;
@@ -619,20 +667,20 @@ struct Plan {
 // the LDS bytes a product (31 and 23 bytes a cycle and wave). The reduction is split where the tiles leave CUs idle
 // (the weight gradient over many tokens; an input gradient of few rows), as
 // long as a split keeps a few staged steps.
-Plan plan_tile(Form f, long long I, long long J, long long R, bool af, bool bf, bool aligned)
+Plan plan_tile(Form f, long long I, long long J, long long R, Source sa, Source sb)
 {
     Plan p;
-    p.aligned = aligned;
-    const int bk = af || bf ? 32 : 64;
+    const int bk = is_bf16(sa) && is_bf16(sb) ? 64 : 32;
     const long long big = cdiv(I, 128) * cdiv(J, 128);
-    p.bi = aligned && (big >= 256 || (f == GRAD_W && big * cdiv(R, 8 * bk) >= 256 && I >= 96 && J >= 96)) ? 128 : 64;
-    if (aligned && !af && !bf && f != GRAD_W && cdiv(I, 256) * cdiv(J, 256) >= 256 && R >= 256)
+    p.bi = (big >= 256 || (f == GRAD_W && big * cdiv(R, 8 * bk) >= 256 && I >= 96 && J >= 96)) ? 128 : 64;
+    if (sa == BF16 && sb == BF16 && f != GRAD_W && cdiv(I, 256) * cdiv(J, 256) >= 256 && R >= 256)
         p.bi = 256;
     p.ti = cdiv(I, p.bi);
     p.tj = cdiv(J, p.bi);
     const int step = p.bi >= 128 ? bk : 2 * bk;
     const long long tiles = p.ti * p.tj;
-    long long s = f == FORWARD ? 1 : tiles >= 256 ? 1 : 256 / tiles;
+    // ten steps take about as long as the launch that joins a split
+    long long s = f == FORWARD || tiles >= 256 || R <= 10 * step ? 1 : 256 / tiles;
     const long long most = cdiv(R, (p.bi >= 128 ? 4 : 2) * step);
     s = s < most ? s : most;
     s = s < 1 ? 1 : s;
@@ -659,54 +707,63 @@ void launch_tile(const TileArgs &g, const Plan &p, hipStream_t st)
     const dim3 grid(blocks_of(p)), block(256);
     if (p.bi == 256) {
         if constexpr (SA == BF16 && SB == BF16 && F != GRAD_W)
-            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 256, 256, true, SUMS>), grid, dim3(512), 0, st, g);
+            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 256, 256, SUMS>), grid, dim3(512), 0, st, g);
     } else if (p.bi == 128) {
-        hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 128, 128, true, SUMS>), grid, block, 0, st, g);
+        hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 128, 128, SUMS>), grid, block, 0, st, g);
     } else if constexpr (F == FORWARD) {
-        if (p.aligned)
-            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 64, 64, true, SUMS>), grid, block, 0, st, g);
-        else
-            hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 64, 64, false, SUMS>), grid, block, 0, st, g);
+        hipLaunchKernelGGL((linear_tile_kernel<SA, SB, RCA, RCB, 64, 64, SUMS>), grid, block, 0, st, g);
     }
 }
 
-template <Form F>
-srnl_status run_tile(const TileArgs &g, const Plan &p, bool af, bool bf, hipStream_t st)
+template <Source SA, Form F> void launch_tile_of(const TileArgs &g, const Plan &p, Source sb, hipStream_t st)
 {
-    if (af && bf) launch_tile<FP32, FP32, F>(g, p, st);
-    else if (af) launch_tile<FP32, BF16, F>(g, p, st);
-    else if (bf) launch_tile<BF16, FP32, F>(g, p, st);
-    else launch_tile<BF16, BF16, F>(g, p, st);
+    // forward: both operands' rows are K long, so of one kind
+    if (sb == FP32) {
+        launch_tile<SA, FP32, F>(g, p, st);
+    } else if (sb == BF16) {
+        if constexpr (F != FORWARD || SA != BF16_ANY)
+            launch_tile<SA, BF16, F>(g, p, st);
+    } else {
+        if constexpr (F != FORWARD || SA != BF16)
+            launch_tile<SA, BF16_ANY, F>(g, p, st);
+    }
+}
+
+template <Form F> srnl_status run_tile(const TileArgs &g, const Plan &p, Source sa, Source sb, hipStream_t st)
+{
+    if (sa == FP32) launch_tile_of<FP32, F>(g, p, sb, st);
+    else if (sa == BF16) launch_tile_of<BF16, F>(g, p, sb, st);
+    else launch_tile_of<BF16_ANY, F>(g, p, sb, st);
     return launched("linear_tile_kernel");
 }
 
 struct GradsLaunch {
     TileArgs gx, gw;
     unsigned nx, nw;
-    bool wf, xf, aligned;
+    Source sz, sw, sx;
 };
 
 template <Source SZ, Source SW, Source SX> void launch_grads(const GradsLaunch &l, hipStream_t st)
 {
-    const dim3 grid(l.nx + l.nw), block(256);
-    if (l.aligned)
-        hipLaunchKernelGGL((linear_grads_kernel<SZ, SW, SX, true>), grid, block, 0, st, l.gx, l.gw, l.nx);
-    else
-        hipLaunchKernelGGL((linear_grads_kernel<SZ, SW, SX, false>), grid, block, 0, st, l.gx, l.gw, l.nx);
+    hipLaunchKernelGGL((linear_grads_kernel<SZ, SW, SX>), dim3(l.nx + l.nw), dim3(256), 0, st, l.gx, l.gw, l.nx);
 }
 
 template <Source SZ> void launch_grads_of(const GradsLaunch &l, hipStream_t st)
 {
-    if (l.wf && l.xf) launch_grads<SZ, FP32, FP32>(l, st);
-    else if (l.wf) launch_grads<SZ, FP32, BF16>(l, st);
-    else if (l.xf) launch_grads<SZ, BF16, FP32>(l, st);
-    else launch_grads<SZ, BF16, BF16>(l, st);
+    if (l.sw == FP32 && l.sx == FP32) launch_grads<SZ, FP32, FP32>(l, st);
+    else if (l.sw == FP32 && l.sx == BF16) launch_grads<SZ, FP32, BF16>(l, st);
+    else if (l.sw == FP32) launch_grads<SZ, FP32, BF16_ANY>(l, st);
+    else if (l.sx == FP32 && l.sw == BF16) launch_grads<SZ, BF16, FP32>(l, st);
+    else if (l.sx == FP32) launch_grads<SZ, BF16_ANY, FP32>(l, st);
+    else if (l.sw == BF16) launch_grads<SZ, BF16, BF16>(l, st);     // both have rows of K
+    else launch_grads<SZ, BF16_ANY, BF16_ANY>(l, st);
 }
 
-srnl_status run_grads(const GradsLaunch &l, Source sz, hipStream_t st)
+srnl_status run_grads(const GradsLaunch &l, hipStream_t st)
 {
-    switch (sz) {
+    switch (l.sz) {
     case BF16: launch_grads_of<BF16>(l, st); break;
+    case BF16_ANY: launch_grads_of<BF16_ANY>(l, st); break;
     case FP32: launch_grads_of<FP32>(l, st); break;
     case SLOPE_BF16: launch_grads_of<SLOPE_BF16>(l, st); break;
     case SLOPE_FP32: launch_grads_of<SLOPE_FP32>(l, st); break;
@@ -714,21 +771,19 @@ srnl_status run_grads(const GradsLaunch &l, Source sz, hipStream_t st)
     return launched("linear_grads_kernel");
 }
 
-template <bool AF, bool BF>
-void launch_few(const TileArgs &g, bool aligned, int mi, unsigned grid, hipStream_t st)
+template <bool AF, bool BF> void launch_few(const TileArgs &g, int mi, unsigned grid, hipStream_t st)
 {
-#define FEW(MI, AL) hipLaunchKernelGGL((linear_few_kernel<AF, BF, MI, AL>), dim3(grid), dim3(64 * kFewWaves), 0, st, g)
-    if (aligned) {
-        if (mi == 1) FEW(1, true);
-        else if (mi == 2) FEW(2, true);
-        else FEW(4, true);
-    } else {
-        if (mi == 1) FEW(1, false);
-        else if (mi == 2) FEW(2, false);
-        else FEW(4, false);
-    }
-#undef FEW
+    const dim3 block(64 * kFewWaves);
+    if (mi == 1)
+        hipLaunchKernelGGL((linear_few_kernel<AF, BF, 1>), dim3(grid), block, 0, st, g);
+    else if (mi == 2)
+        hipLaunchKernelGGL((linear_few_kernel<AF, BF, 2>), dim3(grid), block, 0, st, g);
+    else
+        hipLaunchKernelGGL((linear_few_kernel<AF, BF, 4>), dim3(grid), block, 0, st, g);
 }
+
+// what an operand with rows of n elements is, for the tiled kernels
+Source source_of(srnl_dtype t, long long n) { return t == SRNL_F32 ? FP32 : n % 8 == 0 ? BF16 : BF16_ANY; }
 
 // Workspace of the backward pass (floats, 64-float aligned parts): dz where a
 // pass of its own makes it, then the partial products of the input gradient and of
@@ -737,35 +792,35 @@ struct BwdLayout {
     Plan px, pw;
     bool fused = false;    // the activation's slope is applied while dz is staged
     int narrow = 0;        // partial gradients of the narrow form (both gradients wanted), or 0
-    Source sz = BF16, sw = BF16, sx = BF16;      // dz as the staging kernels form it, w, x
+    Source sz = BF16, sw = BF16, sx = BF16;      // what the tiled kernels stage
+    Source narrow_z = BF16;
     long long o_x = 0, o_w = 0, o_b = 0, o_nb = 0, total = 0;
 };
 long long up64(long long n) { return (n + 63) & ~63LL; }
 
-bool pieces_ok(long long a, long long b) { return a % 8 == 0 && b % 8 == 0; }
-
 BwdLayout bwd_layout(long long M, int K, int N, const srnl_linear_params *p)
 {
     BwdLayout l;
-    const bool zf = p->act != SRNL_ACT_NONE || p->out_dtype == SRNL_F32;     // dz is fp32
-    const bool al = pieces_ok(K, N);
-    l.px = plan_tile(GRAD_X, M, K, N, zf, p->w_dtype == SRNL_F32, al);
-    l.pw = plan_tile(GRAD_W, N, K, M, zf, p->x_dtype == SRNL_F32, al);
+    const bool act = p->act != SRNL_ACT_NONE;
+    l.sw = source_of(p->w_dtype, K);
+    l.sx = source_of(p->x_dtype, K);
+    const Source sy = source_of(p->out_dtype, N), sz = act ? FP32 : sy;      // dz as a pass leaves it
+    l.px = plan_tile(GRAD_X, M, K, N, sz, l.sw);
+    l.pw = plan_tile(GRAD_W, N, K, M, sz, l.sx);
+    const Source slope = p->out_dtype == SRNL_F32 ? SLOPE_FP32 : SLOPE_BF16;
     // dz = dy act'(z) is formed anew for every 64 columns of either product:
     // up to 2 M values that costs less than a pass of its own (backward kernels
     // with gelu less those without, fp32: 500 x 200 -> 300, 0.6 M values, 2 us;
     // 1000 x 512 -> 512, 4 M, 5 us; the pass takes 4.6 us and a launch)
-    l.fused = p->act != SRNL_ACT_NONE && l.px.bi == 64 && l.pw.bi == 64 && M * N * cdiv(K, 64) <= (2LL << 20);
-    l.o_x = p->act != SRNL_ACT_NONE && !l.fused ? up64(M * N) : 0;
+    l.fused = act && l.px.bi == 64 && l.pw.bi == 64 && M * N * cdiv(K, 64) <= (2LL << 20);
+    l.sz = l.fused ? slope : sz;
+    l.o_x = act && !l.fused ? up64(M * N) : 0;
     l.o_w = l.o_x + (l.px.splits > 1 ? up64(l.px.splits * M * K) : 0);
     const bool split = l.pw.splits > 1;
     l.o_b = l.o_w + (split ? up64(static_cast<long long>(l.pw.splits) * N * K) : 0);
     l.total = l.o_b + (split ? up64(static_cast<long long>(l.pw.splits) * N) : 0);
-    const Source wide = p->out_dtype == SRNL_F32 ? FP32 : BF16;
-    l.sz = p->act == SRNL_ACT_NONE ? wide : wide == FP32 ? SLOPE_FP32 : SLOPE_BF16;
-    l.sw = p->w_dtype == SRNL_F32 ? FP32 : BF16;
-    l.sx = p->x_dtype == SRNL_F32 ? FP32 : BF16;
-    l.narrow = narrow_bwd_parts(M, K, N, l.sz, l.sw, l.sx);
+    l.narrow_z = act ? slope : sy;
+    l.narrow = narrow_bwd_parts(M, K, N, l.narrow_z, l.sw, l.sx);
     if (l.narrow) {
         l.o_nb = up64(static_cast<long long>(l.narrow) * N * K);
         const long long all = l.o_nb + up64(static_cast<long long>(l.narrow) * N);
@@ -820,8 +875,7 @@ srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N, const srnl
     g.R = K;
     g.e = {out, p->out_dtype == SRNL_BF16, p->bias, p->act, p->residual,
            p->residual_dtype == SRNL_BF16, pre};
-    const bool af = p->x_dtype == SRNL_F32, bf = p->w_dtype == SRNL_F32;
-    const bool al = pieces_ok(K, N);
+    const Source sx = source_of(p->x_dtype, K), sw = source_of(p->w_dtype, K);
     // The few-rows kernel where 64 x 16 pieces of the output are no more than
     // the CUs, in the smallest pieces for which that holds. Measured (us, few
     // rows / 64 x 64 tiles): 49 x 2048 -> 512 bf16 5.9 / 11.7, 512 x 512 -> 512
@@ -830,15 +884,15 @@ srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N, const srnl
     if (cdiv(M, 64) * g.tj <= 256) {
         const int mi = cdiv(M, 16) * g.tj <= 256 ? 1 : cdiv(M, 32) * g.tj <= 256 ? 2 : 4;
         const unsigned grid = static_cast<unsigned>(cdiv(M, 16 * mi) * g.tj);
-        if (af && bf) launch_few<true, true>(g, al, mi, grid, st);
-        else if (af) launch_few<true, false>(g, al, mi, grid, st);
-        else if (bf) launch_few<false, true>(g, al, mi, grid, st);
-        else launch_few<false, false>(g, al, mi, grid, st);
+        if (sx == FP32 && sw == FP32) launch_few<true, true>(g, mi, grid, st);
+        else if (sx == FP32) launch_few<true, false>(g, mi, grid, st);
+        else if (sw == FP32) launch_few<false, true>(g, mi, grid, st);
+        else launch_few<false, false>(g, mi, grid, st);
         return launched("linear_few_kernel");
     }
-    const Plan plan = plan_tile(FORWARD, M, N, K, af, bf, al);
+    const Plan plan = plan_tile(FORWARD, M, N, K, sx, sw);
     take_plan(g, plan);
-    return run_tile<FORWARD>(g, plan, af, bf, st);
+    return run_tile<FORWARD>(g, plan, sx, sw, st);
 }
 
 size_t srnl_linear_bwd_workspace_bytes(long long M, int K, int N, const srnl_linear_params *p)
@@ -889,8 +943,9 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
         const Epilogue ex = {dx, xb, nullptr, SRNL_ACT_NONE, dx_add, xb, nullptr};
         float *const nb = db ? ws + l.o_nb : nullptr;
         const NarrowArgs g = {oz, ow, ox, M, K, N, ex, ws, nb};
-        switch (l.sz) {
-        case BF16: s = narrow_launch<BF16>(g, l.narrow, l.sw, l.sx, st); break;
+        switch (l.narrow_z) {
+        case BF16:
+        case BF16_ANY: s = narrow_launch<BF16>(g, l.narrow, l.sw, l.sx, st); break;
         case FP32: s = narrow_launch<FP32>(g, l.narrow, l.sw, l.sx, st); break;
         case SLOPE_BF16: s = narrow_launch<SLOPE_BF16>(g, l.narrow, l.sw, l.sx, st); break;
         case SLOPE_FP32: s = narrow_launch<SLOPE_FP32>(g, l.narrow, l.sw, l.sx, st); break;
@@ -899,7 +954,6 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
                                    make_join(nb, db ? l.narrow : 1, N, eb), st) : s;
     }
     const void *dz = dout;
-    bool zf = p->out_dtype == SRNL_F32;
     if (act && !l.fused) {
         const long long n = M * N, blocks = cdiv(n, 2048);
         hipLaunchKernelGGL(act_slope_kernel, dim3(static_cast<unsigned>(blocks < 16384 ? blocks : 16384)),
@@ -908,17 +962,16 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
         if (s != SRNL_OK)
             return s;
         dz = ws;
-        zf = true;
     }
-    const bool wf = p->w_dtype == SRNL_F32, xf = p->x_dtype == SRNL_F32;
+    const bool xb = p->x_dtype == SRNL_BF16;
     TileArgs gx = {}, gw = {};
     gx.a = {dz, N, M, pre, p->act};
     gx.b = {p->w, K, K, nullptr, 0};
     gx.R = N;
     gx.e.out = dx;
-    gx.e.obf = !xf;
+    gx.e.obf = xb;
     gx.e.add = dx_add;
-    gx.e.abf = !xf;
+    gx.e.abf = xb;
     gx.part = l.px.splits > 1 ? ws + l.o_x : nullptr;
     take_plan(gx, l.px);
     gw.a = {dz, N, N, pre, p->act};
@@ -932,12 +985,11 @@ srnl_status srnl_linear_bwd(const void *dout, const void *x, long long M, int K,
     const bool bigx = dx && l.px.bi >= 128, bigw = dw && l.pw.bi >= 128;
     const unsigned nx = dx && !bigx ? blocks_of(l.px) : 0, nw = dw && !bigw ? blocks_of(l.pw) : 0;
     if (bigx)
-        s = run_tile<GRAD_X>(gx, l.px, zf, wf, st);
+        s = run_tile<GRAD_X>(gx, l.px, l.sz, l.sw, st);
     if (s == SRNL_OK && bigw)
-        s = run_tile<GRAD_W>(gw, l.pw, zf, xf, st);
-    if (s == SRNL_OK && nx + nw) {
-        s = run_grads({gx, gw, nx, nw, wf, xf, l.px.aligned}, l.fused ? l.sz : zf ? FP32 : BF16, st);
-    }
+        s = run_tile<GRAD_W>(gw, l.pw, l.sz, l.sx, st);
+    if (s == SRNL_OK && nx + nw)
+        s = run_grads({gx, gw, nx, nw, l.sz, l.sw, l.sx}, st);
     if (s != SRNL_OK)
         return s;
     return join(make_join(gx.part, dx ? l.px.splits : 1, M * K, gx.e),
