@@ -663,10 +663,20 @@ struct Plan {
 
 // Tile and split of out[I][J] over R. 256 x 256 (bf16 operands) or 128 x 128
 // tiles where they give every CU one, else 64 x 64: 16384 x 2048 -> 2048 bf16
-// takes 156 us in the largest and 182 us in 128 x 128, whose waves read twice
-// the LDS bytes a product (31 and 23 bytes a cycle and wave). The reduction is split where the tiles leave CUs idle
-// (the weight gradient over many tokens; an input gradient of few rows), as
-// long as a split keeps a few staged steps.
+// takes 148 us in the largest and 182 us in 128 x 128, whose waves read twice
+// the LDS bytes a product (31 and 23 bytes a cycle and wave).
+//
+// A gradient's reduction is split where the tiles leave CUs idle (the weight
+// gradient over many tokens; an input gradient of few rows):
+// - to two blocks a CU for tiles of 128 (backward of 10496 x 1472 -> 440 fp32
+//   240 us at one block, 214 at two, 227 at three) of at least four steps;
+// - to one block a CU for tiles of 64, of at least two steps, and to two where
+//   each keeps eight steps, since one block mostly waits for its loads (backward
+//   of 14560 x 1776 -> 74, fp32 with bf16 weights: 145 and 106 us; but 1003 x
+//   333 -> 777 fp32, 13 steps: 23.5 and 27);
+// - not at all where the whole reduction takes about as long as the launch that
+//   joins the parts: three steps of converted operands (640 x 16 -> 50 fp32 split
+//   19.5, whole 10.7 us), ten of bf16 ones (439 x 854 -> 707 split 14.5, whole 11.8).
 Plan plan_tile(Form f, long long I, long long J, long long R, Source sa, Source sb)
 {
     Plan p;
@@ -679,10 +689,15 @@ Plan plan_tile(Form f, long long I, long long J, long long R, Source sa, Source 
     p.tj = cdiv(J, p.bi);
     const int step = p.bi >= 128 ? bk : 2 * bk;
     const long long tiles = p.ti * p.tj;
-    // ten steps take about as long as the launch that joins a split
-    long long s = f == FORWARD || tiles >= 256 || R <= 10 * step ? 1 : 256 / tiles;
-    const long long most = cdiv(R, (p.bi >= 128 ? 4 : 2) * step);
-    s = s < most ? s : most;
+    auto split = [&](long long blocks, long long steps) {
+        const long long s = blocks / tiles, most = cdiv(R, steps * step);
+        return s < most ? s : most;
+    };
+    long long s = 1;
+    if (f != FORWARD && R > (bk == 64 ? 10 : 3) * step) {
+        const long long one = split(256, 2), two = split(512, 8);
+        s = p.bi >= 128 ? split(512, 4) : one > two ? one : two;
+    }
     s = s < 1 ? 1 : s;
     p.slice = cdiv(cdiv(R, s), step) * step;
     p.splits = static_cast<int>(cdiv(R, p.slice));
