@@ -149,20 +149,19 @@ struct Epilogue {
     float *pre;            // [I][J] or NULL: z before the activation
 };
 
-// eight neighbouring outputs (i, j .. j + 7) from their sums; n are inside. WHOLE: the
-// rows are whole pieces, so that n is 8 or nothing
+// Eight neighbouring outputs from their sums z, o their place; n are inside.
+// WHOLE: the rows are whole pieces, so that n is 8 or nothing. The bias is in
+// registers: a load between the stores of two pieces would wait for the first
+// piece's stores.
 template <bool WHOLE>
-__device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, int n, float (&v)[8])
+__device__ __forceinline__ void finish_piece(const Epilogue &e, long long o, int n, float (&v)[8],
+                                             const float (&bias)[8])
 {
     if (n <= 0)
         return;
-    if (e.bias) {
-        float b[8];
-        load_row<8, WHOLE>(e.bias, false, j, n, b);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] += b[k];
-    }
+    for (int k = 0; k < 8; ++k)
+        v[k] += bias[k];
     if (e.pre)
         store_row<8, WHOLE>(e.pre, false, o, n, v);
     act_values(v, e.act);
@@ -174,6 +173,23 @@ __device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, i
             v[k] += a[k];
     }
     store_row<8, WHOLE>(e.out, e.obf, o, n, v);
+}
+// the bias of outputs j .. j + 7, zeros without one
+template <bool WHOLE>
+__device__ __forceinline__ void load_bias(const Epilogue &e, int j, int n, float (&b)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        b[k] = 0.0f;
+    if (e.bias)
+        load_row<8, WHOLE>(e.bias, false, j, n, b);
+}
+// the two together, for a thread with one piece
+__device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, int n, float (&v)[8])
+{
+    float b[8];
+    load_bias<false>(e, j, n, b);
+    finish_piece<false>(e, o, n, v, b);
 }
 
 constexpr long long cdiv(long long a, long long b) { return (a + b - 1) / b; }

@@ -416,6 +416,16 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
         e = Epilogue{};
         e.out = g.part + sp * g.a.rows * g.b.rows;
     }
+    constexpr int LPR = 4 * FJ, RPQ = 64 / LPR, NQ = 32 / RPQ;  // lanes per row; rows a pass, passes
+    const long long oj = j0 + wj + 8 * (lane % LPR), left = g.b.rows - oj;
+    const int cols = left < 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
+    const bool whole = g.b.rows % 8 == 0;
+    float bias[8];
+    if (whole)
+        load_bias<true>(e, static_cast<int>(oj), cols, bias);
+    else
+        load_bias<false>(e, static_cast<int>(oj), cols, bias);
+    const long long oi0 = i0 + wi + lane / LPR;
 #pragma unroll
     for (int i = 0; i < FI; ++i) {
 #pragma unroll
@@ -425,20 +435,17 @@ __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint
                 st[(8 * (k / 4) + 4 * (lane >> 5) + k % 4) * OUTP + 32 * j + (lane & 31)] = acc[i][j][k];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        constexpr int LPR = 4 * FJ;                             // lanes per row
 #pragma unroll 2
-        for (int q = 0; q < 32 * LPR / 64; ++q) {
-            const int row = q * (64 / LPR) + lane / LPR, c = 8 * (lane % LPR);
+        for (int q = 0; q < NQ; ++q) {
             float v[8];
-            load_f32<8, true>(st + row * OUTP + c, v);
-            const long long oi = i0 + wi + 32 * i + row;
-            const long long oj = j0 + wj + c;
-            const long long left = g.b.rows - oj;
-            const int n = oi >= g.a.rows || left <= 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
-            if (g.b.rows % 8 == 0)
-                finish8<true>(e, oi * g.b.rows + oj, static_cast<int>(oj), n, v);
-            else
-                finish8<false>(e, oi * g.b.rows + oj, static_cast<int>(oj), n, v);
+            load_f32<8, true>(st + (RPQ * q + lane / LPR) * OUTP + 8 * (lane % LPR), v);
+            const long long oi = oi0 + 32 * i + RPQ * q, o = oi * g.b.rows + oj;
+            const int n = oi < g.a.rows ? cols : 0;
+            if (whole) {
+                finish_piece<true>(e, o, n, v, bias);
+            } else {
+                finish_piece<false>(e, o, n, v, bias);
+            }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -534,7 +541,7 @@ __device__ __forceinline__ void join_block(const Join &j, long long block)
                 v[k] += top[e * outs + 8 * piece + k];
         }
     }
-    finish8<false>(j.e, o, 0, m, v);
+    finish8(j.e, o, 0, m, v);
 }
 
 // the input gradient's, the weight gradient's and the bias gradient's partial
@@ -669,8 +676,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
             v[k] += t[k];
     }
     const long long left = g.b.rows - (j0 + c);
-    finish8<false>(g.e, (i0 + row) * g.b.rows + j0 + c, static_cast<int>(j0 + c),
-                   left < 8 ? static_cast<int>(left) : 8, v);
+    finish8(g.e, (i0 + row) * g.b.rows + j0 + c, static_cast<int>(j0 + c),
+            left < 8 ? static_cast<int>(left) : 8, v);
 }
 
 // ------------------------------------------------------------ host
@@ -686,7 +693,7 @@ struct Plan {
 
 // Tile and split of out[I][J] over R. 256 x 256 (bf16 operands) or 128 x 128
 // tiles where they give every CU one, else 64 x 64: 16384 x 2048 -> 2048 bf16
-// takes 148 us in the largest and 182 us in 128 x 128, whose waves read twice
+// takes 145 us in the largest and 182 us in 128 x 128, whose waves read twice
 // the LDS bytes a product (31 and 23 bytes a cycle and wave).
 //
 // A gradient's reduction is split where the tiles leave CUs idle (the weight
