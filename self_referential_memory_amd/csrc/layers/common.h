@@ -223,28 +223,31 @@ __global__ __launch_bounds__(1024) static void sum_rows_kernel(const float *__re
 {
     __shared__ float s[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const long long c = static_cast<long long>(blockIdx.x) * 32 + tx;
-    float a = 0.0f;
-    if (c < cols) {
+    for (long long c0 = 32LL * blockIdx.x; c0 < cols; c0 += 32LL * gridDim.x) {
+        const long long c = c0 + tx;
+        float a = 0.0f;
+        if (c < cols) {
 #pragma unroll 8
-        for (int p = ty; p < rows; p += 32)
-            a += part[p * ld + c];
-    }
-    s[ty][tx] = a;
-    __syncthreads();
-    // the thread's column is its row of the transposed read
-    float v = s[tx][ty];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        v += __shfl_xor(v, off);
-    const long long cc = static_cast<long long>(blockIdx.x) * 32 + ty;
-    if (tx == 0 && cc < cols) {
-        if (cc < n0) {
-            if (out0)
-                out0[cc] = v;
-        } else if (out1) {
-            out1[cc - n0] = v;
+            for (int p = ty; p < rows; p += 32)
+                a += part[p * ld + c];
         }
+        s[ty][tx] = a;
+        __syncthreads();
+        // the thread's column is its row of the transposed read
+        float v = s[tx][ty];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            v += __shfl_xor(v, off);
+        const long long cc = c0 + ty;
+        if (tx == 0 && cc < cols) {
+            if (cc < n0) {
+                if (out0)
+                    out0[cc] = v;
+            } else if (out1) {
+                out1[cc - n0] = v;
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -266,7 +269,8 @@ inline srnl_status zero_fill(float *p, long long n, hipStream_t st)
 inline srnl_status sum_rows(const float *part, int rows, long long ld, long long cols, long long n0,
                             float *out0, float *out1, hipStream_t st)
 {
-    hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), dim3(1024), 0, st,
+    const long long blocks = (cols + 31) / 32;
+    hipLaunchKernelGGL(sum_rows_kernel, dim3(static_cast<unsigned>(blocks < 65536 ? blocks : 65536)), dim3(1024), 0, st,
                        part, rows, ld, cols, n0, out0, out1);
     return launched("sum_rows_kernel");
 }

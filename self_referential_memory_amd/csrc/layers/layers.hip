@@ -10,10 +10,11 @@ using namespace srnl_i;
 #include "norm.inc"
 #include "dwconv.inc"
 
-// rows x C elements of at most 4 bytes within the address range
+// rows x C elements of at most 4 bytes within the address range, a row's (and
+// its two gradients') channels within an int
 bool norm_sizes_ok(long long rows, int C)
 {
-    return static_cast<__int128>(rows) * C < (static_cast<__int128>(1) << 60);
+    return C <= 1 << 30 && static_cast<__int128>(rows) * C < (static_cast<__int128>(1) << 60);
 }
 
 srnl_status check_norm(long long rows, int C, srnl_dtype a, srnl_dtype b)

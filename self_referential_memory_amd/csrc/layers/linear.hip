@@ -893,7 +893,7 @@ srnl_status check_linear(long long M, int K, int N, const srnl_linear_params *p)
         return fail(SRNL_ERR_ARG, "unknown activation");
     const long long wide = K > N ? K : N;
     if (static_cast<__int128>(M) * wide >= (static_cast<__int128>(1) << 58) ||
-        cdiv(M, 16) * cdiv(wide, 16) > 0x7FFFFFFF || cdiv(K, 16) * cdiv(N, 16) > 0xFFFFFF)
+        cdiv(M, 128) * cdiv(wide, 128) > 0xFFFFFF || cdiv(K, 16) * cdiv(N, 16) > 0xFFFFFF)    // launches of 2^32 threads
         return fail(SRNL_ERR_ARG, "sizes too large");
     if (!valid_dtype(p->x_dtype) || !valid_dtype(p->w_dtype) || !valid_dtype(p->out_dtype) ||
         (p->residual && !valid_dtype(p->residual_dtype)))

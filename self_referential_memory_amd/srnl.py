@@ -673,7 +673,7 @@ def layer_norm_fwd(x: torch.Tensor, gain: Optional[torch.Tensor], bias: Optional
         if stats:
             mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
             rstd = torch.empty_like(mean)
-        _check(lib().srnl_layer_norm_fwd(_ptr(x), x.numel() // C, C, dtx, _ptr(gain), _ptr(bias),
+        _check(lib().srnl_layer_norm_fwd(_ptr(x), x.numel() // max(C, 1), C, dtx, _ptr(gain), _ptr(bias),
                                          eps, dto, _ptr(out), _ptr(mean), _ptr(rstd),
                                          _stream(stream)), "srnl_layer_norm_fwd")
     return (out, mean, rstd) if stats else out
@@ -692,7 +692,7 @@ def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gain: Optional[torch.Ten
     _expect(dx_add, x.shape, None, "dx_add")
     for t, name in ((mean, "mean"), (rstd, "rstd")):
         _expect(t, x.shape[:-1], torch.float32, name)
-    rows = x.numel() // C
+    rows = x.numel() // max(C, 1)
     dtx, dto = _dtype_code(x), _dtype_code(dout)
     dta = 0 if dx_add is None else _dtype_code(dx_add)
     with _on(x, dout, gain, mean, rstd, dx_add):
@@ -740,7 +740,7 @@ def linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
         pre = torch.empty(shape, dtype=torch.float32, device=x.device) if keep_pre else None
         p = LinearParams(_ptr(w), _ptr(bias), _ptr(residual), _dtype_code(x), _dtype_code(w), dtr,
                          _dtype_code(out), code, _stream(stream))
-        _check(lib().srnl_linear_fwd(_ptr(x), x.numel() // K, K, N, ctypes.byref(p), _ptr(out),
+        _check(lib().srnl_linear_fwd(_ptr(x), x.numel() // max(K, 1), K, N, ctypes.byref(p), _ptr(out),
                                      _ptr(pre)), "srnl_linear_fwd")
     return (out, pre) if keep_pre else out
 
@@ -767,7 +767,7 @@ def linear_bwd(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
     _expect(pre, shape, torch.float32, "pre")
     if need_db and not need_dw:
         raise ValueError("need_db needs need_dw: the bias gradient is formed with the weight's")
-    M = x.numel() // K
+    M = x.numel() // max(K, 1)
     with _on(x, dout, w, pre, dx_add):
         sh = _stream(stream)
         p = LinearParams(_ptr(w), None, None, _dtype_code(x), _dtype_code(w), 0,
@@ -831,6 +831,13 @@ def dwconv_bwd(dout: torch.Tensor, u: torch.Tensor, w: torch.Tensor, *,
 
 # ---- the layers as autograd nodes (on the current stream)
 
+def _dense(dout: torch.Tensor) -> torch.Tensor:
+    """An incoming gradient as the entry points take it: contiguous, from a
+    16-byte boundary (a slice of a larger gradient may start anywhere)."""
+    dout = dout.contiguous()
+    return dout.clone() if dout.data_ptr() % 16 else dout
+
+
 def _wants_grad(*tensors: Optional[torch.Tensor]) -> bool:
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
@@ -849,7 +856,7 @@ class LayerNorm(torch.autograd.Function):
     def backward(ctx, dout):
         x, gain, mean, rstd = ctx.saved_tensors
         need = ctx.needs_input_grad
-        dx, dgain, dbias = layer_norm_bwd(dout.contiguous(), x, gain, mean, rstd,
+        dx, dgain, dbias = layer_norm_bwd(_dense(dout), x, gain, mean, rstd,
                                           param_grads=need[1] or need[2])
         return dx, dgain if need[1] else None, dbias if need[2] else None, None, None
 
@@ -884,7 +891,7 @@ class Linear(torch.autograd.Function):
         need = ctx.needs_input_grad
         dx = dw = db = None
         if any(need[:3]):
-            dx, dw, db = linear_bwd(dout.contiguous(), x, w, pre, act=act, need_dx=need[0],
+            dx, dw, db = linear_bwd(_dense(dout), x, w, pre, act=act, need_dx=need[0],
                                     need_dw=need[1] or need[2], need_db=need[2])
         dw = dw.to(w.dtype) if need[1] else None
         dres = dout.to(res_dtype) if need[3] else None
@@ -915,7 +922,7 @@ class DWConv(torch.autograd.Function):
         need = ctx.needs_input_grad
         du = dw = db = None
         if any(need[:3]):
-            du, dw, db = dwconv_bwd(dout.contiguous(), u, w, need_du=need[0],
+            du, dw, db = dwconv_bwd(_dense(dout), u, w, need_du=need[0],
                                     param_grads=need[1] or need[2])
         adds = [dout.to(t) if n else None for n, t in zip(need[3:5], ctx.add_dtypes)]
         return (du, dw if need[1] else None, db if need[2] else None, *adds, None)
@@ -961,7 +968,7 @@ class Block(torch.autograd.Function):
         x, states, scales, u, m1, r1, q, y, rec, h, m2, r2, v, a, z, *weights = ctx.saved_tensors
         ln1_w, ln1_b, wq, dw_w, dw_b, ln2_w, ln2_b, w1, b1, w2, b2 = weights
         heads, d, route_mask, kw = ctx.cfg
-        dout = dout.contiguous()
+        dout = _dense(dout)
         da, gw2, gb2 = linear_bwd(dout, a, w2)
         dv, gw1, gb1 = linear_bwd(da, v, w1, z, act=ACT_GELU)
         dh, gl2w, gl2b = layer_norm_bwd(dv, h, ln2_w, m2, r2, dx_add=dout)

@@ -135,6 +135,32 @@ def test_layers_as_autograd_nodes():
     assert b.grad is not None
 
 
+def test_gradients_from_any_address():
+    """A joined output's gradient comes back in slices that may start at any
+    element."""
+    x = torch.randn(3, 5, device=DEV, requires_grad=True)
+    w = torch.randn(7, 5, device=DEV, requires_grad=True)
+    g = torch.randn(7, device=DEV, requires_grad=True)
+    u = torch.randn(1, 1, 3, 7, device=DEV, requires_grad=True)
+    cw = torch.randn(7, 3, 3, device=DEV, requires_grad=True)
+    leaves = (x, w, g, u, cw)
+    seed = torch.randn(10, 7, device=DEV)
+    parts = [torch.zeros(1, 7, device=DEV), srnl.linear(x, w), srnl.layer_norm(x @ w.t(), g, None),
+             srnl.dwconv(u, cw).view(3, 7)]
+    got = torch.autograd.grad(torch.cat(parts), leaves, seed)
+    want = [torch.zeros_like(t) for t in leaves]
+    for p, a, b in ((parts[1], 1, 4), (parts[2], 4, 7), (parts[3], 7, 10)):
+        p = srnl.linear(x, w) if a == 1 else srnl.layer_norm(x @ w.t(), g, None) if a == 4 \
+            else srnl.dwconv(u, cw).view(3, 7)
+        for t, v in zip(want, torch.autograd.grad(p, leaves, seed[a:b].clone(), allow_unused=True)):
+            if v is not None:
+                t += v
+    # the same terms (below 100) in another order: three additions, each off by
+    # 2^-24 of a sum below 200
+    for a, b in zip(got, want):
+        assert (a - b).abs().max() <= 3 * 200 * 2.0 ** -24
+
+
 def test_layers_on_a_side_stream():
     """Inputs made on the current stream, calls on another one that waits for
     it: the workspaces the binding frees on return are not handed out again

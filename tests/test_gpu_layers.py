@@ -341,3 +341,38 @@ def test_dwconv_no_cells():
     assert srnl.dwconv_fwd(u, w, None).shape == u.shape
     du, dw, db = srnl.dwconv_bwd(u, u, w)
     assert du.shape == u.shape and not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("M,K,N", [(66773, 64, 64), (1003, 333, 777), (1003, 336, 776), (20, 40, 64)])
+def test_linear_bwd_infinite_last_row(M, K, N):
+    """An infinity in the last row of bf16 inputs makes its own column of the
+    weight gradient infinite and nothing else: rows past the last count as
+    nothing, in whichever kernel."""
+    x = torch.ones(M, K, device=DEV, dtype=BF16)
+    x[-1, 5] = float("inf")
+    w = torch.ones(N, K, device=DEV, dtype=BF16)
+    dout = torch.ones(M, N, device=DEV, dtype=BF16)
+    dx, dw, db = srnl.linear_bwd(dout, x, w)
+    assert torch.isposinf(dw[:, 5]).all()
+    dw[:, 5] = M
+    assert (dw == M).all() and (db == M).all() and (dx == N).all()
+
+
+def test_dwconv_bwd_very_many_channels():
+    """More channels than one launch has columns for in the joining kernel."""
+    C = 13_500_000
+    u = torch.randn(1, 1, 1, C, device=DEV)
+    dy = torch.randn(1, 1, 1, C, device=DEV)
+    w = torch.ones(C, 3, 3, device=DEV)
+    du, dw, db = srnl.dwconv_bwd(dy, u, w)
+    assert torch.equal(du, dy) and torch.equal(db, dy.view(-1))
+    assert torch.equal(dw[:, 1, 1], (u * dy).view(-1))
+    dw[:, 1, 1] = 0
+    assert not dw.any()
+
+
+def test_layers_refuse_empty_rows():
+    with pytest.raises(srnl.SrnlError):
+        srnl.layer_norm_fwd(torch.empty(3, 0, device=DEV), None, None)
+    with pytest.raises(srnl.SrnlError):
+        srnl.linear_fwd(torch.empty(3, 0, device=DEV), torch.empty(4, 0, device=DEV))

@@ -17,6 +17,7 @@ def norm_fwd(x=0, rows=2, C=8, i=0, o=0, eps=1e-5):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), ARG), (dict(C=0), ARG), (dict(C=-8), ARG), (dict(rows=1 << 62, C=1 << 20), ARG),
+    (dict(C=(1 << 30) + 8), ARG), (dict(C=(1 << 31) - 1), ARG),
     (dict(eps=0.0), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG),
     (dict(eps=float("inf")), ARG), (dict(i=2), DTYPE), (dict(o=-1), DTYPE), (dict(), PTR),
     (dict(x=24), PTR), (dict(rows=0), OK)])
@@ -49,6 +50,7 @@ def linear(fn, M=2, K=8, N=8, act=0, types=(0, 0, 0, 0), res=None, params=True, 
 @pytest.mark.parametrize("kw,status", [
     (dict(params=False), PTR), (dict(M=-1), ARG), (dict(K=0), ARG), (dict(N=-4), ARG),
     (dict(act=3), ARG), (dict(act=-1), ARG), (dict(M=1 << 60), ARG), (dict(M=1 << 40, N=4096), ARG),
+    (dict(M=1 << 31, K=1, N=1), ARG),
     (dict(types=(2, 0, 0, 0)), DTYPE), (dict(types=(0, 7, 0, 0)), DTYPE),
     (dict(types=(0, 0, 0, -1)), DTYPE), (dict(types=(0, 0, 4, 0), res=16), DTYPE), (dict(M=0), OK)])
 def test_linear_errors(fn, kw, status):
