@@ -457,7 +457,8 @@ typedef struct {
  *   x [M][K]; out [M][N] in out_dtype; pre [M][N] fp32: z, written unless
  *   NULL (the backward pass of an activation reads it).
  * Products are exact for bf16 operands and within 2^-26 of each term for
- * fp32 ones, summed in fp32. Rows with an infinite fp32 operand (or one that
+ * fp32 ones, summed in fp32; an fp32 operand below 2^-108 counts to within
+ * 2^-134 (half the smallest bf16 number). Rows with an infinite fp32 operand (or one that
  * bf16 rounds to infinity, above 3.39e38) come out NaN.
  * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_HIP.
  */

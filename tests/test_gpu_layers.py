@@ -376,3 +376,18 @@ def test_layers_refuse_empty_rows():
         srnl.layer_norm_fwd(torch.empty(3, 0, device=DEV), None, None)
     with pytest.raises(srnl.SrnlError):
         srnl.linear_fwd(torch.empty(3, 0, device=DEV), torch.empty(4, 0, device=DEV))
+
+
+@pytest.mark.parametrize("M", [4, 3000])
+@pytest.mark.parametrize("e", [-100, -112, -126, -140])
+def test_linear_tiny_fp32_operands(M, e):
+    """fp32 operands near the bottom of the range: each product to 2^-26 of
+    itself or 2^-134 of the other operand, the 64 summed in fp32 (at most 64
+    roundings of a sum of positive terms, and the output's)."""
+    g = torch.Generator().manual_seed(e * e + M)
+    x = ((torch.rand(M, 64, generator=g) + 1).double() * 2.0 ** e).float().to(DEV)
+    w = ((torch.rand(96, 64, generator=g) + 1) * 2.0 ** min(120, -e)).to(DEV)
+    y = srnl.linear_fwd(x, w)
+    want = x.double() @ w.double().t()
+    bound = want * (2.0 ** -26 + 65 * 2.0 ** -24) + 2.0 ** -134 * w.double().sum(1)
+    assert ((y.double() - want).abs() <= bound).all()
