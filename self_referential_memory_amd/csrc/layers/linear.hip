@@ -589,69 +589,125 @@ srnl_status join(const Join &a, const Join &b, const Join &c, hipStream_t st)
 
 // ------------------------------------------------------------ few rows
 
-// 16 MI rows by 16 columns of the output per block; its eight waves take the
-// reduction 32 indices at a time in turn, straight from memory into MFMA operands
+// 16 MI x 16 MJ outputs per block; its eight waves take the reduction 32 indices
+// at a time in turn, straight from memory into MFMA operands
 // (v_mfma_f32_16x16x32_bf16), and join through LDS in wave order. Bound by the
-// latency of one round of loads: 1 x 512 -> 2048 bf16 gelu 4.0 us, 49 x 2048 ->
-// 512 6.6 us, where an empty launch takes 3.
+// latency of a round or two of loads (1 x 512 -> 2048 bf16 gelu 3.4 us, 49 x 2048
+// -> 512 6.3 us, where an empty launch takes 3), for wide weights by memory
+// (1 x 4096 -> 16384 bf16 24 us, 5.6 TB/s).
 constexpr int kFewWaves = 8;
 
-template <bool F32>
-__device__ __forceinline__ void few_load(const Operand &o, long long row, long long r, long long R,
-                                         u32x4 (&w)[3])
-{
-    const long long left = R - r;
-    const int n = row >= o.rows || left <= 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
-    const long long at = row * o.ld + r;
-    if constexpr (F32) {
-        float v[8];
-        load_row<8, false>(o.p, false, at, n, v);
-        split_parts(v, w);
-    } else {
-        w[0] = u32x4{0, 0, 0, 0};
-        const uint16_t *src = static_cast<const uint16_t *>(o.p) + at;
-        if (n == 8) {
-            __builtin_memcpy(&w[0], src, 16);
-        } else if (n > 0) {
-            uint16_t t[8];
+// Eight reduction indices from k on of an operand's row, as they lie in memory.
+template <bool F32> struct FewPiece {
+    u32x4 w[F32 ? 2 : 1];
+    // Without a condition, so that a round's loads leave together: rows past the
+    // last take the last (their outputs are not stored), and what lies past the
+    // operand's last eight elements is loaded by mend().
+    __device__ __forceinline__ void load(const Operand &o, long long row, long long k, long long total)
+    {
+        row = row < o.rows ? row : o.rows - 1;
+        const long long at = row * o.ld + k, last = total < 8 ? 0 : total - 8;
+        const uintptr_t p = total < 8 ? reinterpret_cast<uintptr_t>(zero_piece) : reinterpret_cast<uintptr_t>(o.p);
+        const __attribute__((address_space(1))) char *src = reinterpret_cast<const __attribute__((address_space(1))) char *>(p);
+        __builtin_memcpy(w, src + (at < last ? at : last) * (F32 ? 4 : 2), sizeof w);
+    }
+    // where the piece may reach past the reduction's end R
+    __device__ __forceinline__ void mend(const Operand &o, long long row, long long k, long long R, long long total)
+    {
+        row = row < o.rows ? row : o.rows - 1;
+        const int n = R - k < 8 ? static_cast<int>(R - k < 0 ? 0 : R - k) : 8;
+        const long long at = row * o.ld + k;
+        uint32_t e[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                t[e] = src[e < n ? e : 0];
+        for (int i = 0; i < 8; ++i)
+            e[i] = F32 ? w[F32 ? i / 4 : 0][i % 4] : w[0][i / 2] >> (16 * (i & 1)) & 0xFFFFu;
+        if (n > 0 && at > total - 8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[0][e] = (2 * e < n ? t[2 * e] : 0u) | (2 * e + 1 < n ? static_cast<uint32_t>(t[2 * e + 1]) << 16 : 0u);
+            for (int i = 0; i < 8; ++i) {
+                const long long x = i < n ? at + i : at;
+                e[i] = F32 ? static_cast<const uint32_t *>(o.p)[x] : static_cast<const uint16_t *>(o.p)[x];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            e[i] = i < n ? e[i] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+                w[0][i] = e[i];
+                w[1][i] = e[4 + i];
+            } else {
+                w[0][i] = e[2 * i] | e[2 * i + 1] << 16;
+            }
         }
     }
-}
+    __device__ __forceinline__ void parts(u32x4 (&p)[3]) const
+    {
+        if constexpr (F32) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = __uint_as_float(w[i / 4][i % 4]);
+            split_parts(v, p);
+        } else {
+            p[0] = w[0];
+        }
+    }
+};
 
-template <bool AF, bool BF, int MI>
+template <bool AF, bool BF, int MI, int MJ>
 __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
 {
     constexpr int PA = AF ? 3 : 1, PB = BF ? 3 : 1;
-    constexpr int P = 20;                                       // floats per staged row of 16
+    constexpr int P = 16 * MJ + 4;                              // floats per staged row
     __shared__ __align__(16) float red[kFewWaves][16 * MI * P];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, rl = lane & 15, g8 = 8 * (lane >> 4);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, rl = lane & 15, g8 = 8 * (lane >> 4);
     const int tj = blockIdx.x % g.tj;
-    const long long i0 = static_cast<long long>(blockIdx.x / g.tj) * 16 * MI, j0 = 16LL * tj;
-    v4f acc[MI];
+    const long long i0 = static_cast<long long>(blockIdx.x / g.tj) * 16 * MI, j0 = 16LL * MJ * tj;
+    const long long na = g.a.rows * g.R, nb = g.b.rows * g.R;
+    v4f acc[MI][MJ];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
-        acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    constexpr int U = MI == 1 ? 4 : 2;                          // pieces in flight
-    for (long long r = 32LL * wave; r < g.R; r += 32LL * U * kFewWaves) {
-        u32x4 wb[U][3], wa[U][MI][3];
+#pragma unroll
+        for (int j = 0; j < MJ; ++j)
+            acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    constexpr int U = 2;                                        // pieces in flight
+    constexpr long long ROUND = 32LL * U * kFewWaves;
+    for (long long r = 32LL * wave; r < g.R; r += ROUND) {
+        FewPiece<BF> wb[U][MJ];
+        FewPiece<AF> wa[U][MI];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const long long k = r + 32LL * kFewWaves * u + g8;
-            few_load<BF>(g.b, j0 + rl, k, g.R, wb[u]);
+#pragma unroll
+            for (int j = 0; j < MJ; ++j)
+                wb[u][j].load(g.b, j0 + 16 * j + rl, k, nb);
 #pragma unroll
             for (int i = 0; i < MI; ++i)
-                few_load<AF>(g.a, i0 + 16 * i + rl, k, g.R, wa[u][i]);
+                wa[u][i].load(g.a, i0 + 16 * i + rl, k, na);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            const long long k0 = r + 32LL * kFewWaves * u, k = k0 + g8;
+            if (k0 >= g.R)
+                break;
+            if (k0 + 32 > g.R) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+                for (int j = 0; j < MJ; ++j)
+                    wb[u][j].mend(g.b, j0 + 16 * j + rl, k, g.R, nb);
+#pragma unroll
+                for (int i = 0; i < MI; ++i)
+                    wa[u][i].mend(g.a, i0 + 16 * i + rl, k, g.R, na);
+            }
+            u32x4 pb[MJ][3];
+#pragma unroll
+            for (int j = 0; j < MJ; ++j)
+                wb[u][j].parts(pb[j]);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                u32x4 pa[3];
+                wa[u][i].parts(pa);
 #pragma unroll
                 for (int s = 2; s >= 0; --s)
 #pragma unroll
@@ -659,18 +715,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void linear_few_kernel(TileArgs g)
                         const int q = s - p;
                         if (q < 0 || q >= PB)
                             continue;
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, wa[u][i][p]), __builtin_bit_cast(bf16x8, wb[u][q]),
-                            acc[i], 0, 0, 0);
+#pragma unroll
+                        for (int j = 0; j < MJ; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                __builtin_bit_cast(bf16x8, pa[p]), __builtin_bit_cast(bf16x8, pb[j][q]),
+                                acc[i][j], 0, 0, 0);
                     }
+            }
+        }
     }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            red[wave][(16 * i + 4 * (lane >> 4) + k) * P + rl] = acc[i][k];
+        for (int j = 0; j < MJ; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                red[wave][(16 * i + 4 * (lane >> 4) + k) * P + 16 * j + rl] = acc[i][j][k];
     __syncthreads();
-    const int row = threadIdx.x >> 1, c = 8 * (threadIdx.x & 1);
+    const int row = threadIdx.x / (2 * MJ), c = 8 * (threadIdx.x % (2 * MJ));
     if (row >= 16 * MI || i0 + row >= g.a.rows)
         return;
     float v[8];
@@ -824,15 +886,56 @@ srnl_status run_grads(const GradsLaunch &l, hipStream_t st)
     return launched("linear_grads_kernel");
 }
 
-template <bool AF, bool BF> void launch_few(const TileArgs &g, int mi, unsigned grid, hipStream_t st)
+struct FewShape {
+    int mi, mj;            // 16 mi x 16 mj outputs a block; 0: not for the few-rows kernel
+};
+
+// The few-rows kernel takes a product of which every CU gets at most one block,
+// in the smallest blocks for which that holds. Its blocks are longer along the
+// bf16 operand, so that less of an fp32 one is split twice; the largest only
+// pay where an operand is split and the reduction is no short one. A product of
+// up to 32 rows goes there whatever its columns. Measured (us, few rows / tiles;
+// x, w fp32, then bf16): 49 x 2048 -> 512 10.0 / 51 and 6.3 / 12.4; 512 x 512 ->
+// 512 7.2 / 15.3 and 4.8 / 5.6; 672 x 864 -> 512 14.3 / 24.4, with bf16 w 8.9 /
+// 16.8, but all bf16 6.3 / 7.7; 128 x 1024 -> 4096 16.0 / 30.3, all bf16 8.9 /
+// 8.3; 300 x 64 -> 1024 5.5 / 4.8; 1 x 1024 -> 8192 7.4 / 28.9 and 5.1 / 7.6;
+// past it 1003 x 333 -> 777 15.5 / 13.6 and 16.9 / 8.8.
+FewShape few_shape(long long M, long long N, long long R, bool xf, bool wf)
 {
-    const dim3 block(64 * kFewWaves);
-    if (mi == 1)
-        hipLaunchKernelGGL((linear_few_kernel<AF, BF, 1>), dim3(grid), block, 0, st, g);
-    else if (mi == 2)
-        hipLaunchKernelGGL((linear_few_kernel<AF, BF, 2>), dim3(grid), block, 0, st, g);
-    else
-        hipLaunchKernelGGL((linear_few_kernel<AF, BF, 4>), dim3(grid), block, 0, st, g);
+    const bool wide = (xf && !wf) || M <= 16;
+    auto fits = [&](int mi, int mj) { return cdiv(M, 16 * mi) * cdiv(N, 16 * mj) <= 256; };
+    if (fits(1, 1))
+        return {1, 1};
+    if (wide ? fits(1, 2) : fits(2, 1))
+        return wide ? FewShape{1, 2} : FewShape{2, 1};
+    const bool few = M <= 32 && N <= 1 << 26;                  // and a launch below 2^32 threads
+    if (fits(2, 2) || (few && M > 16))
+        return {2, 2};
+    if (few)
+        return {1, 2};
+    if ((xf || wf) && R >= 256 && (wide ? fits(2, 4) : fits(4, 2)))
+        return wide ? FewShape{2, 4} : FewShape{4, 2};
+    return {0, 0};
+}
+
+template <bool AF, bool BF> void launch_few(TileArgs g, FewShape f, hipStream_t st)
+{
+    g.tj = static_cast<int>(cdiv(g.b.rows, 16 * f.mj));
+    const dim3 grid(static_cast<unsigned>(cdiv(g.a.rows, 16 * f.mi) * g.tj)), block(64 * kFewWaves);
+#define FEW(MI, MJ) hipLaunchKernelGGL((linear_few_kernel<AF, BF, MI, MJ>), grid, block, 0, st, g)
+    if (f.mi == 1 && f.mj == 1)
+        FEW(1, 1);
+    else if (f.mi == 1)
+        FEW(1, 2);
+    else if (f.mj == 1)
+        FEW(2, 1);
+    else if (f.mi == 2 && f.mj == 2)
+        FEW(2, 2);
+    else if constexpr (AF && !BF)
+        FEW(2, 4);
+    else if constexpr (BF)
+        FEW(4, 2);
+#undef FEW
 }
 
 // what an operand with rows of n elements is, for the tiled kernels
@@ -929,18 +1032,11 @@ srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N, const srnl
     g.e = {out, p->out_dtype == SRNL_BF16, p->bias, p->act, p->residual,
            p->residual_dtype == SRNL_BF16, pre};
     const Source sx = source_of(p->x_dtype, K), sw = source_of(p->w_dtype, K);
-    // The few-rows kernel where 64 x 16 pieces of the output are no more than
-    // the CUs, in the smallest pieces for which that holds. Measured (us, few
-    // rows / 64 x 64 tiles): 49 x 2048 -> 512 bf16 5.9 / 11.7, 512 x 512 -> 512
-    // bf16 5.0 / 5.4, fp32 8.2 / 13.6; past it 1000 x 336 -> 776 bf16 6.3 / 5.0.
-    g.tj = static_cast<int>(cdiv(N, 16));
-    if (cdiv(M, 64) * g.tj <= 256) {
-        const int mi = cdiv(M, 16) * g.tj <= 256 ? 1 : cdiv(M, 32) * g.tj <= 256 ? 2 : 4;
-        const unsigned grid = static_cast<unsigned>(cdiv(M, 16 * mi) * g.tj);
-        if (sx == FP32 && sw == FP32) launch_few<true, true>(g, mi, grid, st);
-        else if (sx == FP32) launch_few<true, false>(g, mi, grid, st);
-        else if (sw == FP32) launch_few<false, true>(g, mi, grid, st);
-        else launch_few<false, false>(g, mi, grid, st);
+    if (const FewShape f = few_shape(M, N, K, sx == FP32, sw == FP32); f.mi) {
+        if (sx == FP32 && sw == FP32) launch_few<true, true>(g, f, st);
+        else if (sx == FP32) launch_few<true, false>(g, f, st);
+        else if (sw == FP32) launch_few<false, true>(g, f, st);
+        else launch_few<false, false>(g, f, st);
         return launched("linear_few_kernel");
     }
     const Plan plan = plan_tile(FORWARD, M, N, K, sx, sw);

@@ -391,3 +391,12 @@ def test_linear_tiny_fp32_operands(M, e):
     want = x.double() @ w.double().t()
     bound = want * (2.0 ** -26 + 65 * 2.0 ** -24) + 2.0 ** -134 * w.double().sum(1)
     assert ((y.double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("types", [t for t in TYPES if t[2] == F32])
+@pytest.mark.parametrize("M,K,N", [(1, 3, 2), (7, 1, 1), (5, 37, 8201), (16, 264, 4200), (30, 100, 8200), (100, 333, 517),
+                                   (260, 40, 400), (640, 261, 515), (300, 600, 1100), (40, 517, 5000)])
+def test_linear_few_rows_in_blocks_of_each_shape(M, K, N, types):
+    """Blocks of 16 x 16 to 64 x 32 and 32 x 64 outputs, reductions that end
+    inside a piece, rows that end inside a block, operands shorter than a piece."""
+    check_linear(M, K, N, *types, act="silu", res=F32, seed=3)
