@@ -764,7 +764,11 @@ struct Plan {
 // Tile and split of out[I][J] over R. 256 x 256 (bf16 operands) or 128 x 128
 // tiles where they give every CU one, else 64 x 64: 16384 x 2048 -> 2048 bf16
 // takes 147 us in the largest and 182 us in 128 x 128, whose waves read twice
-// the LDS bytes a product (31 and 23 bytes a cycle and wave).
+// the LDS bytes a product (31 and 23 bytes a cycle and wave). A weight
+// gradient's reduction is long enough to fill the card with parts of 128 x 128
+// tiles; where these are a quarter empty, at twice the parts (backward, fp32:
+// 14560 x 1776 -> 74, 797 parts, with bf16 weights 111 us in tiles of 64 and 92
+// in 128; 4626 x 93 -> 1863, 285 parts, 60 and 67).
 //
 // A gradient's reduction is split where the tiles leave CUs idle (the weight
 // gradient over many tokens; an input gradient of few rows):
@@ -782,7 +786,8 @@ Plan plan_tile(Form f, long long I, long long J, long long R, Source sa, Source 
     Plan p;
     const int bk = is_bf16(sa) && is_bf16(sb) ? 64 : 32;
     const long long big = cdiv(I, 128) * cdiv(J, 128);
-    p.bi = (big >= 256 || (f == GRAD_W && big * cdiv(R, 8 * bk) >= 256 && I >= 96 && J >= 96)) ? 128 : 64;
+    const long long side = I < J ? I : J, parts = big * cdiv(R, 8 * bk);
+    p.bi = big >= 256 || (f == GRAD_W && side > 64 && parts >= (side >= 96 ? 256 : 512)) ? 128 : 64;
     if (sa == BF16 && sb == BF16 && f != GRAD_W && cdiv(I, 256) * cdiv(J, 256) >= 256 && R >= 256)
         p.bi = 256;
     p.ti = cdiv(I, p.bi);
