@@ -764,7 +764,11 @@ struct Plan {
 // Tile and split of out[I][J] over R. 256 x 256 (bf16 operands) or 128 x 128
 // tiles where they give every CU one, else 64 x 64: 16384 x 2048 -> 2048 bf16
 // takes 147 us in the largest and 182 us in 128 x 128, whose waves read twice
-// the LDS bytes a product (31 and 23 bytes a cycle and wave). A weight
+// the LDS bytes a product (31 and 23 bytes a cycle and wave). An input gradient
+// of a short reduction shares a launch with the weight gradient in tiles of 64,
+// which is worth more than the larger tiles up to one and a half a CU (backward
+// of 6272 x 768 -> 256 bf16, 294 tiles, 25.3 us in tiles of 64 and 29.2 in 128;
+// 12544 x 768 -> 192, 588 tiles, 45.3 and 41.6). A weight
 // gradient's reduction is long enough to fill the card with parts of 128 x 128
 // tiles; where these are a quarter empty, at twice the parts (backward, fp32:
 // 14560 x 1776 -> 74, 797 parts, with bf16 weights 111 us in tiles of 64 and 92
@@ -787,7 +791,7 @@ Plan plan_tile(Form f, long long I, long long J, long long R, Source sa, Source 
     const int bk = is_bf16(sa) && is_bf16(sb) ? 64 : 32;
     const long long big = cdiv(I, 128) * cdiv(J, 128);
     const long long side = I < J ? I : J, parts = big * cdiv(R, 8 * bk);
-    p.bi = big >= 256 || (f == GRAD_W && side > 64 && parts >= (side >= 96 ? 256 : 512)) ? 128 : 64;
+    p.bi = big >= (f == GRAD_X && R <= 256 ? 384 : 256) || (f == GRAD_W && side > 64 && parts >= (side >= 96 ? 256 : 512)) ? 128 : 64;
     if (sa == BF16 && sb == BF16 && f != GRAD_W && cdiv(I, 256) * cdiv(J, 256) >= 256 && R >= 256)
         p.bi = 256;
     p.ti = cdiv(I, p.bi);
