@@ -647,9 +647,13 @@ def _workspace(nbytes: int, device) -> Optional[torch.Tensor]:
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
-def _new(out: Optional[torch.Tensor], shape, dtype, device, name: str = "out") -> torch.Tensor:
+def _new(out: Optional[torch.Tensor], shape, dtype, device, name: str = "out",
+         like: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The caller's output, or a new one; like: an input of the same shape
+    (contiguous, as _ptr sees to), from which it is made in less host time."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return (torch.empty(shape, dtype=dtype, device=device) if like is None
+                else torch.empty_like(like, dtype=dtype))
     _expect(out, shape, dtype, name)
     if out.device != device:
         raise ValueError(f"{name} is on {out.device}, expected {device}")
@@ -667,7 +671,7 @@ def layer_norm_fwd(x: torch.Tensor, gain: Optional[torch.Tensor], bias: Optional
         _expect(t, (C,), torch.float32, name)
     dtx = _dtype_code(x)
     with _on(x, gain, bias):
-        out = _new(out, x.shape, x.dtype if out_dtype is None else out_dtype, x.device)
+        out = _new(out, x.shape, x.dtype if out_dtype is None else out_dtype, x.device, like=x)
         dto = _dtype_code(out)
         mean = rstd = None
         if stats:
@@ -696,7 +700,7 @@ def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gain: Optional[torch.Ten
     dtx, dto = _dtype_code(x), _dtype_code(dout)
     dta = 0 if dx_add is None else _dtype_code(dx_add)
     with _on(x, dout, gain, mean, rstd, dx_add):
-        dx = _new(dx, x.shape, x.dtype, x.device, "dx")
+        dx = _new(dx, x.shape, x.dtype, x.device, "dx", x)
         dgain = dbias = ws = None
         if param_grads:
             dgain = torch.empty(C, dtype=torch.float32, device=x.device)
@@ -772,8 +776,8 @@ def linear_bwd(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
         sh = _stream(stream)
         p = LinearParams(_ptr(w), None, None, _dtype_code(x), _dtype_code(w), 0,
                          _dtype_code(dout), code, sh)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
-        dw = torch.empty((N, K), dtype=torch.float32, device=x.device) if need_dw else None
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(w, dtype=torch.float32) if need_dw else None
         db = torch.empty(N, dtype=torch.float32, device=x.device) if need_db else None
         ws = _workspace(lib().srnl_linear_bwd_workspace_bytes(M, K, N, ctypes.byref(p)), x.device)
         _check(lib().srnl_linear_bwd(_ptr(dout), _ptr(x), M, K, N, ctypes.byref(p), _ptr(pre),
@@ -796,7 +800,7 @@ def dwconv_fwd(u: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
         _expect(t, u.shape, None, name)
     codes = [0 if t is None else _dtype_code(t) for t in (add1, add2)]
     with _on(u, w, bias, add1, add2):
-        out = _new(out, u.shape, u.dtype if out_dtype is None else out_dtype, u.device)
+        out = _new(out, u.shape, u.dtype if out_dtype is None else out_dtype, u.device, like=u)
         _check(lib().srnl_dwconv_fwd(_ptr(u), B, H, W, C, _dtype_code(u), _ptr(w), _ptr(bias),
                                      _ptr(add1), codes[0], _ptr(add2), codes[1], _dtype_code(out),
                                      _ptr(out), _stream(stream)), "srnl_dwconv_fwd")
@@ -814,10 +818,10 @@ def dwconv_bwd(dout: torch.Tensor, u: torch.Tensor, w: torch.Tensor, *,
     _expect(dout, u.shape, None, "dout")
     _expect(du_add, u.shape, u.dtype, "du_add")
     with _on(u, dout, w, du_add):
-        du = torch.empty(u.shape, dtype=u.dtype, device=u.device) if need_du else None
+        du = torch.empty_like(u) if need_du else None
         dw = db = ws = None
         if param_grads:
-            dw = torch.empty((C, 3, 3), dtype=torch.float32, device=u.device)
+            dw = torch.empty_like(w)
             db = torch.empty(C, dtype=torch.float32, device=u.device)
             ws = _workspace(lib().srnl_dwconv_bwd_workspace_bytes(B, H, W, C), u.device)
         sh = _stream(stream)
