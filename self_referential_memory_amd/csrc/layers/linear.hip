@@ -40,8 +40,9 @@ __global__ __launch_bounds__(256) void act_slope_kernel(const void *__restrict__
     }
 }
 
-// 16 bytes that lanes read in place of pieces outside an operand
-__device__ __align__(16) const uint32_t zero_piece[4] = {0, 0, 0, 0};
+// What lanes read in place of pieces outside an operand: 16 bytes in the tiled
+// kernels, the 32 of eight fp32 values in the few-rows kernel.
+__device__ __align__(16) const uint32_t zero_piece[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
 // A tile of ROWS x BK of an operand, staged in LDS as PARTS planes of bf16.
 // RC: plane[row][BK], 16-byte pieces of a row permuted so that 16 consecutive
@@ -605,6 +606,7 @@ template <bool F32> struct FewPiece {
     // operand's last eight elements is loaded by mend().
     __device__ __forceinline__ void load(const Operand &o, long long row, long long k, long long total)
     {
+        static_assert(sizeof w <= sizeof zero_piece, "a whole piece is read in place of a short operand");
         row = row < o.rows ? row : o.rows - 1;
         const long long at = row * o.ld + k, last = total < 8 ? 0 : total - 8;
         const uintptr_t p = total < 8 ? reinterpret_cast<uintptr_t>(zero_piece) : reinterpret_cast<uintptr_t>(o.p);
