@@ -300,9 +300,9 @@ template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ> struct TileC
 // tile t of g, in lds of TileCfg::LDS words. Long reductions are bound by the
 // LDS reads behind the MFMAs (16384 x 2048 -> 2048 bf16: 147 us, 0.94 PFLOP/s),
 // short ones by memory and the epilogue's arithmetic (200704 x 64 -> 256 fp32,
-// gelu: 68 us, 3.7 TB/s; vector instructions issue 60% of the time, 18 of 33 a
-// value for gelu), small ones by the latency of their steps (1003 x 333 -> 777
-// fp32: 17 us for six steps).
+// gelu: 73 us, 3.5 TB/s; 24 of a value's 39 vector issue slots are gelu's),
+// small ones by the latency of their steps (1003 x 333 -> 777 fp32: 17 us for
+// six steps).
 template <Source SA, Source SB, bool RCA, bool RCB, int BI, int BJ, bool SUMS>
 __device__ __forceinline__ void tile_product(const TileArgs &g, unsigned t, uint16_t *lds)
 {

@@ -1,10 +1,11 @@
 """The layers' corners, against their formulas in float64: operands shorter
-than one wide load. Bounds as derived in test_gpu_layers.py."""
+than one wide load, activations over their whole range. Bounds as derived in
+test_gpu_layers.py; an activation's are given with its test."""
 import pytest
 import torch
 
 from self_referential_memory_amd import srnl
-from test_gpu_layers import BF16, F32, U, rnd, say, within
+from test_gpu_layers import BF16, DEV, F32, U, act_ref, rnd, say, slope_ref, within
 
 pytestmark = pytest.mark.gpu
 
@@ -20,3 +21,89 @@ def test_linear_operands_shorter_than_a_load(x_t, w_t):
         X, W = x.double(), w.double()
         within(srnl.linear_fwd(x, w, b, out_dtype=F32), X @ W.t() + b.double(),
                2 * (K + 8) * U * (X.abs() @ W.abs().t() + b.double().abs()), f"{M} {K} {N}")
+
+
+# ------------------------------------------------------------- activations
+
+def tail_error(z):
+    """Relative error of q = 1 - Phi(|z|) = exp(-z^2/2) P(s), s = |z| / (|z| + 3).
+
+    P: the polynomial's own error, then Horner's seven fused steps (7 u times
+    the sum of its terms' magnitudes over P, at most 2 + 6 |z|) and s, which
+    is off by 4 u (reciprocal 2 u, sum and product u each) and enters 5.3
+    times at most. exp: the argument z^2/2 is off by 3 u of itself (its
+    constant and two products), the instruction 2 u; the last product u."""
+    a = z.abs()
+    fit = torch.where(a < 3, 1.8e-7, torch.where(a < 5, 1.2e-6, 4.2e-6))
+    return fit + U * (7 * (2 + 6 * a) + 4 * 5.3 + 1.5 * a * a + 3)
+
+
+def act_error(z, act):
+    if act == "silu":       # exp(-z): its argument is off by 1.5 u of itself, exp 2 u; sum, reciprocal, product
+        return ((1.5 * z.abs() + 2) * torch.sigmoid(-z) + 6) * U * act_ref(z, act).abs()
+    q = torch.special.erfc(z.abs() / 2 ** 0.5) / 2
+    return z.abs() * q * tail_error(z) + 2 * U * act_ref(z, act).abs()
+
+
+def slope_error(z, act):
+    s = torch.sigmoid(z)
+    if act == "silu":       # s (1 + z (1 - s)), 1 - s formed from s
+        return s * ((1.5 * z.abs() + 8) * U * (1 + 2 * z.abs()) + 4 * U * (1 + z.abs()))
+    q = torch.special.erfc(z.abs() / 2 ** 0.5) / 2
+    peak = z.abs() * torch.exp(-z * z / 2) / (2 * torch.pi) ** 0.5
+    return q * tail_error(z) + peak * U * (1.5 * z * z + 6) + 2 * U * (slope_ref(z, act).abs() + 1)
+
+
+def sweep(n):
+    """n values over [-13, 13], every second one within 1.5 of zero."""
+    z = torch.linspace(-13, 13, n, dtype=torch.float64)
+    z[::2] = torch.linspace(-1.5, 1.5, len(z[::2]), dtype=torch.float64)
+    return z.float().to(DEV)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("y_t", [F32, BF16])
+@pytest.mark.parametrize("M", [3001, 20001, 60001])
+def test_linear_activation_over_its_range(M, y_t, act):
+    """z passes through the product unchanged (one weight of 1, the rest 0),
+    in the few-rows kernel and both tile sizes; below zero the output keeps
+    its own digits, not only the largest value's."""
+    say("activation", M, y_t, act)
+    z = sweep(M)
+    x, w = torch.zeros(M, 8, device=DEV), torch.zeros(16, 8, device=DEV)
+    x[:, 0], w[:, 0] = z, 1.0
+    y, pre = srnl.linear_fwd(x, w, act=act, out_dtype=y_t, keep_pre=True)
+    assert torch.equal(pre, z[:, None].expand(M, 16))
+    z = z.double()[:, None].expand(M, 16)
+    within(y, act_ref(z, act), act_error(z, act), act)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("y_t", [F32, BF16])
+@pytest.mark.parametrize("M", [500, 9000, 70000])
+def test_linear_slope_over_its_range(M, y_t, act):
+    """dz = act'(z) comes back as dx through a weight of ones on the diagonal:
+    formed while staged (with its own pass, and in the narrow form)."""
+    say("slope", M, y_t, act)
+    N = 8 if M != 9000 else 264                # 264: a pass of its own makes dz
+    z = sweep(M * N).view(M, N)
+    w = torch.eye(N, device=DEV)
+    x = torch.zeros(M, N, device=DEV)
+    dx, dw, db = srnl.linear_bwd(torch.ones(M, N, device=DEV, dtype=y_t), x, w, z, act=act)
+    z = z.double()
+    within(dx, slope_ref(z, act), slope_error(z, act), act)
+    assert not dw.any()
+
+
+def test_linear_activation_of_extremes():
+    """z Phi(z) and z logistic(z) as they are in fp32: +infinity stays, the
+    largest values stay or vanish, -infinity x 0 and NaN are NaN."""
+    v = torch.tensor([float("inf"), -float("inf"), float("nan"), 0.0, -0.0, 3e38, -3e38, 1e-38, -1e-38,
+                      100.0, -100.0, 13.5, -13.5, 15.0, -15.0, 1.0], device=DEV)
+    x, w = torch.zeros(16, 8, device=DEV, dtype=BF16), torch.zeros(16, 8, device=DEV, dtype=BF16)
+    x[:, 0], w[:, 0] = v.to(BF16), 1.0
+    for act in ("gelu", "silu"):
+        y = srnl.linear_fwd(x, w, act=act, out_dtype=F32)[:, 0]
+        z = x[:, 0].double()
+        assert torch.isposinf(y[0]) and torch.isnan(y[1]) and torch.isnan(y[2]), act
+        within(y[3:], act_ref(z[3:], act), act_error(z[3:], act) + 2e-36, act)
