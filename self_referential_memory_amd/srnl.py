@@ -14,6 +14,7 @@ import os
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsrnl.so")
 
@@ -833,7 +834,8 @@ def dwconv_bwd(dout: torch.Tensor, u: torch.Tensor, w: torch.Tensor, *,
     return du, dw, db
 
 
-# ---- the layers as autograd nodes (on the current stream)
+# ---- the layers as autograd nodes (on the current stream; reverse mode, once
+# differentiable: forward-mode tangents and second derivatives raise)
 
 def _dense(dout: torch.Tensor) -> torch.Tensor:
     """An incoming gradient as the entry points take it: contiguous, from a
@@ -842,8 +844,13 @@ def _dense(dout: torch.Tensor) -> torch.Tensor:
     return dout.clone() if dout.data_ptr() % 16 else dout
 
 
-def _wants_grad(*tensors: Optional[torch.Tensor]) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+def _tracked(*tensors: Optional[torch.Tensor]) -> bool:
+    """Whether autograd has to see the call: a gradient is wanted, or a tensor
+    carries a forward-mode tangent (the node has none to give and raises)."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        return True
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 class LayerNorm(torch.autograd.Function):
@@ -868,7 +875,7 @@ class LayerNorm(torch.autograd.Function):
 def layer_norm(x: torch.Tensor, gain: Optional[torch.Tensor], bias: Optional[torch.Tensor],
                eps: float = 1e-5, out_dtype=None) -> torch.Tensor:
     """Differentiable layer norm over the last axis (layer_norm_fwd)."""
-    if not _wants_grad(x, gain, bias):
+    if not _tracked(x, gain, bias):
         return layer_norm_fwd(x, gain, bias, eps, out_dtype=out_dtype)
     return LayerNorm.apply(x, gain, bias, eps, out_dtype)
 
@@ -905,7 +912,7 @@ class Linear(torch.autograd.Function):
 def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *, act="none",
            residual: Optional[torch.Tensor] = None, out_dtype=None) -> torch.Tensor:
     """Differentiable act(x w^T + bias) + residual (linear_fwd)."""
-    if not _wants_grad(x, w, bias, residual):
+    if not _tracked(x, w, bias, residual):
         return linear_fwd(x, w, bias, act=act, residual=residual, out_dtype=out_dtype)
     return Linear.apply(x, w, bias, residual, act, out_dtype)
 
@@ -936,7 +943,7 @@ def dwconv(u: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
            add1: Optional[torch.Tensor] = None, add2: Optional[torch.Tensor] = None, *,
            out_dtype=None) -> torch.Tensor:
     """Differentiable depthwise 3x3 branch with its addends (dwconv_fwd)."""
-    if not _wants_grad(u, w, bias, add1, add2):
+    if not _tracked(u, w, bias, add1, add2):
         return dwconv_fwd(u, w, bias, add1, add2, out_dtype=out_dtype)
     return DWConv.apply(u, w, bias, add1, add2, out_dtype)
 
