@@ -501,8 +501,9 @@ srnl_status srnl_dwconv_fwd(const void *u, int B, int H, int W, int C, srnl_dtyp
 /*
  * srnl_dwconv_bwd -- du (in in_dtype), dw [C][3][3] and db [C] (fp32) of the
  * branch from dout (in out_dtype); any NULL if not wanted. du_add, in
- * in_dtype, or NULL: another gradient of u, added to du. The addends'
- * gradient is dout itself. Workspace (only with dw or db):
+ * in_dtype, or NULL: another gradient of u, added to du. dw sums over pairs of
+ * cells that exist, so an infinity of u or dout reaches only the taps that have
+ * it as a term. The addends' gradient is dout itself. Workspace (only with dw or db):
  * srnl_dwconv_bwd_workspace_bytes.
  * Errors: as the forward, plus SRNL_ERR_WORKSPACE.
  */

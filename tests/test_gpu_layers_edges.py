@@ -107,3 +107,48 @@ def test_linear_activation_of_extremes():
         z = x[:, 0].double()
         assert torch.isposinf(y[0]) and torch.isnan(y[1]) and torch.isnan(y[2]), act
         within(y[3:], act_ref(z[3:], act), act_error(z[3:], act) + 2e-36, act)
+
+
+# ----------------------------------------------------------- depthwise 3x3
+
+def dw_terms(u, w, dy):
+    """du, dw, db and the sums of their terms' magnitudes, over the pairs of
+    cells that exist: no product with a zero in place of a missing cell."""
+    H, W = u.shape[1:3]
+    cut = lambda o, n: (slice(max(0, -o), n - max(0, o)), slice(max(0, o), n + min(0, o)))
+    du, sdu = torch.zeros_like(dy), torch.zeros_like(dy)
+    dw, sdw = torch.zeros_like(w), torch.zeros_like(w)
+    for a in range(3):
+        for e in range(3):
+            (i, si), (j, sj) = cut(a - 1, H), cut(e - 1, W)
+            t = dy[:, i, j] * w[:, a, e]
+            du[:, si, sj] += t
+            sdu[:, si, sj] += t.abs()
+            t = dy[:, i, j] * u[:, si, sj]
+            dw[:, a, e], sdw[:, a, e] = t.sum((0, 1, 2)), t.abs().sum((0, 1, 2))
+    return (du, sdu), (dw, sdw), (dy.sum((0, 1, 2)), dy.abs().sum((0, 1, 2)))
+
+
+@pytest.mark.parametrize("u_t,y_t", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+@pytest.mark.parametrize("B,H,W,C", [(3, 5, 7, 64), (2, 9, 3, 33), (90, 57, 7, 64), (1, 1, 1, 6), (1, 2, 2, 8),
+                                     (600, 11, 5, 24)])
+def test_dwconv_bwd_infinities_stay_with_their_terms(B, H, W, C, u_t, y_t):
+    """An infinity of u or dy in a channel, at the grid's corners and edges and
+    at rows where one block's walk ends: gradients that have it as a term are
+    infinite (NaN for opposite ones), the others are finite and right."""
+    say("dwconv infinities", B, H, W, C, u_t, y_t)
+    g = torch.Generator().manual_seed(B + C)
+    u, w, dy = rnd(1, B, H, W, C, dtype=u_t), rnd(2, C, 3, 3), rnd(3, B, H, W, C, dtype=y_t)
+    rows = [0, H - 1, 0, H - 1, *torch.randint(H, (C,), generator=g).tolist()]
+    cols = [0, W - 1, W // 2, 0, *torch.randint(W, (C,), generator=g).tolist()]
+    for c in range(C):
+        t = (u, dy)[c % 2]
+        t[c % B, rows[c // 2], cols[c // 2], c] = float("-inf" if c % 3 else "inf")
+    (rdu, sdu), (rdw, sdw), (rdb, sdb) = dw_terms(u.double(), w.double(), dy.double())
+    n = B * H * W
+    for got, ref, size, k, what in zip(srnl.dwconv_bwd(dy, u, w), (rdu, rdw, rdb), (sdu, sdw, sdb), (12, n + 8, n + 8),
+                                       ("du", "dw", "db")):
+        fin = torch.isfinite(ref)
+        assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
+        assert torch.equal(got[~fin & ~torch.isnan(ref)].double(), ref[~fin & ~torch.isnan(ref)]), what
+        within(got[fin], ref[fin], k * U * size[fin], what)
