@@ -458,11 +458,15 @@ typedef struct {
  *   NULL (the backward pass of an activation reads it).
  * Products are exact for bf16 operands and within 2^-26 of each term for
  * fp32 ones, summed in fp32; an fp32 operand below 2^-108 counts to within
- * 2^-134 (half the smallest bf16 number). Rows with an infinite fp32 operand (or one that
- * bf16 rounds to infinity, above 3.39e38) come out NaN. An activation is z times
- * Phi(z), or times the logistic function, each with its own digits in the lower
- * tail: GELU is off by at most 6e-7 of itself for |z| <= 2 and 1.5e-5 down to
- * z = -13, where it leaves fp32's range. At z = -infinity it is 0 x infinity, NaN.
+ * 2^-134 (half the smallest bf16 number).
+ * Infinities follow the formula where both operands are bf16. Where one is fp32,
+ * an infinity of either (for an fp32 value: anything above 3.39e38, which bf16
+ * rounds to infinity) gives infinities or NaN in the outputs that have it as a
+ * term: a row of out for x, a column for w. All others are as without it.
+ * An activation is z times Phi(z), or times the logistic function, each with its
+ * own digits in the lower tail: GELU is off by at most 6e-7 of itself for
+ * |z| <= 2 and 1.5e-5 down to z = -13, where it leaves fp32's range. At
+ * z = -infinity it is 0 x infinity, NaN.
  * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_HIP.
  */
 srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N,
@@ -476,6 +480,9 @@ srnl_status srnl_linear_fwd(const void *x, long long M, int K, int N,
  *   dw [N][K], db [N] fp32; any of dx, dw, db NULL if not wanted, db only
  *   together with dw. pre: as the forward wrote it; ignored without an
  *   activation. The residual's gradient is dout itself.
+ * Infinities as in the forward (dz is fp32 where an activation makes it): one of
+ * dz[m][n] reaches row m of dx, row n of dw and db[n], one of x[m][k] column k of
+ * dw, one of w[n][k] column k of dx.
  * Workspace: srnl_linear_bwd_workspace_bytes (may be 0).
  * Errors: as the forward, plus SRNL_ERR_WORKSPACE.
  */

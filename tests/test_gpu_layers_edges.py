@@ -152,3 +152,49 @@ def test_dwconv_bwd_infinities_stay_with_their_terms(B, H, W, C, u_t, y_t):
         assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
         assert torch.equal(got[~fin & ~torch.isnan(ref)].double(), ref[~fin & ~torch.isnan(ref)]), what
         within(got[fin], ref[fin], k * U * size[fin], what)
+
+
+# ----------------------------------------------------- infinities in linear
+
+@pytest.mark.parametrize("types", [(BF16, BF16, BF16), (F32, BF16, F32), (F32, F32, F32), (BF16, F32, F32),
+                                   (BF16, BF16, F32)])
+@pytest.mark.parametrize("M,K,N", [(20, 40, 64), (300, 7, 5), (1003, 333, 777), (9000, 512, 640), (66773, 64, 64)])
+def test_linear_infinities_stay_in_their_rows(M, K, N, types):
+    """Whatever an infinity becomes beside fp32 operands, it touches only the
+    outputs that have it as a term; those are not finite. Every other output
+    is bitwise the one without it."""
+    say("linear infinities", M, K, N, types)
+    x_t, w_t, y_t = types
+    clean = rnd(1, M, K, dtype=x_t), rnd(2, N, K, dtype=w_t), rnd(3, M, N, dtype=y_t)
+    x, w, dy = (t.clone() for t in clean)
+    m, k, n = M - 1, K // 2, N - 2
+
+    def same(got, want, touched, what):
+        assert torch.equal(got[~touched], want[~touched]), what
+        assert not torch.isfinite(got[touched]).any(), what
+
+    def lines(shape, *places):
+        hit = torch.zeros(shape, dtype=torch.bool, device=DEV)
+        for p in places:
+            hit[p] = True
+        return hit
+
+    every = slice(None)
+    y, (dx, dw, db) = srnl.linear_fwd(x, w, out_dtype=y_t), srnl.linear_bwd(dy, x, w)
+    x[m, k] = float("inf")
+    same(srnl.linear_fwd(x, w, out_dtype=y_t), y, lines((M, N), m), "y of x")
+    g = srnl.linear_bwd(dy, x, w)
+    assert torch.equal(g[0], dx) and torch.equal(g[2], db)
+    same(g[1], dw, lines((N, K), (every, k)), "dw of x")
+    x = clean[0]
+    w[n, k] = float("-inf")
+    same(srnl.linear_fwd(x, w, out_dtype=y_t), y, lines((M, N), (every, n)), "y of w")
+    g = srnl.linear_bwd(dy, x, w)
+    assert torch.equal(g[1], dw) and torch.equal(g[2], db)
+    same(g[0], dx, lines((M, K), (every, k)), "dx of w")
+    w = clean[1]
+    dy[m, n] = float("inf")
+    g = srnl.linear_bwd(dy, x, w)
+    same(g[0], dx, lines((M, K), m), "dx of dy")
+    same(g[1], dw, lines((N, K), n), "dw of dy")
+    same(g[2], db, lines((N,), n), "db of dy")
