@@ -4,6 +4,7 @@
 #define SRNL_LAYERS_LINEAR_H
 
 #include "common.h"
+#include "plan.h"
 
 namespace srnl_i {
 
@@ -109,13 +110,6 @@ struct Operand {
     int act;
 };
 
-// What an operand is made of: bf16 words (in rows of whole 16-byte pieces, or
-// in rows of any length), fp32 values, or dy act'(z) formed while it is staged,
-// with dy in bf16 or fp32. The card takes wide loads at any element's address;
-// only the direct loads into LDS ask for whole pieces.
-enum Source { BF16, BF16_ANY, FP32, SLOPE_BF16, SLOPE_FP32 };
-constexpr bool is_bf16(Source s) { return s == BF16 || s == BF16_ANY; }
-
 // Barrier for LDS alone: __syncthreads() would also wait for every load from
 // memory that is in flight, prefetched registers among them.
 __device__ __forceinline__ void lds_barrier()
@@ -179,8 +173,6 @@ __device__ __forceinline__ void finish8(const Epilogue &e, long long o, int j, i
     load_bias<false>(e, j, n, b);
     finish_piece<false>(e, o, n, v, b);
 }
-
-constexpr long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 }  // namespace srnl_i
 
