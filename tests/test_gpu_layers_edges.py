@@ -1,6 +1,8 @@
 """The layers' corners, against their formulas in float64: operands shorter
 than one wide load, activations over their whole range. Bounds as derived in
 test_gpu_layers.py; an activation's are given with its test."""
+import ctypes
+
 import pytest
 import torch
 
@@ -198,3 +200,72 @@ def test_linear_infinities_stay_in_their_rows(M, K, N, types):
     same(g[0], dx, lines((M, K), m), "dx of dy")
     same(g[1], dw, lines((N, K), n), "dw of dy")
     same(g[2], db, lines((N,), n), "db of dy")
+
+
+# ------------------------------------------------------------------ in place
+
+def abi_linear_bwd(dout, x, w, add, dx):
+    """srnl_linear_bwd with dx at a given address (the binding makes its own)."""
+    L, (N, K), M = srnl.lib(), w.shape, x.shape[0]
+    p = srnl.LinearParams(w.data_ptr(), None, None, srnl._dtype_code(x), srnl._dtype_code(w), 0,
+                          srnl._dtype_code(dout), 0, torch.cuda.current_stream().cuda_stream)
+    dw, db = torch.empty(N, K, device=DEV), torch.empty(N, device=DEV)
+    ws = torch.empty(max(16, L.srnl_linear_bwd_workspace_bytes(M, K, N, ctypes.byref(p))), dtype=torch.uint8,
+                     device=DEV)
+    assert L.srnl_linear_bwd(dout.data_ptr(), x.data_ptr(), M, K, N, ctypes.byref(p), None, add.data_ptr(),
+                             dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel()) == 0
+    return dw, db
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("C", [5, 8, 12, 65, 513, 777, 1100, 2500, 4096, 4097])
+def test_norm_backward_in_place(C, t):
+    """dx over dx_add: lanes that share channels (rows that are not whole
+    pieces), also of different waves, add the gradient once."""
+    say("norm in place", C, t)
+    x, dout, gain, add = rnd(1, 700, C, dtype=t), rnd(2, 700, C), rnd(3, C), rnd(4, 700, C, dtype=t)
+    _, mean, rstd = srnl.layer_norm_fwd(x, gain, None, stats=True)
+    want = srnl.layer_norm_bwd(dout, x, gain, mean, rstd, dx_add=add)
+    here = add.clone()
+    got = srnl.layer_norm_bwd(dout, x, gain, mean, rstd, dx_add=here, dx=here)
+    assert got[0] is here and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("M,K,N", [(3, 40, 24), (100, 333, 517), (700, 72, 523), (5200, 64, 1000), (8200, 264, 2056),
+                                   (40, 2000, 64), (70000, 64, 40)])
+def test_linear_in_place(M, K, N, t):
+    """out over the residual, dx over dx_add: few rows, every tile, a split
+    input gradient and the narrow form."""
+    say("linear in place", M, K, N, t)
+    x, w, r = rnd(1, M, K, dtype=t), rnd(2, N, K, dtype=t), rnd(3, M, N, dtype=t)
+    want = srnl.linear_fwd(x, w, act="silu", residual=r)
+    here = r.clone()
+    assert srnl.linear_fwd(x, w, act="silu", residual=here, out=here) is here
+    assert torch.equal(here, want)
+    add = rnd(4, M, K, dtype=t)
+    want = srnl.linear_bwd(r, x, w, dx_add=add)
+    dw, db = abi_linear_bwd(r, x, w, add, add)
+    assert all(torch.equal(a, b) for a, b in zip((add, dw, db), want))
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+@pytest.mark.parametrize("B,H,W,C", [(3, 9, 7, 64), (2, 5, 6, 33), (90, 57, 7, 16)])
+def test_dwconv_in_place(B, H, W, C, t):
+    """out over either addend, du over du_add."""
+    say("dwconv in place", B, H, W, C, t)
+    u, w, a, b = rnd(1, B, H, W, C, dtype=t), rnd(2, C, 3, 3), rnd(3, B, H, W, C, dtype=t), rnd(4, B, H, W, C)
+    want = srnl.dwconv_fwd(u, w, None, a, b)
+    here = a.clone()
+    assert srnl.dwconv_fwd(u, w, None, here, b, out=here) is here and torch.equal(here, want)
+    want = srnl.dwconv_fwd(u, w, None, b, a)
+    here = a.clone()
+    assert torch.equal(srnl.dwconv_fwd(u, w, None, b, here, out=here), want)
+    want = srnl.dwconv_bwd(b, u, w, du_add=a)
+    L, here = srnl.lib(), a.clone()
+    dw, db = torch.empty_like(w), torch.empty(C, device=DEV)
+    ws = torch.empty(L.srnl_dwconv_bwd_workspace_bytes(B, H, W, C), dtype=torch.uint8, device=DEV)
+    assert L.srnl_dwconv_bwd(b.data_ptr(), 0, u.data_ptr(), B, H, W, C, srnl._dtype_code(u), w.data_ptr(),
+                             here.data_ptr(), here.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
+                             ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+    assert all(torch.equal(p, q) for p, q in zip((here, dw, db), want))
