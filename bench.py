@@ -80,8 +80,9 @@ def algorithmic_bytes(wl, R: int) -> dict:
 
 
 def src_sha() -> str:
-    """sha256 prefix of the library's kernel sources: every file of csrc/ in
-    name order, concatenated."""
+    """sha256 prefix of the operator's kernel sources, which the counters are
+    taken on: every .hip and .inc file of csrc/ itself in name order,
+    concatenated (the layers' units in csrc/layers/ are not among them)."""
     d = os.path.dirname(SRC)
     h = hashlib.sha256()
     for f in sorted(os.listdir(d)):

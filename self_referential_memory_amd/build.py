@@ -8,7 +8,6 @@ import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "srnl.hip")
 # translation units, compiled side by side and linked into the one library
 UNITS = [os.path.join(PKG, "csrc", "layers", f)
          for f in ("operator_unit.hip", "linear.hip", "narrow_bf16.hip", "narrow_fp32.hip",
