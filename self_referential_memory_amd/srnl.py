@@ -182,9 +182,13 @@ def _state_shape(heads: int, d: int):
     return (4, heads, 3 * d * d + 2 * d)
 
 
-def _stream(stream) -> int:
+def _stream(stream, x: Optional[torch.Tensor] = None) -> int:
+    """The handle of stream (None: the current device's current one), which
+    must be of x's device."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if x is not None and stream.device_index != x.get_device():
+        raise ValueError(f"stream of cuda:{stream.device_index}, tensors on {x.device}")
     return stream.cuda_stream
 
 
@@ -680,7 +684,7 @@ def layer_norm_fwd(x: torch.Tensor, gain: Optional[torch.Tensor], bias: Optional
             rstd = torch.empty_like(mean)
         _check(lib().srnl_layer_norm_fwd(_ptr(x), x.numel() // max(C, 1), C, dtx, _ptr(gain), _ptr(bias),
                                          eps, dto, _ptr(out), _ptr(mean), _ptr(rstd),
-                                         _stream(stream)), "srnl_layer_norm_fwd")
+                                         _stream(stream, x)), "srnl_layer_norm_fwd")
     return (out, mean, rstd) if stats else out
 
 
@@ -707,7 +711,7 @@ def layer_norm_bwd(dout: torch.Tensor, x: torch.Tensor, gain: Optional[torch.Ten
             dgain = torch.empty(C, dtype=torch.float32, device=x.device)
             dbias = torch.empty_like(dgain)
             ws = _workspace(lib().srnl_layer_norm_bwd_workspace_bytes(rows, C), x.device)
-        sh = _stream(stream)
+        sh = _stream(stream, x)
         _check(lib().srnl_layer_norm_bwd(
             _ptr(dout), dto, _ptr(x), rows, C, dtx, _ptr(gain), _ptr(mean), _ptr(rstd),
             _ptr(dx_add), dta, _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(ws),
@@ -744,7 +748,7 @@ def linear_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
         out = _new(out, shape, x.dtype if out_dtype is None else out_dtype, x.device)
         pre = torch.empty(shape, dtype=torch.float32, device=x.device) if keep_pre else None
         p = LinearParams(_ptr(w), _ptr(bias), _ptr(residual), _dtype_code(x), _dtype_code(w), dtr,
-                         _dtype_code(out), code, _stream(stream))
+                         _dtype_code(out), code, _stream(stream, x))
         _check(lib().srnl_linear_fwd(_ptr(x), x.numel() // max(K, 1), K, N, ctypes.byref(p), _ptr(out),
                                      _ptr(pre)), "srnl_linear_fwd")
     return (out, pre) if keep_pre else out
@@ -774,7 +778,7 @@ def linear_bwd(dout: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
         raise ValueError("need_db needs need_dw: the bias gradient is formed with the weight's")
     M = x.numel() // max(K, 1)
     with _on(x, dout, w, pre, dx_add):
-        sh = _stream(stream)
+        sh = _stream(stream, x)
         p = LinearParams(_ptr(w), None, None, _dtype_code(x), _dtype_code(w), 0,
                          _dtype_code(dout), code, sh)
         dx = torch.empty_like(x) if need_dx else None
@@ -804,7 +808,7 @@ def dwconv_fwd(u: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = 
         out = _new(out, u.shape, u.dtype if out_dtype is None else out_dtype, u.device, like=u)
         _check(lib().srnl_dwconv_fwd(_ptr(u), B, H, W, C, _dtype_code(u), _ptr(w), _ptr(bias),
                                      _ptr(add1), codes[0], _ptr(add2), codes[1], _dtype_code(out),
-                                     _ptr(out), _stream(stream)), "srnl_dwconv_fwd")
+                                     _ptr(out), _stream(stream, u)), "srnl_dwconv_fwd")
     return out
 
 
@@ -825,7 +829,7 @@ def dwconv_bwd(dout: torch.Tensor, u: torch.Tensor, w: torch.Tensor, *,
             dw = torch.empty_like(w)
             db = torch.empty(C, dtype=torch.float32, device=u.device)
             ws = _workspace(lib().srnl_dwconv_bwd_workspace_bytes(B, H, W, C), u.device)
-        sh = _stream(stream)
+        sh = _stream(stream, u)
         _check(lib().srnl_dwconv_bwd(_ptr(dout), _dtype_code(dout), _ptr(u), B, H, W, C,
                                      _dtype_code(u), _ptr(w), _ptr(du_add), _ptr(du), _ptr(dw),
                                      _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(), sh),

@@ -269,3 +269,18 @@ def test_dwconv_in_place(B, H, W, C, t):
                              here.data_ptr(), here.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(),
                              ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
     assert all(torch.equal(p, q) for p, q in zip((here, dw, db), want))
+
+
+def test_streams_of_another_device_are_refused():
+    class Other:                       # what the binding reads of a torch stream
+        cuda_stream, device_index = 0, 5
+
+    x, w, g = rnd(1, 4, 8), rnd(2, 16, 8), rnd(3, 8)
+    u, cw = rnd(4, 1, 2, 2, 8), rnd(5, 8, 3, 3)
+    s = torch.zeros(4, device=DEV)
+    for call in (lambda **k: srnl.layer_norm_fwd(x, g, g, **k), lambda **k: srnl.layer_norm_bwd(x, x, g, s, s, **k),
+                 lambda **k: srnl.linear_fwd(x, w, **k), lambda **k: srnl.linear_bwd(rnd(6, 4, 16), x, w, **k),
+                 lambda **k: srnl.dwconv_fwd(u, cw, **k), lambda **k: srnl.dwconv_bwd(u, u, cw, **k)):
+        with pytest.raises(ValueError, match="stream of cuda:5"):
+            call(stream=Other)
+        call(stream=torch.cuda.current_stream())
