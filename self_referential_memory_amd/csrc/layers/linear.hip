@@ -594,9 +594,10 @@ srnl_status join(const Join &a, const Join &b, const Join &c, hipStream_t st)
 // 16 MI x 16 MJ outputs per block; its eight waves take the reduction 32 indices
 // at a time in turn, straight from memory into MFMA operands
 // (v_mfma_f32_16x16x32_bf16), and join through LDS in wave order. Bound by the
-// latency of a round or two of loads (1 x 512 -> 2048 bf16 gelu 3.4 us, 49 x 2048
-// -> 512 6.3 us, where an empty launch takes 3), for wide weights by memory
-// (1 x 4096 -> 16384 bf16 24 us, 5.6 TB/s).
+// latency of its rounds of loads, 512 indices each, one after the other (1 x 512
+// -> 2048 bf16 gelu, one round, 4.0 us; 49 x 2048 -> 512, four rounds on 128 CUs,
+// 6.7 us; an empty launch takes 3), for wide weights by memory (1 x 4096 -> 16384
+// bf16 24 us, 5.6 TB/s).
 constexpr int kFewWaves = 8;
 
 // Eight reduction indices from k on of an operand's row, as they lie in memory.
