@@ -521,6 +521,107 @@ srnl_status srnl_dwconv_bwd(const void *dout, srnl_dtype out_dtype, const void *
                             size_t workspace_bytes, void *stream);
 
 /*
+ * srnl_group_norm_fwd -- group norm with an activation over channels-last maps
+ * (a layer beside srnl_layer_norm_fwd, whose conventions hold): with n = (x -
+ * mean) rstd over the S cells and the C / groups channels of an item's group,
+ *   out = act(n gain + bias),  rstd = 1 / sqrt(var + eps), var biased.
+ *   x [B][S][C] in in_dtype; out [B][S][C] in out_dtype; gain, bias [C] fp32,
+ *   either NULL for 1 and 0; mean, rstd [B][groups] fp32, written unless NULL
+ *   (the backward pass reads them; 0 over no cells). C a multiple of groups,
+ *   C <= 2^20, B C <= 2^23. The variance is taken about the mean. Activations as
+ *   in srnl_linear_fwd. A NaN or infinity makes NaN of its item's group alone.
+ * Workspace: srnl_group_norm_fwd_workspace_bytes.
+ * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_WORKSPACE,
+ * SRNL_ERR_HIP.
+ */
+size_t srnl_group_norm_fwd_workspace_bytes(int B, long long S, int C, int groups);
+srnl_status srnl_group_norm_fwd(const void *x, int B, long long S, int C, int groups, srnl_dtype in_dtype,
+                                const float *gain, const float *bias, float eps, srnl_act act,
+                                srnl_dtype out_dtype, void *out, float *mean, float *rstd, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * srnl_group_norm_bwd -- with z = n gain + bias, dz = dout act'(z), d = dz gain:
+ *   dx = rstd (d - mean(d) - n mean(d n)) [+ dx_add]  (means over the group),
+ *   dgain[c] = sum over items and cells of dz n,  dbias[c] = the same of dz.
+ *   dout [B][S][C] in out_dtype; x, dx, dx_add in in_dtype; dx, dx_add, dgain,
+ *   dbias NULL if not wanted. gain, bias, act as in the forward.
+ * Workspace: srnl_group_norm_bwd_workspace_bytes.
+ * Errors: as the forward.
+ */
+size_t srnl_group_norm_bwd_workspace_bytes(int B, long long S, int C, int groups);
+srnl_status srnl_group_norm_bwd(const void *dout, srnl_dtype out_dtype, const void *x, int B, long long S, int C,
+                                int groups, srnl_dtype in_dtype, const float *gain, const float *bias,
+                                const float *mean, const float *rstd, srnl_act act, const void *dx_add, void *dx,
+                                float *dgain, float *dbias, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * srnl_dropout_fwd -- dropout whose mask is a function of seed, offset and the
+ * element's place, and is not stored (a layer, whose conventions hold):
+ *   out[n] = x[n] / (1 - p) where kept, else 0, [+ residual[n]],  n < count.
+ * Element n takes the 16 bits n % 8 of block n / 8 of Philox4x32-10 (as in
+ * srnl_init_states; low half of the first word first) with counter (block mod
+ * 2^32, block div 2^32, offset mod 2^32, offset div 2^32) and key seed. It is
+ * dropped where they are below c = floor(65536 p + 1/2), at most 65535; p is
+ * then c / 65536, exactly, in the scale too. p in [0, 1). What is dropped may be
+ * infinite or NaN.
+ *   counter: device, or NULL: a 64-bit number read when the kernel runs and
+ *   added to offset, so that a captured graph's replays draw new masks; both
+ *   passes of a step must find the same number there.
+ * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_HIP.
+ */
+srnl_status srnl_dropout_fwd(const void *x, srnl_dtype in_dtype, long long count, double p, unsigned long long seed,
+                             unsigned long long offset, const unsigned long long *counter, const void *residual,
+                             srnl_dtype residual_dtype, srnl_dtype out_dtype, void *out, void *stream);
+
+/*
+ * srnl_dropout_bwd -- dx[n] = dout[n] / (1 - p) where the forward kept n, else
+ * 0, [+ dx_add[n]]; p, seed, offset and counter the forward's. dout in out_dtype,
+ * dx and dx_add in in_dtype. The residual's gradient is dout itself.
+ * Errors: as the forward.
+ */
+srnl_status srnl_dropout_bwd(const void *dout, srnl_dtype out_dtype, long long count, double p,
+                             unsigned long long seed, unsigned long long offset, const unsigned long long *counter,
+                             const void *dx_add, srnl_dtype in_dtype, void *dx, void *stream);
+
+/*
+ * The gated delta rule: the retained delta rule of this operator's content
+ * memory with a write strength and a decay given per token, as a layer. Per item
+ * and head, with a state S (Dk x Dv) that a call may take up and hand on,
+ *   S <- exp(g_t) S,  u_t = beta_t (v_t - S^T k_t),  S <- S + k_t u_t^T,
+ *   o_t = scale S^T q_t.
+ * With norm_eps > 0, q and k are first divided by sqrt(|.|^2 + norm_eps).
+ *   q, k [B][T][Hk][Dk], v, out [B][T][H][Dv] in dtype; head h takes q and k of
+ *   head h / (H / Hk). Tokens of q, k and v may lie q_stride, k_stride, v_stride
+ *   elements apart (slices of one projection); item b starts T strides on.
+ *   g, beta [B][T][H], states [B][H][Dk][Dv], fp32.
+ *   Dk, Dv multiples of 8 from 8 to 256, H a multiple of Hk.
+ *   lengths [B] or NULL: tokens at or past an item's length (held to 0..T) are
+ *   not read and change nothing; their outputs and gradients are zero.
+ * g is at most 0 in use and may be -infinity (the state starts anew); beta is
+ * any number. States, sums and norms are fp32; the layers' conventions hold.
+ */
+typedef struct {
+    const void *q, *k, *v;
+    const float *g, *beta;
+    const float *state;        /* the states before the first token, or NULL for 0 */
+    const int *lengths;
+    int B, T, Hk, H, Dk, Dv;
+    long long q_stride, k_stride, v_stride;   /* 0: dense; else a multiple of 8 */
+    srnl_dtype dtype;
+    float scale, norm_eps;
+    void *stream;
+} srnl_gated_delta_params;
+
+/*
+ * srnl_gated_delta_step -- the rule token by token: a few tokens per sequence,
+ * as a server appends them. state_out: the states after the last token, or NULL;
+ * it may be params->state itself. Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE,
+ * SRNL_ERR_PTR, SRNL_ERR_HIP.
+ */
+srnl_status srnl_gated_delta_step(const srnl_gated_delta_params *params, void *out, float *state_out);
+
+/*
  * srnl_route_gather -- the route traversal as a standalone copy [OVERVIEW
  * Four-Directional Scanning and Spatial Chunking]:
  *   out[slot(r)][b][t][c] = x[b][i][j][c],  (i, j) = route r's t-th cell.

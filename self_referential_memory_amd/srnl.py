@@ -40,6 +40,9 @@ EXPORTS = ("srnl_scan_fwd", "srnl_scan_workspace_bytes", "srnl_scan_1d",
            "srnl_layer_norm_fwd", "srnl_layer_norm_bwd", "srnl_layer_norm_bwd_workspace_bytes",
            "srnl_linear_fwd", "srnl_linear_bwd", "srnl_linear_bwd_workspace_bytes",
            "srnl_dwconv_fwd", "srnl_dwconv_bwd", "srnl_dwconv_bwd_workspace_bytes",
+           "srnl_group_norm_fwd", "srnl_group_norm_fwd_workspace_bytes", "srnl_group_norm_bwd",
+           "srnl_group_norm_bwd_workspace_bytes", "srnl_dropout_fwd", "srnl_dropout_bwd",
+           "srnl_gated_delta_step",
            "srnl_route_index", "srnl_chunk_len", "srnl_status_string",
            "srnl_last_error")
 
@@ -76,6 +79,15 @@ class LinearParams(ctypes.Structure):
                 ("x_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
                 ("residual_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
                 ("act", ctypes.c_int), ("stream", ctypes.c_void_p)]
+
+
+class GatedDeltaParams(ctypes.Structure):
+    """srnl_gated_delta_params."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "g", "beta", "state", "lengths")]
+                + [(n, ctypes.c_int) for n in ("B", "T", "Hk", "H", "Dk", "Dv")]
+                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
+                + [("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("norm_eps", ctypes.c_float),
+                   ("stream", ctypes.c_void_p)])
 
 
 _lib = None
@@ -135,8 +147,23 @@ def lib() -> ctypes.CDLL:
         L.srnl_dwconv_bwd.argtypes = [vp, i, vp, i, i, i, i, i, vp, vp, vp, vp, vp, vp, sz, vp]
         L.srnl_dwconv_bwd_workspace_bytes.argtypes = [i, i, i, i]
         L.srnl_dwconv_bwd_workspace_bytes.restype = sz
+        L.srnl_group_norm_fwd_workspace_bytes.argtypes = [i, ll, i, i]
+        L.srnl_group_norm_fwd_workspace_bytes.restype = sz
+        L.srnl_group_norm_fwd.argtypes = [vp, i, ll, i, i, i, vp, vp, ctypes.c_float, i, i, vp, vp,
+                                          vp, vp, sz, vp]
+        L.srnl_group_norm_bwd_workspace_bytes.argtypes = [i, ll, i, i]
+        L.srnl_group_norm_bwd_workspace_bytes.restype = sz
+        L.srnl_group_norm_bwd.argtypes = [vp, i, vp, i, ll, i, i, i, vp, vp, vp, vp, i, vp, vp, vp,
+                                          vp, vp, sz, vp]
+        ull = ctypes.c_ulonglong
+        L.srnl_dropout_fwd.argtypes = [vp, i, ll, ctypes.c_double, ull, ull, vp, vp, i, i, vp, vp]
+        L.srnl_dropout_bwd.argtypes = [vp, i, ll, ctypes.c_double, ull, ull, vp, vp, i, vp, vp]
+        dp = ctypes.POINTER(GatedDeltaParams)
+        L.srnl_gated_delta_step.argtypes = [dp, vp, vp]
         for f in ("srnl_layer_norm_fwd", "srnl_layer_norm_bwd", "srnl_linear_fwd",
-                  "srnl_linear_bwd", "srnl_dwconv_fwd", "srnl_dwconv_bwd"):
+                  "srnl_linear_bwd", "srnl_dwconv_fwd", "srnl_dwconv_bwd", "srnl_group_norm_fwd",
+                  "srnl_group_norm_bwd", "srnl_dropout_fwd", "srnl_dropout_bwd",
+                  "srnl_gated_delta_step"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("srnl_scan_fwd", "srnl_scan_1d", "srnl_fuse", "srnl_scan_bwd",
                   "srnl_scan_1d_bwd", "srnl_fuse_bwd", "srnl_fuse_bwd_noalloc",
@@ -838,6 +865,169 @@ def dwconv_bwd(dout: torch.Tensor, u: torch.Tensor, w: torch.Tensor, *,
     return du, dw, db
 
 
+def group_norm_fwd(x: torch.Tensor, groups: int, gain: Optional[torch.Tensor],
+                   bias: Optional[torch.Tensor], eps: float = 1e-5, *, act="none", out_dtype=None,
+                   stats: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """srnl_group_norm_fwd: act of the group norm of x [B, ..., C] (channels
+    last, statistics over the cells between and the channels of a group) in
+    out_dtype (x's when None); with stats also (mean, rstd) [B, groups] fp32,
+    which group_norm_bwd takes. gain, bias: [C] fp32 or None. act as in
+    linear_fwd."""
+    B, S, C = _map(x)
+    for t, name in ((gain, "gain"), (bias, "bias")):
+        _expect(t, (C,), torch.float32, name)
+    code, dtx = _act_code(act), _dtype_code(x)
+    with _on(x, gain, bias):
+        out = _new(out, x.shape, x.dtype if out_dtype is None else out_dtype, x.device, like=x)
+        dto = _dtype_code(out)
+        mean = rstd = None
+        if stats:
+            mean = torch.empty((B, groups), dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
+        ws = _workspace(lib().srnl_group_norm_fwd_workspace_bytes(B, S, C, groups), x.device)
+        sh = _stream(stream, x)
+        _check(lib().srnl_group_norm_fwd(_ptr(x), B, S, C, groups, dtx, _ptr(gain), _ptr(bias), eps,
+                                         code, dto, _ptr(out), _ptr(mean), _ptr(rstd), _ptr(ws),
+                                         0 if ws is None else ws.numel(), sh), "srnl_group_norm_fwd")
+        _keep_for_stream(sh, ws)
+    return (out, mean, rstd) if stats else out
+
+
+def group_norm_bwd(dout: torch.Tensor, x: torch.Tensor, groups: int, gain: Optional[torch.Tensor],
+                   bias: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor, *,
+                   act="none", dx_add: Optional[torch.Tensor] = None, need_dx: bool = True,
+                   param_grads: bool = True, stream=None):
+    """srnl_group_norm_bwd: dout [B, ..., C] -> (dx in x's dtype, dgain, dbias
+    [C] fp32), None where not needed. dx_add: a gradient of x's shape and
+    dtype, added to dx."""
+    B, S, C = _map(x)
+    for t, name in ((gain, "gain"), (bias, "bias")):
+        _expect(t, (C,), torch.float32, name)
+    _expect(dout, x.shape, None, "dout")
+    _expect(dx_add, x.shape, x.dtype, "dx_add")
+    for t, name in ((mean, "mean"), (rstd, "rstd")):
+        _expect(t, (B, groups), torch.float32, name)
+    code, dtx, dto = _act_code(act), _dtype_code(x), _dtype_code(dout)
+    with _on(x, dout, gain, bias, mean, rstd, dx_add):
+        dx = torch.empty_like(x) if need_dx else None
+        dgain = torch.empty(C, dtype=torch.float32, device=x.device) if param_grads else None
+        dbias = torch.empty_like(dgain) if param_grads else None
+        ws = _workspace(lib().srnl_group_norm_bwd_workspace_bytes(B, S, C, groups), x.device)
+        sh = _stream(stream, x)
+        _check(lib().srnl_group_norm_bwd(
+            _ptr(dout), dto, _ptr(x), B, S, C, groups, dtx, _ptr(gain), _ptr(bias), _ptr(mean),
+            _ptr(rstd), code, _ptr(dx_add), _ptr(dx), _ptr(dgain), _ptr(dbias), _ptr(ws),
+            0 if ws is None else ws.numel(), sh), "srnl_group_norm_bwd")
+        _keep_for_stream(sh, ws)
+    return dx, dgain, dbias
+
+
+def _map(x: torch.Tensor):
+    """(items, cells, channels) of a channels-last map."""
+    if x.dim() < 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [B, ..., C]")
+    B, C = x.shape[0], x.shape[-1]
+    S = 1
+    for n in x.shape[1:-1]:
+        S *= n
+    return B, S, C
+
+
+_MASK64 = (1 << 64) - 1
+
+
+def dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int = 0, *,
+                residual: Optional[torch.Tensor] = None, counter: Optional[torch.Tensor] = None,
+                out_dtype=None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """srnl_dropout_fwd: x / (1 - p) where kept, else 0, plus the residual of
+    x's shape, in out_dtype (x's when None). The mask is a function of seed,
+    offset (64 bits each) and the element's place. counter: an int64 tensor of
+    one number on x's device, read when the kernel runs and added to offset
+    (advance it inside a captured graph, and each replay draws a new mask)."""
+    _expect(residual, x.shape, None, "residual")
+    _expect(counter, (1,), torch.int64, "counter")
+    dtx, dtr = _dtype_code(x), 0 if residual is None else _dtype_code(residual)
+    with _on(x, residual, counter):
+        out = _new(out, x.shape, x.dtype if out_dtype is None else out_dtype, x.device, like=x)
+        _check(lib().srnl_dropout_fwd(_ptr(x), dtx, x.numel(), p, seed & _MASK64, offset & _MASK64,
+                                      _ptr(counter), _ptr(residual), dtr, _dtype_code(out),
+                                      _ptr(out), _stream(stream, x)), "srnl_dropout_fwd")
+    return out
+
+
+def dropout_bwd(dout: torch.Tensor, p: float, seed: int, offset: int = 0, *, dtype=None,
+                dx_add: Optional[torch.Tensor] = None, counter: Optional[torch.Tensor] = None,
+                dx: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """srnl_dropout_bwd: the gradient of x in dtype (dout's when None), with the
+    forward's p, seed, offset and counter. dx_add: a gradient of that shape and
+    dtype, added to it."""
+    dtype = dout.dtype if dtype is None else dtype
+    _expect(dx_add, dout.shape, dtype, "dx_add")
+    _expect(counter, (1,), torch.int64, "counter")
+    dto = _dtype_code(dout)
+    with _on(dout, dx_add, counter):
+        dx = _new(dx, dout.shape, dtype, dout.device, "dx", dout)
+        _check(lib().srnl_dropout_bwd(_ptr(dout), dto, dout.numel(), p, seed & _MASK64,
+                                      offset & _MASK64, _ptr(counter), _ptr(dx_add), _dtype_code(dx),
+                                      _ptr(dx), _stream(stream, dout)), "srnl_dropout_bwd")
+    return dx
+
+
+# ---- the gated delta rule
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between tokens of t [B, T, heads, D], whose heads must be dense
+    and whose items must follow one another (a slice of one projection)."""
+    B, T, h, d = t.shape
+    if t.is_contiguous():
+        return 0
+    s = t.stride()
+    step = s[1] if T > 1 else s[0]
+    if s[3] != 1 or s[2] != d or (T > 1 and B > 1 and s[0] != T * step):
+        raise ValueError(f"{name} must be contiguous, or a slice of the last axis of a contiguous "
+                         "[B, T, ...] tensor")
+    return step
+
+
+def _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream):
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dim() != 4:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [B, T, heads, D]")
+    B, T, Hk, Dk = q.shape
+    H, Dv = v.shape[2:]
+    _expect(k, (B, T, Hk, Dk), q.dtype, "k")
+    _expect(v, (B, T, H, Dv), q.dtype, "v")
+    _expect(g, (B, T, H), torch.float32, "g")
+    _expect(beta, (B, T, H), torch.float32, "beta")
+    _expect(state, (B, H, Dk, Dv), torch.float32, "state")
+    _expect(lengths, (B,), torch.int32, "lengths")
+    return GatedDeltaParams(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(beta), _ptr(state), _ptr(lengths),
+        B, T, Hk, H, Dk, Dv, _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
+        _dtype_code(q), Dk ** -0.5 if scale is None else scale, norm_eps, _stream(stream, q))
+
+
+def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                     beta: torch.Tensor, state: torch.Tensor, *, lengths: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, norm_eps: float = 0.0,
+                     state_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     stream=None):
+    """srnl_gated_delta_step: a few tokens appended to each sequence, q, k [B, T,
+    Hk, Dk], v [B, T, H, Dv], g, beta [B, T, H], lengths [B] int32 or None.
+    Returns (out [B, T, H, Dv] in q's dtype, the states after the last token):
+    state [B, H, Dk, Dv] itself, updated in place, unless state_out is given.
+    scale: 1 / sqrt(Dk) when None."""
+    B, T, H, Dv = v.shape if v.dim() == 4 else (0, 0, 0, 0)
+    with _on(q, k, v, g, beta, state, lengths):
+        p = _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
+        state_out = state if state_out is None else _new(state_out, state.shape, torch.float32,
+                                                         q.device, "state_out")
+        out = _new(out, (B, T, H, Dv), q.dtype, q.device)
+        _check(lib().srnl_gated_delta_step(ctypes.byref(p), _ptr(out), _ptr(state_out)),
+               "srnl_gated_delta_step")
+    return out, state_out
+
+
 # ---- the layers as autograd nodes (on the current stream; reverse mode, once
 # differentiable: forward-mode tangents and second derivatives raise)
 
@@ -950,6 +1140,71 @@ def dwconv(u: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     if not _tracked(u, w, bias, add1, add2):
         return dwconv_fwd(u, w, bias, add1, add2, out_dtype=out_dtype)
     return DWConv.apply(u, w, bias, add1, add2, out_dtype)
+
+
+class GroupNorm(torch.autograd.Function):
+    """srnl_group_norm_fwd and srnl_group_norm_bwd as an autograd node."""
+
+    @staticmethod
+    def forward(ctx, x, groups, gain, bias, eps, act, out_dtype):
+        out, mean, rstd = group_norm_fwd(x, groups, gain, bias, eps, act=act, out_dtype=out_dtype,
+                                         stats=True)
+        ctx.save_for_backward(x, gain, bias, mean, rstd)
+        ctx.cfg = (groups, act)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        x, gain, bias, mean, rstd = ctx.saved_tensors
+        groups, act = ctx.cfg
+        need = ctx.needs_input_grad
+        dx, dgain, dbias = group_norm_bwd(_dense(dout), x, groups, gain, bias, mean, rstd, act=act,
+                                          need_dx=need[0], param_grads=need[2] or need[3])
+        return (dx, None, dgain if need[2] else None, dbias if need[3] else None, None, None, None)
+
+
+def group_norm(x: torch.Tensor, groups: int, gain: Optional[torch.Tensor],
+               bias: Optional[torch.Tensor], eps: float = 1e-5, *, act="none",
+               out_dtype=None) -> torch.Tensor:
+    """Differentiable group norm with an activation over x [B, ..., C]
+    (group_norm_fwd)."""
+    if not _tracked(x, gain, bias):
+        return group_norm_fwd(x, groups, gain, bias, eps, act=act, out_dtype=out_dtype)
+    return GroupNorm.apply(x, groups, gain, bias, eps, act, out_dtype)
+
+
+class Dropout(torch.autograd.Function):
+    """srnl_dropout_fwd and srnl_dropout_bwd as an autograd node: seed and
+    offset are kept, the mask is not. A counter's number is kept too, so that
+    it may move on between the passes."""
+
+    @staticmethod
+    def forward(ctx, x, p, seed, offset, residual, counter, out_dtype):
+        out = dropout_fwd(x, p, seed, offset, residual=residual, counter=counter,
+                          out_dtype=out_dtype)
+        ctx.save_for_backward(None if counter is None else counter.clone())
+        ctx.cfg = (p, seed, offset, x.dtype, None if residual is None else residual.dtype)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        p, seed, offset, dtype, res_dtype = ctx.cfg
+        need = ctx.needs_input_grad
+        dx = dropout_bwd(_dense(dout), p, seed, offset, dtype=dtype,
+                         counter=ctx.saved_tensors[0]) if need[0] else None
+        return dx, None, None, None, dout.to(res_dtype) if need[4] else None, None, None
+
+
+def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *,
+            residual: Optional[torch.Tensor] = None, counter: Optional[torch.Tensor] = None,
+            out_dtype=None) -> torch.Tensor:
+    """Differentiable dropout, plus the residual (dropout_fwd)."""
+    if not _tracked(x, residual):
+        return dropout_fwd(x, p, seed, offset, residual=residual, counter=counter,
+                           out_dtype=out_dtype)
+    return Dropout.apply(x, p, seed, offset, residual, counter, out_dtype)
 
 
 BLOCK_KEYS = ("ln1_w", "ln1_b", "wq", "dw_w", "dw_b", "ln2_w", "ln2_b", "w1", "b1", "w2", "b2")
