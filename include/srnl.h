@@ -595,7 +595,7 @@ srnl_status srnl_dropout_bwd(const void *dout, srnl_dtype out_dtype, long long c
  *   head h / (H / Hk). Tokens of q, k and v may lie q_stride, k_stride, v_stride
  *   elements apart (slices of one projection); item b starts T strides on.
  *   g, beta [B][T][H], states [B][H][Dk][Dv], fp32.
- *   Dk, Dv multiples of 8 from 8 to 256, H a multiple of Hk.
+ *   Dk and Dv multiples of 8, up to 128 and 256; H a multiple of Hk.
  *   lengths [B] or NULL: tokens at or past an item's length (held to 0..T) are
  *   not read and change nothing; their outputs and gradients are zero.
  * g is at most 0 in use and may be -infinity (the state starts anew); beta is
@@ -620,6 +620,34 @@ typedef struct {
  * SRNL_ERR_PTR, SRNL_ERR_HIP.
  */
 srnl_status srnl_gated_delta_step(const srnl_gated_delta_params *params, void *out, float *state_out);
+
+/*
+ * srnl_gated_delta_fwd -- the rule over whole sequences, 64 tokens at a time.
+ * state_out as above. record: NULL, or srnl_gated_delta_record_bytes of memory
+ * that the call fills for srnl_gated_delta_bwd (errors and states of every chunk).
+ * With bf16 inputs, what the call forms between is kept to 2^-17 (pairs of bf16
+ * words); sums are fp32, in a fixed order (bitwise reproducible).
+ * Workspace: srnl_gated_delta_fwd_workspace_bytes. Errors: as the step, plus
+ * SRNL_ERR_WORKSPACE (workspace or record).
+ */
+size_t srnl_gated_delta_record_bytes(const srnl_gated_delta_params *params);
+size_t srnl_gated_delta_fwd_workspace_bytes(const srnl_gated_delta_params *params);
+srnl_status srnl_gated_delta_fwd(const srnl_gated_delta_params *params, void *out, float *state_out, void *record,
+                                 size_t record_bytes, void *workspace, size_t workspace_bytes);
+
+/*
+ * srnl_gated_delta_bwd -- the gradients, from the forward's params and record:
+ *   dout [B][T][H][Dv] in dtype; dstate_out [B][H][Dk][Dv] fp32, the gradient of
+ *   the states after the last token, or NULL for 0;
+ *   dq, dk [B][T][Hk][Dk], dv [B][T][H][Dv] in dtype, dense (dq and dk summed over
+ *   the heads that share them); dg, dbeta [B][T][H], dstate [B][H][Dk][Dv] fp32;
+ *   any NULL if not wanted. Bitwise reproducible. params->state is not read.
+ * Workspace: srnl_gated_delta_bwd_workspace_bytes. Errors: as the forward.
+ */
+size_t srnl_gated_delta_bwd_workspace_bytes(const srnl_gated_delta_params *params);
+srnl_status srnl_gated_delta_bwd(const srnl_gated_delta_params *params, const void *dout, const float *dstate_out,
+                                 const void *record, size_t record_bytes, void *dq, void *dk, void *dv, float *dg,
+                                 float *dbeta, float *dstate, void *workspace, size_t workspace_bytes);
 
 /*
  * srnl_route_gather -- the route traversal as a standalone copy [OVERVIEW

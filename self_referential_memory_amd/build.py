@@ -12,7 +12,8 @@ ROOT = os.path.dirname(PKG)
 UNITS = [os.path.join(PKG, "csrc", "layers", f)
          for f in ("operator_unit.hip", "linear.hip", "narrow_bf16.hip", "narrow_fp32.hip",
                    "narrow_slope_bf16.hip", "narrow_slope_fp32.hip", "layers.hip", "group_norm.hip",
-                   "dropout.hip", "delta.hip", "delta_step.hip")]
+                   "dropout.hip", "delta.hip", "delta_step.hip", "delta_prep.hip", "delta_chain.hip",
+                   "delta_grads.hip")]
 LIB = os.path.join(PKG, "libsrnl.so")
 # the same source with the scan kernel's phase clocks compiled in (a
 # measurement build, loaded only by bench.py --phase-clocks)

@@ -16,8 +16,8 @@ srnl_status check_delta(const srnl_gated_delta_params *p)
         return fail(SRNL_ERR_ARG, "B and T must be >= 0");
     if (p->Hk < 1 || p->H < 1 || p->H % p->Hk)
         return fail(SRNL_ERR_ARG, "heads must be >= 1 and H a multiple of Hk");
-    if (p->Dk < 8 || p->Dk > 256 || p->Dk % 8 || p->Dv < 8 || p->Dv > 256 || p->Dv % 8)
-        return fail(SRNL_ERR_ARG, "Dk and Dv must be multiples of 8 from 8 to 256");
+    if (p->Dk < 8 || p->Dk > 128 || p->Dk % 8 || p->Dv < 8 || p->Dv > 256 || p->Dv % 8)
+        return fail(SRNL_ERR_ARG, "Dk and Dv must be multiples of 8, up to 128 and 256");
     if (p->H > 1 << 20)
         return fail(SRNL_ERR_ARG, "too many heads");
     if (!valid_dtype(p->dtype))
@@ -65,7 +65,34 @@ DeltaArgs delta_args(const srnl_gated_delta_params &p)
     a.bf = p.dtype == SRNL_BF16;
     a.scale = p.scale;
     a.eps = p.norm_eps;
+    a.N = (p.T + DELTA_CHUNK - 1) / DELTA_CHUNK;
     return a;
+}
+
+size_t chunks_of(const DeltaArgs &a) { return static_cast<size_t>(a.B) * a.H * a.N; }
+
+// workspace: X, P and the row factors of every chunk; the record: errors and states
+size_t square_bytes(const DeltaArgs &a) { return chunks_of(a) * DELTA_SQUARE; }
+size_t vec_bytes(const DeltaArgs &a) { return chunks_of(a) * VEC_FLOATS * sizeof(float); }
+size_t rows_bytes(const DeltaArgs &a) { return chunks_of(a) * DELTA_CHUNK * a.Dv * 4; }
+size_t state_bytes(const DeltaArgs &a) { return chunks_of(a) * a.Dk * a.Dv * 4; }
+
+size_t fwd_bytes(const DeltaArgs &a) { return 2 * square_bytes(a) + vec_bytes(a); }
+size_t record_bytes_of(const DeltaArgs &a) { return rows_bytes(a) + state_bytes(a); }
+size_t bwd_bytes(const DeltaArgs &a) { return fwd_bytes(a) + rows_bytes(a) + state_bytes(a); }
+
+char *place_squares(DeltaArgs &a, void *workspace)
+{
+    a.X = static_cast<char *>(workspace);
+    a.P = a.X + square_bytes(a);
+    a.vec = reinterpret_cast<float *>(a.P + square_bytes(a));
+    return reinterpret_cast<char *>(a.vec) + vec_bytes(a);
+}
+
+void place_record(DeltaArgs &a, const void *record)
+{
+    a.E = static_cast<char *>(const_cast<void *>(record));
+    a.S0 = a.E + rows_bytes(a);
 }
 
 srnl_status check_inputs(const srnl_gated_delta_params &p)
@@ -97,6 +124,107 @@ srnl_status srnl_gated_delta_step(const srnl_gated_delta_params *p, void *out, f
     a.out = out;
     a.state_out = state_out;
     return launch_delta_step(a, static_cast<hipStream_t>(p->stream));
+}
+
+size_t srnl_gated_delta_record_bytes(const srnl_gated_delta_params *p)
+{
+    return check_delta(p) == SRNL_OK ? record_bytes_of(delta_args(*p)) : 0;
+}
+
+size_t srnl_gated_delta_fwd_workspace_bytes(const srnl_gated_delta_params *p)
+{
+    return check_delta(p) == SRNL_OK ? fwd_bytes(delta_args(*p)) : 0;
+}
+
+size_t srnl_gated_delta_bwd_workspace_bytes(const srnl_gated_delta_params *p)
+{
+    return check_delta(p) == SRNL_OK ? bwd_bytes(delta_args(*p)) : 0;
+}
+
+srnl_status srnl_gated_delta_fwd(const srnl_gated_delta_params *p, void *out, float *state_out, void *record,
+                                 size_t record_bytes, void *workspace, size_t workspace_bytes)
+{
+    srnl_set_error(SRNL_OK, "");
+    srnl_status s = check_delta(p);
+    if (s != SRNL_OK || p->B == 0)
+        return s;
+    DeltaArgs a = delta_args(*p);
+    if (a.N && (!workspace || workspace_bytes < fwd_bytes(a)))
+        return fail(SRNL_ERR_WORKSPACE, "workspace smaller than srnl_gated_delta_fwd_workspace_bytes");
+    if (record && record_bytes < record_bytes_of(a))
+        return fail(SRNL_ERR_WORKSPACE, "record smaller than srnl_gated_delta_record_bytes");
+    s = check_inputs(*p);
+    const PtrArg outs[] = {{out, "out", a.N == 0},
+                           {state_out, "state_out", true},
+                           {a.N ? record : nullptr, "record", true},
+                           {a.N ? workspace : nullptr, "workspace", true}};
+    if (s == SRNL_OK)
+        s = check_ptrs(outs, 4);
+    if (s != SRNL_OK)
+        return s;
+    hipStream_t st = static_cast<hipStream_t>(p->stream);
+    a.out = out;
+    a.state_out = state_out;
+    if (a.N) {
+        place_squares(a, workspace);
+        if (record)
+            place_record(a, record);
+        s = launch_delta_prep(a, false, st);
+        if (s != SRNL_OK)
+            return s;
+    }
+    return launch_delta_chain(a, st);
+}
+
+srnl_status srnl_gated_delta_bwd(const srnl_gated_delta_params *p, const void *dout, const float *dstate_out,
+                                 const void *record, size_t record_bytes, void *dq, void *dk, void *dv, float *dg,
+                                 float *dbeta, float *dstate, void *workspace, size_t workspace_bytes)
+{
+    srnl_set_error(SRNL_OK, "");
+    srnl_status s = check_delta(p);
+    if (s != SRNL_OK || p->B == 0)
+        return s;
+    DeltaArgs a = delta_args(*p);
+    if (a.N && (!workspace || workspace_bytes < bwd_bytes(a)))
+        return fail(SRNL_ERR_WORKSPACE, "workspace smaller than srnl_gated_delta_bwd_workspace_bytes");
+    if (a.N && (!record || record_bytes < record_bytes_of(a)))
+        return fail(SRNL_ERR_WORKSPACE, "record smaller than srnl_gated_delta_record_bytes");
+    s = check_inputs(*p);
+    const PtrArg more[] = {{dout, "dout", a.N == 0},
+                           {dstate_out, "dstate_out", true},
+                           {a.N ? record : nullptr, "record", true},
+                           {dq, "dq", true},
+                           {dk, "dk", true},
+                           {dv, "dv", true},
+                           {dg, "dg", true},
+                           {dbeta, "dbeta", true},
+                           {dstate, "dstate", true},
+                           {a.N ? workspace : nullptr, "workspace", true}};
+    if (s == SRNL_OK)
+        s = check_ptrs(more, 10);
+    if (s != SRNL_OK)
+        return s;
+    hipStream_t st = static_cast<hipStream_t>(p->stream);
+    a.dout = dout;
+    a.dstate_out = dstate_out;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dg = dg;
+    a.dbeta = dbeta;
+    a.dstate = dstate;
+    if (a.N) {
+        a.dV = place_squares(a, workspace);
+        a.D1 = a.dV + rows_bytes(a);
+        place_record(a, record);
+        s = launch_delta_prep(a, true, st);
+        if (s != SRNL_OK)
+            return s;
+    }
+    s = launch_delta_chain_bwd(a, st);
+    if (s == SRNL_OK && a.N && (dq || dk || dg || dbeta))
+        s = launch_delta_grads(a, st);
+    return s;
 }
 
 }  // extern "C"

@@ -1,0 +1,193 @@
+// delta_prep.hip -- per chunk and head of the gated delta rule: the row factors,
+// X = (I + M b)^-1 and P (see delta.h), every chunk at once.
+//
+// A block takes one chunk, a wave 16 of its rows. X is inverted in fp32: the four
+// 16 x 16 blocks on the diagonal by substitution, a column a lane; then the blocks
+// below, one diagonal after the other, X_ij = -X_ii sum L_ik X_kj, with fp32
+// matrix products whose result is the next one's operand without a move (its rows
+// 4 quad + s serve as the reduction elements of step s).
+#include "delta_mma.h"
+
+namespace {
+
+using namespace srnl_i;
+
+template <bool BF, int KD, bool TRANSPOSED>
+__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
+{
+    constexpr int KF = KD / 32;
+    __shared__ __attribute__((aligned(16))) float L[64][68], X[64][68];
+    __shared__ float ghi[64], glo[64], bet[64], rks[64], rqs[64];
+    const int c = blockIdx.x % a.N, bh = blockIdx.x / a.N;
+    const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
+    const int n = delta_tokens(a, b), tok0 = DELTA_CHUNK * c;
+    if (tok0 >= n)
+        return;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, quad = lane >> 4, l15 = lane & 15;
+    float *vec = a.vec + static_cast<long long>(blockIdx.x) * VEC_FLOATS;
+
+    if (wave == 0) {
+        // sums in 64 bits: what matters later is their differences. Below -1000 a
+        // factor is 0 either way; -infinity would make NaN of a difference.
+        const bool live = tok0 + lane < n;
+        const long long at = (static_cast<long long>(b) * a.T + tok0 + lane) * a.H + h;
+        const float g = live ? a.g[at] : 0.0f;
+        double G = g < -1000.0f ? -1000.0 : static_cast<double>(g);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(G, off);
+            if (lane >= off)
+                G += o;
+        }
+        const float hi = static_cast<float>(G), lo = static_cast<float>(G - hi);
+        const float beta = live ? a.beta[at] : 0.0f;
+        const double left = __shfl(G, 63) - G;
+        const float lhi = static_cast<float>(left);
+        ghi[lane] = hi;
+        glo[lane] = lo;
+        bet[lane] = beta;
+        vec[VEC_GAM + lane] = expf(hi) * (1.0f + lo);
+        vec[VEC_END + lane] = expf(lhi) * (1.0f + static_cast<float>(left - lhi));
+        vec[VEC_BETA + lane] = beta;
+        vec[VEC_GHI + lane] = hi;
+        vec[VEC_GLO + lane] = lo;
+    }
+
+    const long long tok = static_cast<long long>(b) * a.T + tok0;
+    const int row = 16 * wave + l15;
+    In<BF> kf[KF], qf[KF];
+    float kk = 0.0f, qq = 0.0f;
+#pragma unroll
+    for (int f = 0; f < KF; ++f) {
+        const int k = 32 * f + 8 * quad;
+        const bool live = tok0 + row < n && k < a.Dk;
+        kf[f] = in_load<BF>(a.k, (tok + row) * a.ks + static_cast<long long>(hk) * a.Dk + k, live);
+        qf[f] = in_load<BF>(a.q, (tok + row) * a.qs + static_cast<long long>(hk) * a.Dk + k, live);
+        kk += in_squares(kf[f]);
+        qq += in_squares(qf[f]);
+    }
+    kk += __shfl_xor(kk, 16);
+    kk += __shfl_xor(kk, 32);
+    qq += __shfl_xor(qq, 16);
+    qq += __shfl_xor(qq, 32);
+    if (quad == 0) {
+        // a row past the end has no direction: its factor is 0, not 1 / sqrt(eps)
+        const bool live = tok0 + row < n;
+        const float rk = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
+        const float rq = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(qq + a.eps) : 1.0f;
+        rks[row] = rk;
+        rqs[row] = rq;
+        vec[VEC_RK + row] = rk;
+        vec[VEC_RQ + row] = rq;
+    }
+    __syncthreads();
+
+    v4f p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        p[j] = v4f_zero();
+        if (j > wave) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                X[16 * wave + 4 * quad + r][16 * j + l15] = 0.0f;
+            continue;
+        }
+        const int col = 16 * j + l15;
+        v4f m = v4f_zero();
+#pragma unroll
+        for (int f = 0; f < KF; ++f) {
+            const int k = 32 * f + 8 * quad;
+            const In<BF> o = in_load<BF>(a.k, (tok + col) * a.ks + static_cast<long long>(hk) * a.Dk + k,
+                                         tok0 + col < n && k < a.Dk);
+            m = mma(kf[f], o, m);
+            p[j] = mma(qf[f], o, p[j]);
+        }
+        const float jhi = ghi[col], jlo = glo[col], rj = rks[col], bj = bet[col];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * wave + 4 * quad + r;
+            const float d = decay(ghi[i], glo[i], jhi, jlo) * rj;
+            L[i][col] = col < i ? m[r] * rks[i] * d * bj : 0.0f;
+            p[j][r] = col <= i ? p[j][r] * rqs[i] * d * a.scale : 0.0f;
+        }
+    }
+    __syncthreads();
+
+    // blocks on the diagonal
+    {
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            float s = r == l15 ? 1.0f : 0.0f;
+#pragma unroll
+            for (int k = 0; k < r; ++k)
+                s = fmaf(-L[16 * wave + r][16 * wave + k], x[k], s);
+            x[r] = s;
+        }
+        if (quad == 0)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                X[16 * wave + r][16 * wave + l15] = x[r];
+    }
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+        __syncthreads();
+        if (wave < d)
+            continue;
+        const int j = wave - d;
+        v4f y = v4f_zero();
+        for (int k = j; k < wave; ++k) {
+            const v4f l = *reinterpret_cast<const v4f *>(&L[16 * wave + l15][16 * k + 4 * quad]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                y = __builtin_amdgcn_mfma_f32_16x16x4f32(l[s], X[16 * k + 4 * quad + s][16 * j + l15], y, 0, 0, 0);
+        }
+        const v4f xi = *reinterpret_cast<const v4f *>(&X[16 * wave + l15][16 * wave + 4 * quad]);
+        v4f z = v4f_zero();
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            z = __builtin_amdgcn_mfma_f32_16x16x4f32(xi[s], y[s], z, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            X[16 * wave + 4 * quad + r][16 * j + l15] = -z[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            L[16 * wave + 4 * quad + r][16 * j + l15] = p[j][r];
+    __syncthreads();
+    char *xo = a.X + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 256;
+    char *po = a.P + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 256;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+        const int k = 32 * f + 8 * quad;
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x[e] = TRANSPOSED ? X[k + e][row] : X[row][k + e];
+            y[e] = TRANSPOSED ? L[k + e][row] : L[row][k + e];
+        }
+        mid_store8<BF>(xo + 4 * k, x);
+        mid_store8<BF>(po + 4 * k, y);
+    }
+}
+
+}  // namespace
+
+namespace srnl_i {
+
+srnl_status launch_delta_prep(const DeltaArgs &a, bool transposed, hipStream_t st)
+{
+    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.H * a.N));
+#define SRNL_DELTA_PREP(BF, KD)                                                                    \
+    if (transposed)                                                                                \
+        hipLaunchKernelGGL((delta_prep_kernel<BF, KD, true>), grid, dim3(256), 0, st, a);          \
+    else                                                                                           \
+        hipLaunchKernelGGL((delta_prep_kernel<BF, KD, false>), grid, dim3(256), 0, st, a)
+    SRNL_DELTA_DISPATCH(a, SRNL_DELTA_PREP);
+    return launched("delta_prep_kernel");
+}
+
+}  // namespace srnl_i

@@ -140,10 +140,8 @@ srnl_status launch_delta_step(const DeltaArgs &a, hipStream_t st)
         hipLaunchKernelGGL(delta_step_kernel<2>, grid, dim3(256), 0, st, a);
     else if (a.Dk <= 64)
         hipLaunchKernelGGL(delta_step_kernel<4>, grid, dim3(256), 0, st, a);
-    else if (a.Dk <= 128)
-        hipLaunchKernelGGL(delta_step_kernel<8>, grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL(delta_step_kernel<16>, grid, dim3(256), 0, st, a);
+        hipLaunchKernelGGL(delta_step_kernel<8>, grid, dim3(256), 0, st, a);
     return launched("delta_step_kernel");
 }
 

@@ -42,7 +42,9 @@ EXPORTS = ("srnl_scan_fwd", "srnl_scan_workspace_bytes", "srnl_scan_1d",
            "srnl_dwconv_fwd", "srnl_dwconv_bwd", "srnl_dwconv_bwd_workspace_bytes",
            "srnl_group_norm_fwd", "srnl_group_norm_fwd_workspace_bytes", "srnl_group_norm_bwd",
            "srnl_group_norm_bwd_workspace_bytes", "srnl_dropout_fwd", "srnl_dropout_bwd",
-           "srnl_gated_delta_step",
+           "srnl_gated_delta_step", "srnl_gated_delta_fwd", "srnl_gated_delta_fwd_workspace_bytes",
+           "srnl_gated_delta_record_bytes", "srnl_gated_delta_bwd",
+           "srnl_gated_delta_bwd_workspace_bytes",
            "srnl_route_index", "srnl_chunk_len", "srnl_status_string",
            "srnl_last_error")
 
@@ -160,10 +162,16 @@ def lib() -> ctypes.CDLL:
         L.srnl_dropout_bwd.argtypes = [vp, i, ll, ctypes.c_double, ull, ull, vp, vp, i, vp, vp]
         dp = ctypes.POINTER(GatedDeltaParams)
         L.srnl_gated_delta_step.argtypes = [dp, vp, vp]
+        L.srnl_gated_delta_fwd.argtypes = [dp, vp, vp, vp, sz, vp, sz]
+        L.srnl_gated_delta_bwd.argtypes = [dp, vp, vp, vp, sz, vp, vp, vp, vp, vp, vp, vp, sz]
+        for f in ("srnl_gated_delta_record_bytes", "srnl_gated_delta_fwd_workspace_bytes",
+                  "srnl_gated_delta_bwd_workspace_bytes"):
+            getattr(L, f).argtypes = [dp]
+            getattr(L, f).restype = sz
         for f in ("srnl_layer_norm_fwd", "srnl_layer_norm_bwd", "srnl_linear_fwd",
                   "srnl_linear_bwd", "srnl_dwconv_fwd", "srnl_dwconv_bwd", "srnl_group_norm_fwd",
                   "srnl_group_norm_bwd", "srnl_dropout_fwd", "srnl_dropout_bwd",
-                  "srnl_gated_delta_step"):
+                  "srnl_gated_delta_step", "srnl_gated_delta_fwd", "srnl_gated_delta_bwd"):
             getattr(L, f).restype = ctypes.c_int
         for f in ("srnl_scan_fwd", "srnl_scan_1d", "srnl_fuse", "srnl_scan_bwd",
                   "srnl_scan_1d_bwd", "srnl_fuse_bwd", "srnl_fuse_bwd_noalloc",
@@ -1028,6 +1036,63 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     return out, state_out
 
 
+def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                    beta: torch.Tensor, *, state: Optional[torch.Tensor] = None,
+                    lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    norm_eps: float = 0.0, record: bool = False,
+                    state_out: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    stream=None):
+    """srnl_gated_delta_fwd: whole sequences, arguments as gated_delta_step's
+    (state None: zeros). Returns (out, the states after the last token); with
+    record also the record that gated_delta_bwd takes."""
+    B, T, H, Dv = v.shape if v.dim() == 4 else (0, 0, 0, 0)
+    L = lib()
+    with _on(q, k, v, g, beta, state, lengths):
+        p = _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
+        state_out = _new(state_out, (B, H, q.shape[3], Dv), torch.float32, q.device, "state_out")
+        out = _new(out, (B, T, H, Dv), q.dtype, q.device)
+        rec = None
+        if record:
+            rec = torch.empty(L.srnl_gated_delta_record_bytes(ctypes.byref(p)), dtype=torch.uint8,
+                              device=q.device)
+        ws = _workspace(L.srnl_gated_delta_fwd_workspace_bytes(ctypes.byref(p)), q.device)
+        _check(L.srnl_gated_delta_fwd(ctypes.byref(p), _ptr(out), _ptr(state_out), _ptr(rec),
+                                      0 if rec is None else rec.numel(), _ptr(ws),
+                                      0 if ws is None else ws.numel()), "srnl_gated_delta_fwd")
+        _keep_for_stream(p.stream, ws)
+    return (out, state_out, rec) if record else (out, state_out)
+
+
+def gated_delta_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    g: torch.Tensor, beta: torch.Tensor, record: torch.Tensor, *,
+                    state: Optional[torch.Tensor] = None, dstate: Optional[torch.Tensor] = None,
+                    lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                    norm_eps: float = 0.0, stream=None):
+    """srnl_gated_delta_bwd: dout [B, T, H, Dv], record from gated_delta_fwd with
+    the same arguments, dstate the gradient of the states it returned (None: 0).
+    Returns (dq, dk, dv in q's dtype, dg, dbeta fp32, the gradient of state, or
+    None without one)."""
+    L = lib()
+    with _on(q, k, v, g, beta, state, lengths, dout, record, dstate):
+        p = _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
+        _expect(dout, v.shape, q.dtype, "dout")
+        _expect(dstate, (p.B, p.H, p.Dk, p.Dv), torch.float32, "dstate")
+        if record.dtype != torch.uint8 or record.dim() != 1:
+            raise ValueError("record must be the one that gated_delta_fwd(record=True) returned")
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dk = torch.empty_like(dq)
+        dv = torch.empty(v.shape, dtype=q.dtype, device=q.device)
+        dg, dbeta = torch.empty_like(g), torch.empty_like(g)
+        ds = None if state is None else torch.empty_like(state)
+        ws = _workspace(L.srnl_gated_delta_bwd_workspace_bytes(ctypes.byref(p)), q.device)
+        _check(L.srnl_gated_delta_bwd(ctypes.byref(p), _ptr(dout), _ptr(dstate), _ptr(record),
+                                      record.numel(), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+                                      _ptr(dbeta), _ptr(ds), _ptr(ws),
+                                      0 if ws is None else ws.numel()), "srnl_gated_delta_bwd")
+        _keep_for_stream(p.stream, ws)
+    return dq, dk, dv, dg, dbeta, ds
+
+
 # ---- the layers as autograd nodes (on the current stream; reverse mode, once
 # differentiable: forward-mode tangents and second derivatives raise)
 
@@ -1205,6 +1270,43 @@ def dropout(x: torch.Tensor, p: float, seed: int, offset: int = 0, *,
         return dropout_fwd(x, p, seed, offset, residual=residual, counter=counter,
                            out_dtype=out_dtype)
     return Dropout.apply(x, p, seed, offset, residual, counter, out_dtype)
+
+
+class GatedDelta(torch.autograd.Function):
+    """srnl_gated_delta_fwd and srnl_gated_delta_bwd as an autograd node, with the
+    states after the last token as a second output."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, state, lengths, scale, norm_eps):
+        ctx.set_materialize_grads(False)
+        out, state_out, record = gated_delta_fwd(q, k, v, g, beta, state=state, lengths=lengths,
+                                                 scale=scale, norm_eps=norm_eps, record=True)
+        ctx.save_for_backward(q, k, v, g, beta, state, lengths, record)
+        ctx.cfg = (scale, norm_eps)
+        return out, state_out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, dstate):
+        q, k, v, g, beta, state, lengths, record = ctx.saved_tensors
+        scale, norm_eps = ctx.cfg
+        dout = torch.zeros(v.shape, dtype=v.dtype, device=v.device) if dout is None else _dense(dout)
+        grads = gated_delta_bwd(dout, q, k, v, g, beta, record, state=state,
+                                dstate=None if dstate is None else _dense(dstate), lengths=lengths,
+                                scale=scale, norm_eps=norm_eps)
+        return (*grads, None, None, None)
+
+
+def gated_delta(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
+                beta: torch.Tensor, state: Optional[torch.Tensor] = None, *,
+                lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                norm_eps: float = 0.0):
+    """Differentiable gated delta rule: (out, the states after the last token)
+    of gated_delta_fwd, with gradients for q, k, v, g, beta and state."""
+    if not _tracked(q, k, v, g, beta, state):
+        return gated_delta_fwd(q, k, v, g, beta, state=state, lengths=lengths, scale=scale,
+                               norm_eps=norm_eps)
+    return GatedDelta.apply(q, k, v, g, beta, state, lengths, scale, norm_eps)
 
 
 BLOCK_KEYS = ("ln1_w", "ln1_b", "wq", "dw_w", "dw_b", "ln2_w", "ln2_b", "w1", "b1", "w2", "b2")

@@ -10,6 +10,13 @@ scale is the larger of the reference's norm and its mean over the heads; for
 outputs it is the norm of the terms scale |S| |q| that they are sums of: a sum's
 roundings are relative to its terms, and the one token of a single head may
 leave next to nothing of them (q.k = 0).
+
+In chunks of 64 the rule is five chained products: rows of at most Dk, 64 and 64
+terms, through an inverse that stretches by at most a few (4 is allowed for). fp32
+is off by 4 x 4 (Dk + 136) u a chunk; with bf16 inputs each operand between is
+right to 2^-17, a product of two to 2^-16 of the norms, 4 x 4 x 2^-16 a chunk
+besides. The backward pass makes as many products again, of values that carry the
+forward's error, and adds its own: three times that.
 """
 import pytest
 import torch
@@ -51,8 +58,8 @@ def step_tol(T, Dk):
 
 STEP = [  # B, T, Hk, H, Dk, Dv, norm, lengths
     (1, 1, 1, 1, 8, 8, True, None), (3, 1, 2, 4, 128, 128, True, None), (2, 5, 1, 3, 64, 72, True, (5, 2)),
-    (4, 3, 2, 2, 40, 200, False, (0, 1, 3, 9)), (2, 2, 1, 2, 256, 256, True, (-4, 2)), (2, 7, 3, 3, 16, 64, False, None),
-    (1, 4, 1, 1, 136, 8, True, None)]
+    (4, 3, 2, 2, 40, 200, False, (0, 1, 3, 9)), (2, 2, 1, 2, 120, 256, True, (-4, 2)), (2, 7, 3, 3, 16, 64, False, None),
+    (1, 4, 1, 1, 104, 8, True, None)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -81,3 +88,52 @@ def test_step(case, dtype, state):
             assert not out[b, max(n, 0):].any()
             if n <= 0:
                 assert torch.equal(S1[b], before[b])
+
+
+def chunk_tol(T, Dk, dtype):
+    chunks = max(1, -(-T // 64))
+    return 16 * chunks * ((Dk + 136) * U + (2.0 ** -16 if dtype == BF16 else 0.0))
+
+
+CHUNKED = [  # B, T, Hk, H, Dk, Dv, norm, lengths
+    (1, 1, 1, 1, 8, 8, True, None), (2, 2, 1, 2, 32, 32, True, None), (1, 63, 2, 2, 64, 64, False, None),
+    (2, 64, 1, 3, 128, 128, True, None), (1, 65, 2, 4, 40, 72, True, None), (2, 200, 2, 2, 24, 200, True, (200, 131)),
+    (5, 130, 1, 2, 96, 48, False, (0, 1, 64, 65, 130)), (1, 257, 3, 6, 128, 256, True, None),
+    (3, 90, 1, 1, 16, 8, True, (500, -3, 89)), (2, 129, 2, 2, 56, 40, False, None)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("state", [True, False])
+@pytest.mark.parametrize("case", CHUNKED, ids=str)
+def test_forward_and_backward(case, dtype, state):
+    B, T, Hk, H, Dk, Dv, norm, lengths = case
+    say("chunks", case, dtype, state)
+    d = delta_oracle.inputs(11, B, T, Hk, H, Dk, Dv, dtype, norm=norm, state=state, lengths=lengths)
+    gen = torch.Generator().manual_seed(3)
+    dout = torch.randn((B, T, H, Dv), generator=gen).to(dtype)
+    dstate = 0.3 * torch.randn((B, H, Dk, Dv), generator=gen) if state else None
+    eps = 1e-6 if norm else 0.0
+    ref, S, terms, grads = delta_oracle.reference(d, norm_eps=eps, dout=dout, dstate=dstate)
+    x = on_gpu(d)
+    kw = dict(state=x["state"], lengths=x["lengths"], norm_eps=eps)
+    args = (x["q"], x["k"], x["v"], x["g"], x["beta"])
+    out, S1, rec = srnl.gated_delta_fwd(*args, record=True, **kw)
+    tol = chunk_tol(T, Dk, dtype)
+    close(out, ref, tol, "out", 2, terms)
+    close(S1, S, tol, "state", 1)
+    out2, S2 = srnl.gated_delta_fwd(*args, **kw)          # without a record, the same bits
+    assert torch.equal(out, out2) and torch.equal(S1, S2)
+    got = srnl.gated_delta_bwd(dout.to(DEV), *args, rec, dstate=None if dstate is None else dstate.to(DEV), **kw)
+    for name, t in zip(("q", "k", "v", "g", "beta", "state"), got):
+        if t is None:
+            assert not state and name == "state"
+            continue
+        close(t, grads[name], 3 * tol, "d" + name, 1 if name == "state" else 2)
+    if lengths is not None:
+        for b, n in enumerate(lengths):
+            n = min(max(n, 0), T)
+            assert not any(t[b, n:].any() for t in (out, *got[:5]))
+            if n == 0 and state:
+                assert torch.equal(S1[b], x["state"][b]) and torch.equal(got[5][b], dstate[b].to(DEV))
+    again = srnl.gated_delta_bwd(dout.to(DEV), *args, rec, dstate=None if dstate is None else dstate.to(DEV), **kw)
+    assert all(a is b or torch.equal(a, b) for a, b in zip(got, again))
