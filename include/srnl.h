@@ -593,7 +593,7 @@ srnl_status srnl_dropout_bwd(const void *dout, srnl_dtype out_dtype, long long c
  * With norm_eps > 0, q and k are first divided by sqrt(|.|^2 + norm_eps).
  *   q, k [B][T][Hk][Dk], v, out [B][T][H][Dv] in dtype; head h takes q and k of
  *   head h / (H / Hk). Tokens of q, k and v may lie q_stride, k_stride, v_stride
- *   elements apart (slices of one projection); item b starts T strides on.
+ *   elements apart (slices of one projection), at most 2^22; item b starts T strides on.
  *   g, beta [B][T][H], states [B][H][Dk][Dv], fp32.
  *   Dk and Dv multiples of 8, up to 128 and 256; H a multiple of Hk.
  *   lengths [B] or NULL: tokens at or past an item's length (held to 0..T) are

@@ -9,7 +9,7 @@
 // and backward, D1 and D0 the gradients of S1 and S0:
 //   dU = e^(G_63 - G) K^ D1 + P^T dO,  dV = X^T b dU
 //   D0 = e^(G_63) D1 + (scale e^G Q^)^T dO - (e^G K^)^T dV
-// The error E = V - S^T K before beta, and not U, is what is kept: beta may be 0.
+// (tokens as rows). The error E = V - S^T K before beta, and not U, is what is kept: beta may be 0.
 // Every exponent is a difference of later and earlier sums, at most 0 for g <= 0.
 //
 // Kernels: per chunk X and P (delta_prep.hip); the states from chunk to chunk
@@ -23,7 +23,7 @@
 namespace srnl_i {
 
 constexpr int DELTA_CHUNK = 64;
-constexpr int DELTA_SQUARE = 64 * 64 * 4;      // bytes of X or P of one chunk
+constexpr int DELTA_SQUARE = 64 * 64 * 6;      // bytes of X or P of one chunk, at most
 // a chunk's row factors: e^G, e^(G_63 - G), beta, 1/|k|, 1/|q|, G in two floats
 enum { VEC_GAM = 0, VEC_END = 64, VEC_BETA = 128, VEC_RK = 192, VEC_RQ = 256, VEC_GHI = 320, VEC_GLO = 384,
        VEC_FLOATS = 448 };
@@ -43,15 +43,15 @@ struct DeltaArgs {
     // per (item, head, chunk), in this order
     char *X, *P;                 // [64][64] split values
     float *vec;                  // [VEC_FLOATS]
-    char *E;                     // record: [64][Dv] split values
-    char *S0;                    // record: [Dk][Dv] split values
+    float *E;                    // record: [64][Dv]
+    float *S0;                   // record: [Dk][Dv]
     // backward
     const void *dout;
     const float *dstate_out;
     void *dq, *dk, *dv;
     float *dg, *dbeta, *dstate;
-    char *dV;                    // [64][Dv] split values
-    char *D1;                    // [Dk][Dv] split values
+    float *dV;                   // [64][Dv]
+    float *D1;                   // [Dk][Dv]
 };
 
 // The tokens of item b that count.
@@ -65,8 +65,7 @@ __device__ __forceinline__ int delta_tokens(const DeltaArgs &a, int b)
 
 srnl_status launch_delta_step(const DeltaArgs &a, hipStream_t st);
 srnl_status launch_delta_prep(const DeltaArgs &a, bool transposed, hipStream_t st);
-srnl_status launch_delta_chain(const DeltaArgs &a, hipStream_t st);
-srnl_status launch_delta_chain_bwd(const DeltaArgs &a, hipStream_t st);
+srnl_status launch_delta_chain(const DeltaArgs &a, bool backward, hipStream_t st);
 srnl_status launch_delta_grads(const DeltaArgs &a, hipStream_t st);
 
 // f<BF16, width of k padded to 32, 64 or 128>

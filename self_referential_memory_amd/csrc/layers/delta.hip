@@ -33,6 +33,9 @@ srnl_status check_delta(const srnl_gated_delta_params *p)
         if (strides[i] && (strides[i] < rows[i] || strides[i] % 8))
             return fail(SRNL_ERR_ARG, "a token stride must be 0, or a multiple of 8 and at least heads x head size");
         const long long s = strides[i] ? strides[i] : rows[i];
+        // 64 tokens' offsets are 31 bits
+        if (s > 1 << 22)
+            return fail(SRNL_ERR_ARG, "a token's heads, or a token stride, exceed 2^22 elements");
         if (static_cast<__int128>(p->B) * p->T * s >= (static_cast<__int128>(1) << 60))
             return fail(SRNL_ERR_ARG, "tensors too large");
     }
@@ -91,8 +94,8 @@ char *place_squares(DeltaArgs &a, void *workspace)
 
 void place_record(DeltaArgs &a, const void *record)
 {
-    a.E = static_cast<char *>(const_cast<void *>(record));
-    a.S0 = a.E + rows_bytes(a);
+    a.E = static_cast<float *>(const_cast<void *>(record));
+    a.S0 = a.E + rows_bytes(a) / 4;
 }
 
 srnl_status check_inputs(const srnl_gated_delta_params &p)
@@ -173,7 +176,7 @@ srnl_status srnl_gated_delta_fwd(const srnl_gated_delta_params *p, void *out, fl
         if (s != SRNL_OK)
             return s;
     }
-    return launch_delta_chain(a, st);
+    return launch_delta_chain(a, false, st);
 }
 
 srnl_status srnl_gated_delta_bwd(const srnl_gated_delta_params *p, const void *dout, const float *dstate_out,
@@ -214,14 +217,14 @@ srnl_status srnl_gated_delta_bwd(const srnl_gated_delta_params *p, const void *d
     a.dbeta = dbeta;
     a.dstate = dstate;
     if (a.N) {
-        a.dV = place_squares(a, workspace);
-        a.D1 = a.dV + rows_bytes(a);
+        a.dV = reinterpret_cast<float *>(place_squares(a, workspace));
+        a.D1 = a.dV + rows_bytes(a) / 4;
         place_record(a, record);
         s = launch_delta_prep(a, true, st);
         if (s != SRNL_OK)
             return s;
     }
-    s = launch_delta_chain_bwd(a, st);
+    s = launch_delta_chain(a, true, st);
     if (s == SRNL_OK && a.N && (dq || dk || dg || dbeta))
         s = launch_delta_grads(a, st);
     return s;

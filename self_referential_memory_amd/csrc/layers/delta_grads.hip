@@ -15,9 +15,12 @@
 // large terms would cancel. dk = (dk^ - k^ (k^.dk^)) / |k| at the end, likewise q.
 //
 // A block of eight waves takes a chunk of one q/k head and the v heads that share
-// it, one after the other. Of the 64 x 64 parts a wave forms 16 rows by 32
-// columns; of the products with the head's width, 16 columns (narrow heads: fewer
-// rows), so that the states, the largest operands, are read once.
+// it, one after the other. It walks the columns of v, 32 at a time: dO, E and dV go
+// to LDS, the next 32 columns on their way meanwhile; of the 64 x 64 parts a wave
+// forms 16 rows by 32 columns, of the products with the states 16 of the head's
+// columns (narrow heads: fewer rows), so that the states, the largest operands, are
+// read once, straight into registers. A, Y and the row factors then make the
+// matrices that multiply q and k, in the LDS that dO, E and dV leave.
 #include "delta_mma.h"
 
 namespace {
@@ -26,7 +29,14 @@ using namespace srnl_i;
 
 template <bool BF, int KD> struct GradShared {
     __attribute__((aligned(16))) Rows<BF, KD> k, q;
-    __attribute__((aligned(16))) char A[64][272], At[64][272], Z[64][272];
+    union {
+        struct {
+            __attribute__((aligned(16))) char O[64][mid_row<BF, 1>(32)], E[64][mid_row<BF, 3>(32)], V[64][mid_row<BF, 3>(32)];
+        } in[2];
+        struct {
+            __attribute__((aligned(16))) char A[64][mid_row<BF, 2>(64)], At[64][mid_row<BF, 2>(64)], Z[64][mid_row<BF, 2>(64)];
+        } out;
+    };
     float gam[64], end[64], beta[64], rk[64], rq[64], ghi[64], glo[64];
     float colF[4][64], rowF[2][64], diag[64], dot[2][8][64], sd[8];
 };
@@ -65,9 +75,9 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
         for (int i = threadIdx.x; i < inside * a.Dk; i += 512) {
             const long long o = ((tok + i / a.Dk) * a.Hk + hk) * a.Dk + i % a.Dk;
             if (a.dq)
-                put_value<BF>(a.dq, o, 0.0f);
+                put_at<BF>(a.dq, o, 0.0f);
             if (a.dk)
-                put_value<BF>(a.dk, o, 0.0f);
+                put_at<BF>(a.dk, o, 0.0f);
         }
         for (int i = threadIdx.x; i < inside * per; i += 512) {
             const long long o = (tok + i / per) * a.H + hk * per + i % per;
@@ -79,25 +89,17 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
         return;
     }
 
-    In<BF> kf[KF], qf[KF];
+    const long long head = static_cast<long long>(hk) * a.Dk;
+    const Buf rowsK(a.k, (tok * a.ks + head) * (BF ? 2 : 4)), rowsQ(a.q, (tok * a.qs + head) * (BF ? 2 : 4));
 #pragma unroll
-    for (int f = 0; f < KF; ++f) {
-        const int k = 32 * f + 8 * quad;
-        const bool live = row < left && k < a.Dk;
-        kf[f] = in_load<BF>(a.k, (tok + row) * a.ks + static_cast<long long>(hk) * a.Dk + k, live);
-        qf[f] = in_load<BF>(a.q, (tok + row) * a.qs + static_cast<long long>(hk) * a.Dk + k, live);
-        if (half == 0) {
-            sh.k.put(row, k, kf[f]);
-            sh.q.put(row, k, qf[f]);
+    for (int x = 0; x < KD / 64 + (KD < 64); ++x) {
+        // a thread's pieces of 8: every row, KD / 8 pieces
+        const int i = threadIdx.x + 512 * x, r = i / (KD / 8), k = i % (KD / 8) * 8;
+        if (r < 64) {
+            sh.k.put(r, k, in_load<BF>(rowsK, r * static_cast<int>(a.ks) + k, r < left && k < a.Dk));
+            sh.q.put(r, k, in_load<BF>(rowsQ, r * static_cast<int>(a.qs) + k, r < left && k < a.Dk));
         }
     }
-    // element of this head's q or k
-    const auto element = [](const Rows<BF, KD> &r, int t, int col) -> float {
-        if constexpr (BF)
-            return bf16_one(r.e[t][col]);
-        else
-            return r.e[t][col];
-    };
 
     v4f dq[RT], dk[RT];
 #pragma unroll
@@ -107,9 +109,26 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
     for (int g = 0; g < per; ++g) {
         const int h = hk * per + g;
         const long long at = (static_cast<long long>(b) * a.H + h) * a.N + c;
-        const char *E = a.E + at * DELTA_CHUNK * a.Dv * 4, *dV = a.dV + at * DELTA_CHUNK * a.Dv * 4;
-        const char *S0 = a.S0 + at * a.Dk * a.Dv * 4, *D1 = a.D1 + at * a.Dk * a.Dv * 4;
+        const Buf bS(a.S0, at * a.Dk * a.Dv * 4), bD(a.D1, at * a.Dk * a.Dv * 4);
         const float *vec = a.vec + at * VEC_FLOATS;
+        // this thread's piece of 8 of E or dV, and of dO
+        const int pr = (threadIdx.x & 255) >> 2, pc = (threadIdx.x & 3) * 8;
+        const bool ofE = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
+        const Buf bEV(ofE ? a.E : a.dV, at * DELTA_CHUNK * a.Dv * 4);
+        const Buf bO(a.dout, (tok * a.H + h) * a.Dv * (BF ? 2 : 4));
+        struct { float ev[8], s[8], d[8]; In<BF> o; } next;
+        const auto fetch = [&](int v) __attribute__((always_inline)) {
+            load8(bEV, pr * a.Dv + pc + v, v + pc < a.Dv, next.ev);
+            next.o = in_load<BF>(bO, pr * a.H * a.Dv + pc + v, ofE && v + pc < a.Dv && pr < left);
+            load8(bS, mycol * a.Dv + 8 * quad + v, mycol < a.Dk && v + 8 * quad < a.Dv, next.s);
+            load8(bD, mycol * a.Dv + 8 * quad + v, mycol < a.Dk && v + 8 * quad < a.Dv, next.d);
+        };
+        const auto spread = [&](int buf) __attribute__((always_inline)) {
+            mid_store8<BF, 3>((ofE ? sh.in[buf].E[pr] : sh.in[buf].V[pr]) + pc / 8 * mid8<BF, 3>, next.ev);
+            if (ofE)
+                __builtin_memcpy(__builtin_assume_aligned(sh.in[buf].O[pr] + pc / 8 * mid8<BF, 1>, 16), &next.o, sizeof next.o);
+        };
+        fetch(0);
         __syncthreads();               // the head before is done with the shared arrays
         if (threadIdx.x < 64) {
             sh.gam[lane] = vec[VEC_GAM + lane];
@@ -120,28 +139,58 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
             sh.ghi[lane] = vec[VEC_GHI + lane];
             sh.glo[lane] = vec[VEC_GLO + lane];
         }
-        __syncthreads();
+        spread(0);
 
-        // ---- 64 x 64 parts: this wave's 16 rows i against the columns j
-        v4f A[2], Y[2];
+        v4f A[2], Y[2], oS[RT], vS[RT], eD[RT];
 #pragma unroll
         for (int x = 0; x < 2; ++x)
             A[x] = Y[x] = v4f_zero();
-#pragma unroll 1
-        for (int v = 8 * quad; v - 8 * quad < a.Dv; v += 32) {
-            const bool in = v < a.Dv;
-            const In<BF> o = in_load<BF>(a.dout, ((tok + row) * a.H + h) * a.Dv + v, in && row < left);
-            const Mid<BF> y = in ? mid_load<BF>(dV + (static_cast<long long>(row) * a.Dv + v) * 4) : mid_zero<BF>();
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int j = 2 * half + x;
-                if (j > band)
-                    continue;
-                const Mid<BF> e = in ? mid_load<BF>(E + (static_cast<long long>(16 * j + l15) * a.Dv + v) * 4) : mid_zero<BF>();
-                A[x] = mma(o, e, A[x]);
-                Y[x] = mma(y, e, Y[x]);
+        for (int ri = 0; ri < RT; ++ri)
+            oS[ri] = vS[ri] = eD[ri] = v4f_zero();
+        float sd = 0.0f;
+        int buf = 0;
+#pragma unroll 1
+        for (int v = 0; v < a.Dv; v += 32, buf ^= 1) {
+            const Mid<BF, 3> s = mid_split<BF, 3>(next.s), d = mid_split<BF, 3>(next.d);
+            if (rt0 == 0)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sd = fmaf(next.s[e], next.d[e], sd);
+            if (v + 32 < a.Dv)
+                fetch(v + 32);
+            lds_barrier();
+            const auto rowO = [&](int r) __attribute__((always_inline)) {
+                In<BF> f;
+                __builtin_memcpy(&f, __builtin_assume_aligned(sh.in[buf].O[r] + quad * mid8<BF, 1>, 16), sizeof f);
+                return f;
+            };
+            {
+                const In<BF> o = rowO(row);
+                const Mid<BF, 3> y = mid_load<BF, 3>(sh.in[buf].V[row] + quad * mid8<BF, 3>);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = 2 * half + x;
+                    if (j > band)
+                        continue;
+                    const Mid<BF, 3> e = mid_load<BF, 3>(sh.in[buf].E[16 * j + l15] + quad * mid8<BF, 3>);
+                    A[x] = mma(o, e, A[x]);
+                    Y[x] = mma(y, e, Y[x]);
+                }
             }
+#pragma unroll
+            for (int ri = 0; ri < RT; ++ri) {
+                const int r = 16 * (rt0 + ri) + l15;
+                oS[ri] = mma(rowO(r), s, oS[ri]);
+                vS[ri] = mma(mid_load<BF, 3>(sh.in[buf].V[r] + quad * mid8<BF, 3>), s, vS[ri]);
+                eD[ri] = mma(mid_load<BF, 3>(sh.in[buf].E[r] + quad * mid8<BF, 3>), d, eD[ri]);
+            }
+            if (v + 32 < a.Dv)
+                spread(buf ^ 1);
         }
+        __syncthreads();               // dO, E and dV are read
+
+        // ---- 64 x 64 parts: this wave's rows i against its columns j
         float rowF[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -153,10 +202,9 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
 #pragma unroll
                 for (int f = 0; f < KF; ++f) {
                     const int k = 32 * f + 8 * quad;
-                    const In<BF> o = in_load<BF>(a.k, (tok + col) * a.ks + static_cast<long long>(hk) * a.Dk + k,
-                                                 col < left && k < a.Dk);
-                    kk = mma(kf[f], o, kk);
-                    qk = mma(qf[f], o, qk);
+                    const In<BF> o = sh.k.across(col, k);
+                    kk = mma(sh.k.across(row, k), o, kk);
+                    qk = mma(sh.q.across(row, k), o, qk);
                 }
                 const float bj = sh.beta[col], rj = sh.rk[col];
 #pragma unroll
@@ -179,12 +227,12 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                         sh.diag[i] = F;
                 }
             }
-            mid_store_rows<BF>(sh.A[rows], 272, col, wa, true);
-            mid_store4<BF>(sh.At[col], rows, wat);
+            mid_store_rows<BF, 2>(sh.out.A[rows], sizeof sh.out.A[0], col, wa);
+            mid_store4<BF, 2>(sh.out.At[col], rows, wat);
             // Z's two triangles: rows i > j from here, its mirror from the same values
             if (j < band) {
-                mid_store_rows<BF>(sh.Z[rows], 272, col, zl, true);
-                mid_store4<BF>(sh.Z[col], rows, zu);
+                mid_store_rows<BF, 2>(sh.out.Z[rows], sizeof sh.out.Z[0], col, zl);
+                mid_store4<BF, 2>(sh.out.Z[col], rows, zu);
             }
             colF += __shfl_xor(colF, 16);
             colF += __shfl_xor(colF, 32);
@@ -202,7 +250,7 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                     const float up = (l15 & 2) ? ((l15 & 1) ? u3 : u2) : ((l15 & 1) ? u1 : u0);
                     z[e] = l15 < 4 * quad + e ? zl[e] : l15 > 4 * quad + e ? up : 0.0f;
                 }
-                mid_store_rows<BF>(sh.Z[rows], 272, col, z, true);
+                mid_store_rows<BF, 2>(sh.out.Z[rows], sizeof sh.out.Z[0], col, z);
             }
         }
 #pragma unroll
@@ -215,37 +263,14 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
         // ---- products with the head's width: this wave's columns
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
-            const int o = 4 * (32 * f + 8 * quad);
+            const int o = (4 * f + quad) * mid8<BF, 2>;
             const In<BF> kd = sh.k.down(32 * f, col0), qd = sh.q.down(32 * f, col0);
 #pragma unroll
             for (int ri = 0; ri < RT; ++ri) {
                 const int r = 16 * (rt0 + ri) + l15;
-                dq[ri] = mma(mid_load<BF>(sh.A[r] + o), kd, dq[ri]);
-                dk[ri] = mma(mid_load<BF>(sh.At[r] + o), qd, dk[ri]);
-                dk[ri] = mma(mid_load<BF>(sh.Z[r] + o), kd, dk[ri]);
-            }
-        }
-        v4f oS[RT], vS[RT], eD[RT];
-#pragma unroll
-        for (int ri = 0; ri < RT; ++ri)
-            oS[ri] = vS[ri] = eD[ri] = v4f_zero();
-        float sd = 0.0f;
-#pragma unroll 1
-        for (int v = 8 * quad; v - 8 * quad < a.Dv; v += 32) {
-            const bool in = v < a.Dv, inc = in && mycol < a.Dk;
-            const long long at_s = (static_cast<long long>(mycol) * a.Dv + v) * 4;
-            const Mid<BF> s = inc ? mid_load<BF>(S0 + at_s) : mid_zero<BF>();
-            const Mid<BF> d = inc ? mid_load<BF>(D1 + at_s) : mid_zero<BF>();
-            if (rt0 == 0)
-                sd += mid_dot(s, d);
-#pragma unroll
-            for (int ri = 0; ri < RT; ++ri) {
-                const int r = 16 * (rt0 + ri) + l15;
-                const In<BF> o = in_load<BF>(a.dout, ((tok + r) * a.H + h) * a.Dv + v, in && r < left);
-                const long long at_r = (static_cast<long long>(r) * a.Dv + v) * 4;
-                oS[ri] = mma(o, s, oS[ri]);
-                vS[ri] = mma(in ? mid_load<BF>(dV + at_r) : mid_zero<BF>(), s, vS[ri]);
-                eD[ri] = mma(in ? mid_load<BF>(E + at_r) : mid_zero<BF>(), d, eD[ri]);
+                dq[ri] = mma(mid_load<BF, 2>(sh.out.A[r] + o), kd, dq[ri]);
+                dk[ri] = mma(mid_load<BF, 2>(sh.out.At[r] + o), qd, dk[ri]);
+                dk[ri] = mma(mid_load<BF, 2>(sh.out.Z[r] + o), kd, dk[ri]);
             }
         }
 #pragma unroll
@@ -256,7 +281,7 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                 const float x = a.scale * sh.gam[i] * oS[ri][e];
                 const float y = -sh.gam[i] * vS[ri][e];
                 const float w = sh.end[i] * eD[ri][e];
-                const float kh = sh.rk[i] * element(sh.k, i, mycol), qh = sh.rq[i] * element(sh.q, i, mycol);
+                const float kh = sh.rk[i] * sh.k.at(i, mycol), qh = sh.rq[i] * sh.q.at(i, mycol);
                 const float s = sum16(fmaf(qh, x, kh * y)), t = sum16(kh * w);
                 if (l15 == 0) {
                     sh.dot[0][wave % Co::CW][i] = s;
@@ -315,8 +340,8 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int i = 16 * (rt0 + ri) + 4 * quad + e;
-                const float x = sum16(element(sh.q, i, mycol) * dq[ri][e]);
-                const float y = sum16(element(sh.k, i, mycol) * dk[ri][e]);
+                const float x = sum16(sh.q.at(i, mycol) * dq[ri][e]);
+                const float y = sum16(sh.k.at(i, mycol) * dk[ri][e]);
                 if (l15 == 0) {
                     sh.dot[0][wave % Co::CW][i] = x;
                     sh.dot[1][wave % Co::CW][i] = y;
@@ -338,16 +363,16 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                     xs += sh.dot[0][w][i];
                     ys += sh.dot[1][w][i];
                 }
-                x = rq * (x - rq * element(sh.q, i, mycol) * (rq * xs));
-                y = rk * (y - rk * element(sh.k, i, mycol) * (rk * ys));
+                x = rq * (x - rq * sh.q.at(i, mycol) * (rq * xs));
+                y = rk * (y - rk * sh.k.at(i, mycol) * (rk * ys));
             }
             if (i >= inside || mycol >= a.Dk)
                 continue;
             const long long o = ((tok + i) * a.Hk + hk) * a.Dk + mycol;
             if (a.dq)
-                put_value<BF>(a.dq, o, i < left ? x : 0.0f);
+                put_at<BF>(a.dq, o, i < left ? x : 0.0f);
             if (a.dk)
-                put_value<BF>(a.dk, o, i < left ? y : 0.0f);
+                put_at<BF>(a.dk, o, i < left ? y : 0.0f);
         }
 }
 

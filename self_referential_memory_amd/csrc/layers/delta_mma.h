@@ -5,11 +5,12 @@
 // l & 15 in rows 4 (l >> 4) .. + 3. fp32 products run as eight 16 x 16 x 4 ones
 // whose reduction order is the same for both operands.
 //
-// Inputs (In) are bf16 words or fp32 values. What the kernels form between
-// (Mid) is fp32, or with bf16 inputs the sum of two bf16 words, right to 2^-17:
-// one word would round states and errors to 2^-9 at every chunk. The product of
-// two such pairs leaves out the low words' (2^-18). A row of split values takes 4
-// bytes a value either way, 8 high words followed by their 8 low ones.
+// Inputs (In) are bf16 words or fp32 values. What the kernels form between (Mid) is
+// fp32, or with bf16 inputs a sum of PL bf16 words: two are right to 2^-18 and go
+// where only bf16 outputs depend on them; three, right to 2^-26, where states and
+// fp32 gradients do (with two those were off by 4e-6 to 7e-6, with three by 2e-7 to
+// 5e-7, as the fp32 path). A product of two leaves out the pairs of words below its
+// smallest kept one. 8 values lie together, one plane of 16 bytes after the other.
 #ifndef SRNL_LAYERS_DELTA_MMA_H
 #define SRNL_LAYERS_DELTA_MMA_H
 
@@ -20,8 +21,11 @@ namespace srnl_i {
 
 template <bool BF> struct In { bf16x8 v; };
 template <> struct In<false> { float v[8]; };
-template <bool BF> struct Mid { bf16x8 hi, lo; };
-template <> struct Mid<false> { float v[8]; };
+template <bool BF, int PL> struct Mid { bf16x8 p[PL]; };
+template <int PL> struct Mid<false, PL> { float v[8]; };
+// bytes of 8 values, and of a row of n with the pad that spreads 16 rows over the banks
+template <bool BF, int PL> constexpr int mid8 = BF ? 16 * PL : 32;
+template <bool BF, int PL> constexpr int mid_row(int n) { return n / 8 * mid8<BF, PL> + 16; }
 
 __device__ __forceinline__ v4f mma16(bf16x8 a, bf16x8 b, v4f c)
 {
@@ -36,35 +40,90 @@ __device__ __forceinline__ v4f mma16(const float (&a)[8], const float (&b)[8], v
 }
 // smallest parts first
 __device__ __forceinline__ v4f mma(const In<true> &a, const In<true> &b, v4f c) { return mma16(a.v, b.v, c); }
-__device__ __forceinline__ v4f mma(const In<true> &a, const Mid<true> &b, v4f c)
+template <int PL> __device__ __forceinline__ v4f mma(const In<true> &a, const Mid<true, PL> &b, v4f c)
 {
-    return mma16(a.v, b.hi, mma16(a.v, b.lo, c));
+#pragma unroll
+    for (int j = PL - 1; j >= 0; --j)
+        c = mma16(a.v, b.p[j], c);
+    return c;
 }
-__device__ __forceinline__ v4f mma(const Mid<true> &a, const In<true> &b, v4f c)
+template <int PL> __device__ __forceinline__ v4f mma(const Mid<true, PL> &a, const In<true> &b, v4f c)
 {
-    return mma16(a.hi, b.v, mma16(a.lo, b.v, c));
+#pragma unroll
+    for (int j = PL - 1; j >= 0; --j)
+        c = mma16(a.p[j], b.v, c);
+    return c;
 }
-__device__ __forceinline__ v4f mma(const Mid<true> &a, const Mid<true> &b, v4f c)
+template <int PL> __device__ __forceinline__ v4f mma(const Mid<true, PL> &a, const Mid<true, PL> &b, v4f c)
 {
-    return mma16(a.hi, b.hi, mma16(a.hi, b.lo, mma16(a.lo, b.hi, c)));
+#pragma unroll
+    for (int s = PL - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            c = mma16(a.p[i], b.p[s - i], c);
+    return c;
 }
 __device__ __forceinline__ v4f mma(const In<false> &a, const In<false> &b, v4f c) { return mma16(a.v, b.v, c); }
-__device__ __forceinline__ v4f mma(const In<false> &a, const Mid<false> &b, v4f c) { return mma16(a.v, b.v, c); }
-__device__ __forceinline__ v4f mma(const Mid<false> &a, const In<false> &b, v4f c) { return mma16(a.v, b.v, c); }
-__device__ __forceinline__ v4f mma(const Mid<false> &a, const Mid<false> &b, v4f c) { return mma16(a.v, b.v, c); }
+template <int PL> __device__ __forceinline__ v4f mma(const In<false> &a, const Mid<false, PL> &b, v4f c)
+{
+    return mma16(a.v, b.v, c);
+}
+template <int PL> __device__ __forceinline__ v4f mma(const Mid<false, PL> &a, const In<false> &b, v4f c)
+{
+    return mma16(a.v, b.v, c);
+}
+template <int PL> __device__ __forceinline__ v4f mma(const Mid<false, PL> &a, const Mid<false, PL> &b, v4f c)
+{
+    return mma16(a.v, b.v, c);
+}
 
 __device__ __forceinline__ v4f v4f_zero() { return v4f{0.0f, 0.0f, 0.0f, 0.0f}; }
 
-// ---- values
+// ---- memory
+//
+// Loads and stores go through buffer descriptors over 2 GB from a base that the
+// whole wave shares: a lane that has nothing there gives an offset past the end,
+// reads 0 and writes nothing. No branch parts the loads, so that none is waited for
+// before its value is used.
 
-template <bool BF> __device__ __forceinline__ float value(const void *p, long long o)
+constexpr unsigned NOWHERE = 0x80000000u;
+struct Buf {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ Buf(const void *base, long long byte)
+        : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(static_cast<const char *>(base)) + byte, 0, 0x7FFFFFF0,
+                                              0x00020000))
+    {
+    }
+};
+__device__ __forceinline__ u32x4 buf16(const Buf &b, unsigned o)
+{
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.r, o, 0, 0));
+}
+
+// bf16 words or fp32 values as they come
+template <bool BF> struct Raw { uint16_t v; };
+template <> struct Raw<false> { float v; };
+__device__ __forceinline__ float value(Raw<true> r) { return bf16_one(r.v); }
+__device__ __forceinline__ float value(Raw<false> r) { return r.v; }
+// o in elements
+template <bool BF> __device__ __forceinline__ Raw<BF> raw_load(const Buf &b, int o, bool live)
+{
+    Raw<BF> v;
+    if constexpr (BF)
+        v.v = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(b.r, live ? 2u * o : NOWHERE, 0, 0));
+    else
+        v.v = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b.r, live ? 4u * o : NOWHERE, 0, 0));
+    return v;
+}
+template <bool BF> __device__ __forceinline__ void put_value(const Buf &b, int o, bool live, float v)
 {
     if constexpr (BF)
-        return bf16_one(static_cast<const uint16_t *>(p)[o]);
+        __builtin_amdgcn_raw_buffer_store_b16(to_bf16(v), b.r, live ? 2u * o : NOWHERE, 0, 0);
     else
-        return static_cast<const float *>(p)[o];
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b.r, live ? 4u * o : NOWHERE, 0, 0);
 }
-template <bool BF> __device__ __forceinline__ void put_value(void *p, long long o, float v)
+// a value by its address, for what no loop waits for
+template <bool BF> __device__ __forceinline__ void put_at(void *p, long long o, float v)
 {
     if constexpr (BF)
         static_cast<uint16_t *>(p)[o] = to_bf16(v);
@@ -74,18 +133,16 @@ template <bool BF> __device__ __forceinline__ void put_value(void *p, long long 
 
 // ---- inputs
 
-template <bool BF> __device__ __forceinline__ In<BF> in_zero()
+// 8 elements from element o (a multiple of 8) on, zeros where not live
+template <bool BF> __device__ __forceinline__ In<BF> in_load(const Buf &b, int o, bool live)
 {
     In<BF> f;
-    __builtin_memset(&f, 0, sizeof f);
-    return f;
-}
-// 8 elements from element o (a multiple of 8) on, zeros where not live
-template <bool BF> __device__ __forceinline__ In<BF> in_load(const void *p, long long o, bool live)
-{
-    In<BF> f = in_zero<BF>();
-    if (live)
-        __builtin_memcpy(&f, static_cast<const char *>(p) + o * (BF ? 2 : 4), sizeof f);
+    const unsigned at = live ? static_cast<unsigned>(o) * (BF ? 2u : 4u) : NOWHERE;
+    u32x4 t[BF ? 1 : 2];
+    t[0] = buf16(b, at);
+    if constexpr (!BF)
+        t[1] = buf16(b, at + 16);
+    __builtin_memcpy(&f, t, sizeof f);
     return f;
 }
 __device__ __forceinline__ float in_squares(const In<true> &f)
@@ -109,112 +166,116 @@ __device__ __forceinline__ float in_squares(const In<false> &f)
 
 // ---- split values
 
-template <bool BF> __device__ __forceinline__ Mid<BF> mid_zero()
+// 8 values of the first PL planes at p in LDS, 16-byte aligned
+template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_load(const char *p)
 {
-    Mid<BF> f;
-    __builtin_memset(&f, 0, sizeof f);
+    Mid<BF, PL> f;
+    u32x4 t[BF ? PL : 2];
+#pragma unroll
+    for (int j = 0; j < (BF ? PL : 2); ++j)
+        t[j] = reinterpret_cast<const u32x4 *>(p)[j];
+    __builtin_memcpy(&f, t, sizeof f);
     return f;
 }
-// 8 values at p (LDS or memory; 32 bytes, 16-byte aligned)
-template <bool BF> __device__ __forceinline__ Mid<BF> mid_load(const char *p)
+// ... in memory, at byte o
+template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_load(const Buf &b, unsigned o)
 {
-    Mid<BF> f;
-    const u32x4 *w = reinterpret_cast<const u32x4 *>(p);
-    const u32x4 t[2] = {w[0], w[1]};
-    __builtin_memcpy(&f, t, 32);
+    Mid<BF, PL> f;
+    u32x4 t[BF ? PL : 2];
+#pragma unroll
+    for (int j = 0; j < (BF ? PL : 2); ++j)
+        t[j] = buf16(b, o + 16 * j);
+    __builtin_memcpy(&f, t, sizeof f);
     return f;
 }
-__device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo)
+// the PL words of two values, from the largest
+template <int PL> __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[PL])
 {
-    hi = pack_bf16(a, b);
-    lo = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
+#pragma unroll
+    for (int j = 0; j < PL; ++j) {
+        w[j] = pack_bf16(a, b);
+        if (j + 1 < PL) {
+            a -= bf16_lo(w[j]);
+            b -= bf16_hi(w[j]);
+        }
+    }
 }
-// 8 fp32 values to p
-template <bool BF> __device__ __forceinline__ void mid_store8(char *p, const float (&v)[8])
+template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_split(const float (&v)[8])
 {
-    u32x4 t[2];
+    Mid<BF, PL> f;
     if constexpr (BF) {
+        u32x4 t[PL];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint32_t hi, lo;
-            split_pair(v[2 * j], v[2 * j + 1], hi, lo);
-            t[0][j] = hi;
-            t[1][j] = lo;
+            uint32_t w[PL];
+            split_pair<PL>(v[2 * j], v[2 * j + 1], w);
+#pragma unroll
+            for (int k = 0; k < PL; ++k)
+                t[k][j] = w[k];
         }
+        __builtin_memcpy(&f, t, sizeof f);
     } else {
-        __builtin_memcpy(t, v, 32);
+        __builtin_memcpy(&f, v, sizeof f);
     }
-    reinterpret_cast<u32x4 *>(p)[0] = t[0];
-    reinterpret_cast<u32x4 *>(p)[1] = t[1];
+    return f;
+}
+// 8 fp32 values to p
+template <bool BF, int PL> __device__ __forceinline__ void mid_store8(char *p, const float (&v)[8])
+{
+    const Mid<BF, PL> f = mid_split<BF, PL>(v);
+    u32x4 t[sizeof f / 16];
+    __builtin_memcpy(t, &f, sizeof f);
+#pragma unroll
+    for (unsigned j = 0; j < sizeof f / 16; ++j)
+        reinterpret_cast<u32x4 *>(p)[j] = t[j];
 }
 // a result tile's column as a row of its transpose: 4 values at place k (a
 // multiple of 4) of the row at p
-template <bool BF> __device__ __forceinline__ void mid_store4(char *p, int k, v4f v)
+template <bool BF, int PL> __device__ __forceinline__ void mid_store4(char *p, int k, v4f v)
 {
-    char *q = p + (k & ~7) * 4;
+    char *q = p + k / 8 * mid8<BF, PL>;
     if constexpr (BF) {
-        u32x2 hi, lo;
-        uint32_t h, l;
-        split_pair(v[0], v[1], h, l);
-        hi[0] = h;
-        lo[0] = l;
-        split_pair(v[2], v[3], h, l);
-        hi[1] = h;
-        lo[1] = l;
-        *reinterpret_cast<u32x2 *>(q + (k & 4) * 2) = hi;
-        *reinterpret_cast<u32x2 *>(q + 16 + (k & 4) * 2) = lo;
+        uint32_t a[PL], b[PL];
+        split_pair<PL>(v[0], v[1], a);
+        split_pair<PL>(v[2], v[3], b);
+#pragma unroll
+        for (int j = 0; j < PL; ++j)
+            *reinterpret_cast<u32x2 *>(q + 16 * j + (k & 4) * 2) = u32x2{a[j], b[j]};
     } else {
         *reinterpret_cast<v4f *>(q + (k & 4) * 4) = v;
     }
 }
 // a result tile as it lies: this lane's 4 rows, `stride` bytes apart from the row
-// at p, at column col. Two neighbouring lanes pair up, one writes both high
-// words, the other both low ones. All lanes of a pair call it; live alike.
-template <bool BF> __device__ __forceinline__ void mid_store_rows(char *p, long long stride, int col, v4f v, bool live)
+// at p, at column col. Lanes of neighbouring columns exchange, so that each
+// writes whole words: two rows of both columns. All lanes of a pair call it.
+template <bool BF, int PL> __device__ __forceinline__ void mid_store_rows(char *p, int stride, int col, v4f v)
 {
+    char *q = p + col / 8 * mid8<BF, PL>;
     if constexpr (BF) {
         const int odd = col & 1;
-        char *q = p + (col & ~7) * 4 + (col & 6) * 2 + 16 * odd;
+        // the even lane takes rows 0 and 1, the odd one 2 and 3
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t hi, lo;
-            split_pair(v[i], 0.0f, hi, lo);
-            const uint32_t both = (hi & 0xFFFFu) | (lo << 16);
-            const uint32_t other = __shfl_xor(both, 1);
-            const uint32_t w = odd ? (other >> 16) | (both & 0xFFFF0000u) : (both & 0xFFFFu) | (other << 16);
-            if (live)
-                *reinterpret_cast<uint32_t *>(q + i * stride) = w;
+        for (int i = 0; i < 2; ++i) {
+            const float mine = odd ? v[2 + i] : v[i], give = odd ? v[i] : v[2 + i];
+            const float got = __shfl_xor(give, 1);
+            uint32_t w[PL];
+            split_pair<PL>(odd ? got : mine, odd ? mine : got, w);
+#pragma unroll
+            for (int j = 0; j < PL; ++j)
+                *reinterpret_cast<uint32_t *>(q + (2 * odd + i) * stride + 16 * j + (col & 6) * 2) = w[j];
         }
     } else {
-        if (live)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float *>(p + i * stride + col * 4) = v[i];
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float *>(q + i * stride + (col & 7) * 4) = v[i];
     }
 }
-// sum of the products of two operands' values
-__device__ __forceinline__ float mid_dot(const Mid<true> &a, const Mid<true> &b)
+// 8 fp32 values from memory, o in values, zeros where not live
+__device__ __forceinline__ void load8(const Buf &b, int o, bool live, float (&v)[8])
 {
-    u32x4 ah, al, bh, bl;
-    __builtin_memcpy(&ah, &a.hi, 16);
-    __builtin_memcpy(&al, &a.lo, 16);
-    __builtin_memcpy(&bh, &b.hi, 16);
-    __builtin_memcpy(&bl, &b.lo, 16);
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        s = fmaf(bf16_lo(ah[j]) + bf16_lo(al[j]), bf16_lo(bh[j]) + bf16_lo(bl[j]), s);
-        s = fmaf(bf16_hi(ah[j]) + bf16_hi(al[j]), bf16_hi(bh[j]) + bf16_hi(bl[j]), s);
-    }
-    return s;
-}
-__device__ __forceinline__ float mid_dot(const Mid<false> &a, const Mid<false> &b)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        s = fmaf(a.v[j], b.v[j], s);
-    return s;
+    const unsigned at = live ? 4u * o : NOWHERE;
+    const u32x4 t[2] = {buf16(b, at), buf16(b, at + 16)};
+    __builtin_memcpy(v, t, 32);
 }
 
 // ---- a chunk's rows of q or k in LDS, read down the tokens
@@ -229,6 +290,20 @@ template <bool BF, int KD> struct Rows {
     __device__ __forceinline__ void put(int r, int k, const In<BF> &f)
     {
         __builtin_memcpy(__builtin_assume_aligned(&e[r][k], 16), &f, sizeof f);
+    }
+    // operand: row r, reduction along it from element k on
+    __device__ __forceinline__ In<BF> across(int r, int k) const
+    {
+        In<BF> f;
+        __builtin_memcpy(&f, __builtin_assume_aligned(&e[r][k], 16), sizeof f);
+        return f;
+    }
+    __device__ __forceinline__ float at(int r, int k) const
+    {
+        if constexpr (BF)
+            return bf16_one(e[r][k]);
+        else
+            return e[r][k];
     }
     // operand: columns col0 .. + 15, reduction over tokens tok0 .. + 31
     __device__ __forceinline__ In<BF> down(int tok0, int col0) const

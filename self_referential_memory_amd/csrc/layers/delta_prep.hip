@@ -54,6 +54,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
     }
 
     const long long tok = static_cast<long long>(b) * a.T + tok0;
+    const Buf bk(a.k, (tok * a.ks + static_cast<long long>(hk) * a.Dk) * (BF ? 2 : 4));
+    const Buf bq(a.q, (tok * a.qs + static_cast<long long>(hk) * a.Dk) * (BF ? 2 : 4));
+    const int ks = static_cast<int>(a.ks), qs = static_cast<int>(a.qs);
     const int row = 16 * wave + l15;
     In<BF> kf[KF], qf[KF];
     float kk = 0.0f, qq = 0.0f;
@@ -61,8 +64,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
     for (int f = 0; f < KF; ++f) {
         const int k = 32 * f + 8 * quad;
         const bool live = tok0 + row < n && k < a.Dk;
-        kf[f] = in_load<BF>(a.k, (tok + row) * a.ks + static_cast<long long>(hk) * a.Dk + k, live);
-        qf[f] = in_load<BF>(a.q, (tok + row) * a.qs + static_cast<long long>(hk) * a.Dk + k, live);
+        kf[f] = in_load<BF>(bk, row * ks + k, live);
+        qf[f] = in_load<BF>(bq, row * qs + k, live);
         kk += in_squares(kf[f]);
         qq += in_squares(qf[f]);
     }
@@ -97,8 +100,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
 #pragma unroll
         for (int f = 0; f < KF; ++f) {
             const int k = 32 * f + 8 * quad;
-            const In<BF> o = in_load<BF>(a.k, (tok + col) * a.ks + static_cast<long long>(hk) * a.Dk + k,
-                                         tok0 + col < n && k < a.Dk);
+            const In<BF> o = in_load<BF>(bk, col * ks + k, tok0 + col < n && k < a.Dk);
             m = mma(kf[f], o, m);
             p[j] = mma(qf[f], o, p[j]);
         }
@@ -158,8 +160,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
         for (int r = 0; r < 4; ++r)
             L[16 * wave + 4 * quad + r][16 * j + l15] = p[j][r];
     __syncthreads();
-    char *xo = a.X + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 256;
-    char *po = a.P + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 256;
+    // P itself meets outputs alone, its transpose the states' gradients
+    constexpr int PP = TRANSPOSED ? 3 : 2;
+    char *xo = a.X + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 8 * mid8<BF, 3>;
+    char *po = a.P + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 8 * mid8<BF, PP>;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
         const int k = 32 * f + 8 * quad;
@@ -169,8 +173,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
             x[e] = TRANSPOSED ? X[k + e][row] : X[row][k + e];
             y[e] = TRANSPOSED ? L[k + e][row] : L[row][k + e];
         }
-        mid_store8<BF>(xo + 4 * k, x);
-        mid_store8<BF>(po + 4 * k, y);
+        mid_store8<BF, 3>(xo + k / 8 * mid8<BF, 3>, x);
+        mid_store8<BF, PP>(po + k / 8 * mid8<BF, PP>, y);
     }
 }
 
