@@ -24,9 +24,10 @@ namespace srnl_i {
 
 constexpr int DELTA_CHUNK = 64;
 constexpr int DELTA_SQUARE = 64 * 64 * 6;      // bytes of X or P of one chunk, at most
-// a chunk's row factors: e^G, e^(G_63 - G), beta, 1/|k|, 1/|q|, G in two floats
-enum { VEC_GAM = 0, VEC_END = 64, VEC_BETA = 128, VEC_RK = 192, VEC_RQ = 256, VEC_GHI = 320, VEC_GLO = 384,
-       VEC_FLOATS = 448 };
+// a chunk's row factors: what the chain takes at once (e^G / |k|, e^(G_63 - G) beta
+// / |k|, beta, scale e^G / |q|), and e^G, e^(G_63 - G), 1/|k|, 1/|q|, G in two floats
+enum { VEC_READK = 0, VEC_WRITE = 64, VEC_BETA = 128, VEC_READQ = 192, VEC_GAM = 256, VEC_END = 320, VEC_RK = 384,
+       VEC_RQ = 448, VEC_GHI = 512, VEC_GLO = 576, VEC_FLOATS = 640 };
 
 // One call: the public parameters with strides filled in, and its buffers.
 struct DeltaArgs {
@@ -41,7 +42,7 @@ struct DeltaArgs {
     float *state_out;
     int N;                       // chunks of an item
     // per (item, head, chunk), in this order
-    char *X, *P;                 // [64][64] split values
+    char *X, *P;                 // [64][64] split values, as operands
     float *vec;                  // [VEC_FLOATS]
     float *E;                    // record: [64][Dv]
     float *S0;                   // record: [Dk][Dv]

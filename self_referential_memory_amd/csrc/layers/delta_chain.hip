@@ -21,12 +21,39 @@ using namespace srnl_i;
 // after the other.
 template <int KD, int NV> struct Slab {
     static constexpr int NT = NV / 16, TILES = KD / 16 * NT, MINE = (TILES + 3) / 4;
+    static constexpr int COLS = MINE < NT ? MINE : NT;      // columns of tiles a wave has
     int wave, quad, l15;
     __device__ __forceinline__ bool live(int i) const { return TILES % 4 == 0 || wave * MINE + i < TILES; }
     __device__ __forceinline__ int row16(int i) const { return 16 * ((wave * MINE + i) / NT); }
     __device__ __forceinline__ int row(int i) const { return row16(i) + 4 * quad; }
     __device__ __forceinline__ int col(int i) const { return 16 * ((wave * MINE + i) % NT) + l15; }
+    __device__ __forceinline__ int col0() const { return COLS < NT ? 16 * (wave * MINE % NT) : 0; }
+    // k or q down the chunk's tokens, for every tile
+    template <bool BF> __device__ __forceinline__ void down(const Rows<BF, KD> &r, In<BF> (&f)[2][MINE]) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < MINE; ++i)
+                f[h][i] = i % COLS ? f[h][i - 1] : live(i) ? r.down(32 * h, row16(i)) : in_zero<BF>();
+    }
 };
+
+// The operands that a wave reads of a transposed array in LDS: N reductions of 32
+// for each of NT columns of tiles, all at once, so that the products do not wait
+// for them one by one.
+template <bool BF, int PL, int N, int NT, int STRIDE>
+__device__ __forceinline__ void read_columns(const char (*p)[STRIDE], int step, int quad, int l15, Mid<BF, PL> (&f)[N][NT])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            f[i][j] = mid_load<BF, PL>(p[16 * j + l15] + (4 * i + quad) * step);
+}
+// (A chunk's loads are issued without a condition, the last chunk's again at the end:
+// behind a branch that may have issued loads, a wait for earlier ones waits for all.)
+__device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 // What every wave of a block knows.
 template <int NV> struct Place {
@@ -34,9 +61,12 @@ template <int NV> struct Place {
     bool helper;
     __device__ __forceinline__ explicit Place(const DeltaArgs &a)
     {
-        const int slabs = (a.Dv + NV - 1) / NV;
-        bh = blockIdx.x / slabs;
-        v0 = (blockIdx.x - bh * slabs) * NV;
+        // A head's slabs read the same q, k, X and P: of every eight heads each goes
+        // to one XCD (blocks go round the eight), whose L2 then serves all its slabs.
+        const int slabs = (a.Dv + NV - 1) / NV, full = a.B * a.H / 8 * 8;
+        const int i = blockIdx.x, rest = i - full * slabs;
+        bh = rest < 0 ? i % 8 + i / (8 * slabs) * 8 : full + rest / slabs;
+        v0 = (rest < 0 ? i / 8 % slabs : rest % slabs) * NV;
         b = bh / a.H;
         h = bh - b * a.H;
         hk = h / (a.H / a.Hk);
@@ -70,41 +100,92 @@ __device__ __forceinline__ void load_rows(const DeltaArgs &a, const P &pl, const
     const int o = pl.row * static_cast<int>(stride) + 8 * pl.quad;
 #pragma unroll
     for (int i = 0; i < KF; ++i)
-        f[i] = in_load<BF>(b, o + 32 * i, live && 32 * i + 8 * pl.quad < a.Dk);
+        f[i] = in_load<BF>(b, o + 32 * i, both(live, 32 * i + 8 * pl.quad < a.Dk));
 }
-// this wave's 16 rows of X or P
-template <bool BF, int PL, class P>
+// this wave's 16 rows of X or P, lower triangular (UPPER: of their transposes): the
+// waves whose half of 32 is zero leave it out, here and in the products
+template <bool UPPER> __device__ __forceinline__ bool half_live(int wave, int i) { return i == UPPER || (UPPER ? wave < 2 : wave >= 2); }
+template <bool BF, int PL, bool UPPER, class P>
 __device__ __forceinline__ void load_square(const DeltaArgs &a, const P &pl, const char *p, int c, Mid<BF, PL> (&f)[2])
 {
     const Buf b(p, pl.at(a, c) * DELTA_SQUARE);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        f[i] = mid_load<BF, PL>(b, (pl.row * 8 + pl.quad + 4 * i) * mid8<BF, PL>);
+    if (half_live<UPPER>(pl.wave, !UPPER))
+        f[!UPPER] = frag_load<BF, PL>(b, 2 * pl.wave + !UPPER);
+    f[UPPER] = frag_load<BF, PL>(b, 2 * pl.wave + UPPER);
 }
-// this wave's rows of a [tokens][H][Dv] array, as a result tile
+// This wave's rows of a [tokens][H][Dv] array, as result tiles. Of bf16 ones a lane
+// loads two neighbouring columns in two of its four rows, and has the rest from the
+// lane beside it: half the loads.
+template <bool BF> struct Column { uint32_t w[2]; };
+template <> struct Column<false> { float v[4]; };
 template <bool BF, int NT, class P>
 __device__ __forceinline__ void load_values(const DeltaArgs &a, const P &pl, const void *p, long long stride, int c,
-                                            Raw<BF> (&v)[NT][4])
+                                            Column<BF> (&v)[NT])
 {
     const Buf b(p, (pl.token(a, c) * stride + static_cast<long long>(pl.h) * a.Dv + pl.v0) * (BF ? 2 : 4));
     const int left = pl.n - DELTA_CHUNK * c;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+        const int col = 16 * j + pl.l15;
+        if constexpr (BF) {
+            const int odd = pl.l15 & 1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            v[j][e] = raw_load<BF>(b, (pl.rows + e) * static_cast<int>(stride) + 16 * j + pl.l15,
-                                   pl.rows + e < left && pl.v0 + 16 * j + pl.l15 < a.Dv);
+            for (int i = 0; i < 2; ++i) {
+                const int r = pl.rows + 2 * odd + i;
+                const bool live = both(r < left, pl.v0 + col < a.Dv);
+                v[j].w[i] = __builtin_amdgcn_raw_buffer_load_b32(
+                    b.r, live ? 2u * (r * static_cast<int>(stride) + col - odd) : NOWHERE, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool live = both(pl.rows + e < left, pl.v0 + col < a.Dv);
+                v[j].v[e] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                    b.r, live ? 4u * ((pl.rows + e) * static_cast<int>(stride) + col) : NOWHERE, 0, 0));
+            }
+        }
+    }
 }
+__device__ __forceinline__ v4f values(const Column<true> &c)
+{
+    const int odd = threadIdx.x & 1;
+    v4f v;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t other = __shfl_xor(c.w[i], 1);
+        // even: this lane's rows 0 and 1, the other's rows 2 and 3, low halves
+        v[i] = odd ? bf16_hi(other) : bf16_lo(c.w[i]);
+        v[2 + i] = odd ? bf16_hi(c.w[i]) : bf16_lo(other);
+    }
+    return v;
+}
+__device__ __forceinline__ v4f values(const Column<false> &c) { return v4f{c.v[0], c.v[1], c.v[2], c.v[3]}; }
 // ... and its outputs; tokens past the item's length get zeros
 template <bool BF, class P>
 __device__ __forceinline__ void store_values(const DeltaArgs &a, const P &pl, void *p, int c, int j, v4f v)
 {
     const Buf b(p, ((pl.token(a, c) * a.H + pl.h) * a.Dv + pl.v0) * (BF ? 2 : 4));
     const int left = pl.n - DELTA_CHUNK * c, inside = a.T - DELTA_CHUNK * c;
+    const int col = 16 * j + pl.l15;
+    if constexpr (BF) {
+        // lanes of neighbouring columns exchange: each writes two rows of both
+        const int odd = pl.l15 & 1;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        put_value<BF>(b, (pl.rows + e) * a.H * a.Dv + 16 * j + pl.l15,
-                      pl.rows + e < inside && pl.v0 + 16 * j + pl.l15 < a.Dv, pl.rows + e < left ? v[e] : 0.0f);
+        for (int i = 0; i < 2; ++i) {
+            const float mine = odd ? v[2 + i] : v[i], give = odd ? v[i] : v[2 + i];
+            const float got = __shfl_xor(give, 1);
+            const int r = pl.rows + 2 * odd + i;
+            const uint32_t w = odd ? pack_bf16(got, mine) : pack_bf16(mine, got);
+            const bool live = both(r < inside, pl.v0 + col < a.Dv);
+            __builtin_amdgcn_raw_buffer_store_b32(r < left ? w : 0u, b.r,
+                                                  live ? 2u * (r * a.H * a.Dv + col - odd) : NOWHERE, 0, 0);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            put_value<false>(b, (pl.rows + e) * a.H * a.Dv + col, both(pl.rows + e < inside, pl.v0 + col < a.Dv),
+                             pl.rows + e < left ? v[e] : 0.0f);
+    }
 }
 // this wave's rows of a [64][Dv] fp32 array
 template <class P> __device__ __forceinline__ void store_rows(const DeltaArgs &a, const P &pl, float *p, int c, int j, v4f v)
@@ -123,19 +204,29 @@ template <bool BF, int NV> __device__ __forceinline__ void zero_values(const Del
             put_at<BF>(p, ((pl.token(a, pl.chunks) + i / NV) * a.H + pl.h) * a.Dv + col, 0.0f);
     }
 }
-// this wave's rows of a chunk's factors, and the chunk's whole decay
+// A chunk's row factors go through LDS: two helpers load them for the whole block
+// (a load costs the same for 16 bytes a lane as for the 64 bytes that four rows'
+// factors are), two buffers taking turns.
 struct Factors {
-    v4f gam, end, beta, rk, rq;
-    float last;
+    __attribute__((aligned(16))) float row[256];     // from VEC_READK on
+    float last;                                      // e^(G_63)
+    __device__ __forceinline__ v4f rows(int which, int r) const { return *reinterpret_cast<const v4f *>(&row[which + r]); }
 };
-template <class P> __device__ __forceinline__ Factors load_factors(const DeltaArgs &a, const P &pl, int c)
-{
-    const Buf b(a.vec, pl.at(a, c) * VEC_FLOATS * 4);
-    const auto four = [&](int which) { return __builtin_bit_cast(v4f, buf16(b, 4 * (which + pl.rows))); };
-    Factors f = {four(VEC_GAM), four(VEC_END), four(VEC_BETA), four(VEC_RK), four(VEC_RQ), 0.0f};
-    f.last = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b.r, 4 * (VEC_GAM + 63), 0, 0));
-    return f;
-}
+struct Vec {
+    u32x4 w;
+    template <class P> __device__ __forceinline__ void load(const DeltaArgs &a, const P &pl, int c)
+    {
+        const Buf b(a.vec, pl.at(a, c) * VEC_FLOATS * 4);
+        w = buf16(b, pl.wave == 0 ? 16 * (threadIdx.x & 63) : pl.wave == 1 ? 4 * (VEC_GAM + 63) : NOWHERE);
+    }
+    __device__ __forceinline__ void store(Factors &f, int wave) const
+    {
+        if (wave == 0)
+            *reinterpret_cast<u32x4 *>(&f.row[4 * (threadIdx.x & 63)]) = w;
+        else if (wave == 1)
+            f.last = __builtin_bit_cast(float, w[0]);
+    }
+};
 // the state's slab from memory, and back
 template <int KD, int NV>
 __device__ __forceinline__ void load_state(const DeltaArgs &a, const Place<NV> &pl, const Slab<KD, NV> &sl, const float *p,
@@ -160,7 +251,7 @@ __device__ __forceinline__ void store_state(const DeltaArgs &a, const Place<NV> 
 #pragma unroll
     for (int i = 0; i < Slab<KD, NV>::MINE; ++i) {
         // rows go in fours, Dk in eights
-        const bool live = sl.live(i) && sl.row(i) < a.Dk && pl.v0 + sl.col(i) < a.Dv;
+        const bool live = both(both(sl.live(i), sl.row(i) < a.Dk), pl.v0 + sl.col(i) < a.Dv);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             put_value<false>(b, (sl.row(i) + e) * a.Dv + sl.col(i), live, S[i][e]);
@@ -173,30 +264,36 @@ template <bool BF, int KD, int NV> struct FwdShared {
     __attribute__((aligned(16))) Rows<BF, KD> k;
     __attribute__((aligned(16))) char S[NV][mid_row<BF, 3>(KD)];       // the state, transposed
     __attribute__((aligned(16))) char R[NV][mid_row<BF, 3>(64)], U[NV][mid_row<BF, 2>(64)], W[NV][mid_row<BF, 3>(64)];
+    Factors w[2];
 };
 
-template <bool BF, int KF, int NT> struct ChainIn {
+// What the chain reads of a chunk, in two parts, so that its loads and the helpers'
+// take turns.
+template <bool BF, int KF, int NT, bool BACK> struct ChainIn {
     In<BF> k[KF];
-    Mid<BF, 3> x[2];
-    Raw<BF> v[NT][4];
-    Factors w;
+    Mid<BF, 3> x[2];                  // of X, backward of its transpose
+    Column<BF> v[NT];                 // forward
     template <class P> __device__ __forceinline__ void load(const DeltaArgs &a, const P &pl, int c)
     {
         load_rows<BF, KF>(a, pl, a.k, a.ks, c, k);
-        load_square<BF, 3>(a, pl, a.X, c, x);
-        load_values<BF, NT>(a, pl, a.v, a.vs, c, v);
-        w = load_factors(a, pl, c);
+        if (!BACK)
+            load_values<BF, NT>(a, pl, a.v, a.vs, c, v);
+    }
+    template <class P> __device__ __forceinline__ void load_x(const DeltaArgs &a, const P &pl, int c)
+    {
+        load_square<BF, 3, BACK>(a, pl, a.X, c, x);
     }
 };
 template <bool BF, int KF> struct OutIn {
     In<BF> q[KF];
     Mid<BF, 2> p[2];
-    Factors w;
+    Vec vec;                          // the next chunk's
     template <class P> __device__ __forceinline__ void load(const DeltaArgs &a, const P &pl, int c)
     {
-        load_rows<BF, KF>(a, pl, a.q, a.qs, c, q);
-        load_square<BF, 2>(a, pl, a.P, c, p);
-        w = load_factors(a, pl, c);
+        const int last = pl.chunks - 1;
+        load_rows<BF, KF>(a, pl, a.q, a.qs, c < last ? c : last, q);
+        load_square<BF, 2, false>(a, pl, a.P, c < last ? c : last, p);
+        vec.load(a, pl, c + 1 < last ? c + 1 : last);
     }
 };
 
@@ -215,69 +312,76 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             if (sl.live(i))
                 mid_store4<BF, 3>(sh.S[sl.col(i)], sl.row(i), S[i]);
         __builtin_amdgcn_s_setprio(2);
-        const auto chunk = [&](const ChainIn<BF, KF, NT> &in, ChainIn<BF, KF, NT> &next, int c) __attribute__((always_inline)) {
-            if (c + 1 < pl.chunks)
-                next.load(a, pl, c + 1);
+        const auto chunk = [&](const ChainIn<BF, KF, NT, false> &in, ChainIn<BF, KF, NT, false> &next, int c) __attribute__((always_inline)) {
+            Mid<BF, 3> op[KF][NT];
+            read_columns<BF, 3>(sh.S, S8, pl.quad, pl.l15, op);
+            hold();
+            Sum<BF, 3> kS[NT];
+#pragma unroll
+            for (int f = 0; f < KF; ++f)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    kS[j].add(in.k[f], op[f][j]);
+            const int after = c + 1 < pl.chunks ? c + 1 : c;
+            next.load(a, pl, after);
+            const Factors &w = sh.w[c & 1];
+            const v4f read = w.rows(VEC_READK, pl.rows);
 #pragma unroll
             for (int f = 0; f < KF; ++f)
                 sh.k.put(pl.row, 32 * f + 8 * pl.quad, in.k[f]);
-            const v4f read = in.w.gam * in.w.rk, write = in.w.end * in.w.rk;
-            v4f kS[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                kS[j] = v4f_zero();
-#pragma unroll
-            for (int f = 0; f < KF; ++f)
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    kS[j] = mma(in.k[f], mid_load<BF, 3>(sh.S[16 * j + pl.l15] + (4 * f + pl.quad) * S8), kS[j]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                v4f r;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    r[e] = value(in.v[j][e]) - read[e] * kS[j][e];
-                mid_store4<BF, 3>(sh.R[16 * j + pl.l15], pl.rows, r);
+                mid_store4<BF, 3>(sh.R[16 * j + pl.l15], pl.rows, values(in.v[j]) - read * kS[j].value());
             }
+            lds_barrier();
+            const v4f write = w.rows(VEC_WRITE, pl.rows), beta = w.rows(VEC_BETA, pl.rows);
+            Mid<BF, 3> rs[2][NT];
+            read_columns<BF, 3>(sh.R, S8, pl.quad, pl.l15, rs);
+            hold();
+            Sum<BF, 3> err[NT];
+#pragma unroll
+            for (int f = 0; f < 2; ++f)
+                if (half_live<false>(pl.wave, f))
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+                        err[j].add(in.x[f], rs[f][j]);
+            next.load_x(a, pl, after);
             if (RECORD)
                 store_state<KD, NV>(a, pl, sl, a.S0, pl.at(a, c), S);
-            lds_barrier();
-            v4f err[NT];
+            In<BF> kd[2][Sl::MINE];
+            sl.template down<BF>(sh.k, kd);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                err[j] = v4f_zero();
+            for (int j = 0; j < NT; ++j) {
+                const v4f e = err[j].value();
+                mid_store4<BF, 3>(sh.W[16 * j + pl.l15], pl.rows, write * e);
+                mid_store4<BF, 2>(sh.U[16 * j + pl.l15], pl.rows, beta * e);
+                if (RECORD)
+                    store_rows(a, pl, a.E, c, j, e);
+            }
+            lds_barrier();
+            const float last = w.last;
+            Mid<BF, 3> ws[2][Sl::COLS];
+            read_columns<BF, 3>(sh.W + sl.col0(), S8, pl.quad, pl.l15, ws);
+            hold();
+            Sum<BF, 3> dS[Sl::MINE];
 #pragma unroll
             for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    err[j] = mma(in.x[f], mid_load<BF, 3>(sh.R[16 * j + pl.l15] + (4 * f + pl.quad) * S8), err[j]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const v4f u = in.w.beta * err[j];
-                mid_store4<BF, 3>(sh.W[16 * j + pl.l15], pl.rows, write * u);
-                mid_store4<BF, 2>(sh.U[16 * j + pl.l15], pl.rows, u);
-            }
-            if (RECORD) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    store_rows(a, pl, a.E, c, j, err[j]);
-            }
-            lds_barrier();
+                for (int i = 0; i < Sl::MINE; ++i)
+                    dS[i].add(kd[f][i], ws[f][i % Sl::COLS]);
 #pragma unroll
             for (int i = 0; i < Sl::MINE; ++i) {
-                if (!sl.live(i))
-                    continue;
-                S[i] *= in.w.last;
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    S[i] = mma(sh.k.down(32 * f, sl.row16(i)), mid_load<BF, 3>(sh.W[sl.col(i)] + (4 * f + pl.quad) * S8), S[i]);
-                mid_store4<BF, 3>(sh.S[sl.col(i)], sl.row(i), S[i]);
+                S[i] = S[i] * last + dS[i].value();
+                if (sl.live(i))
+                    mid_store4<BF, 3>(sh.S[sl.col(i)], sl.row(i), S[i]);
             }
             lds_barrier();
         };
-        ChainIn<BF, KF, NT> in[2];
-        if (pl.chunks)
+        ChainIn<BF, KF, NT, false> in[2];
+        if (pl.chunks) {
             in[0].load(a, pl, 0);
+            in[0].load_x(a, pl, 0);
+        }
         lds_barrier();
         for (int c = 0; c < pl.chunks; c += 2) {
             chunk(in[0], in[1], c);
@@ -288,32 +392,37 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             store_state<KD, NV>(a, pl, sl, a.state_out, pl.bh, S);
     } else {
         const auto chunk = [&](const OutIn<BF, KF> &in, OutIn<BF, KF> &next, int c) __attribute__((always_inline)) {
-            if (c + 1 < pl.chunks)
-                next.load(a, pl, c + 1);
-            v4f o[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                o[j] = v4f_zero();
+            Sum<BF, 2> qS[NT];
 #pragma unroll
             for (int f = 0; f < KF; ++f)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    o[j] = mma(in.q[f], mid_load<BF, 2>(sh.S[16 * j + pl.l15] + (4 * f + pl.quad) * S8), o[j]);
+                    qS[j].add(in.q[f], mid_load<BF, 2>(sh.S[16 * j + pl.l15] + (4 * f + pl.quad) * S8));
+            const v4f read = sh.w[c & 1].rows(VEC_READQ, pl.rows);
             lds_barrier();
+            next.load(a, pl, c + 1);
             lds_barrier();
+            in.vec.store(sh.w[(c + 1) & 1], pl.wave);
+            Mid<BF, 2> us[2][NT];
+            read_columns<BF, 2>(sh.U, mid8<BF, 2>, pl.quad, pl.l15, us);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                o[j] *= in.w.gam * in.w.rq * a.scale;
+                Sum<BF, 2> pU;
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
-                    o[j] = mma(in.p[f], mid_load<BF, 2>(sh.U[16 * j + pl.l15] + (4 * f + pl.quad) * mid8<BF, 2>), o[j]);
-                store_values<BF>(a, pl, a.out, c, j, o[j]);
+                    if (half_live<false>(pl.wave, f))
+                        pU.add(in.p[f], us[f][j]);
+                store_values<BF>(a, pl, a.out, c, j, read * qS[j].value() + pU.value());
             }
             lds_barrier();
         };
         OutIn<BF, KF> in[2];
-        if (pl.chunks)
+        if (pl.chunks) {
+            Vec first;
+            first.load(a, pl, 0);
             in[0].load(a, pl, 0);
+            first.store(sh.w[0], pl.wave);
+        }
         lds_barrier();
         for (int c = 0; c < pl.chunks; c += 2) {
             chunk(in[0], in[1], c);
@@ -335,30 +444,23 @@ template <bool BF, int KD, int NV> struct BwdShared {
     __attribute__((aligned(16))) char O[NV][mid_row<BF, 1>(64)];       // dO, transposed
     // what the helpers hand to the chain, as result tiles: P^T dO and Q^T dO
     v4f po[4][NV / 16][64], qo[4][Sl::MINE][64];
+    Factors w[2];
 };
 
-template <bool BF, int KF> struct ChainBack {
-    In<BF> k[KF];
-    Mid<BF, 3> x[2];                  // of X's transpose
-    Factors w;
-    template <class P> __device__ __forceinline__ void load(const DeltaArgs &a, const P &pl, int c)
-    {
-        load_rows<BF, KF>(a, pl, a.k, a.ks, c, k);
-        load_square<BF, 3>(a, pl, a.X, c, x);
-        w = load_factors(a, pl, c);
-    }
-};
 template <bool BF, int KF, int NT> struct HelpBack {
     In<BF> q[KF];
     Mid<BF, 3> p[2];                  // of P's transpose
-    Raw<BF> o[NT][4];
-    Factors w;
+    Column<BF> o[NT];
+    v4f read;                         // scale e^G / |q|
+    Vec vec;
     template <class P> __device__ __forceinline__ void load(const DeltaArgs &a, const P &pl, int c)
     {
         load_rows<BF, KF>(a, pl, a.q, a.qs, c, q);
-        load_square<BF, 3>(a, pl, a.P, c, p);
+        load_square<BF, 3, true>(a, pl, a.P, c, p);
         load_values<BF, NT>(a, pl, a.dout, static_cast<long long>(a.H) * a.Dv, c, o);
-        w = load_factors(a, pl, c);
+        const Buf b(a.vec, pl.at(a, c) * VEC_FLOATS * 4);
+        read = __builtin_bit_cast(v4f, buf16(b, 4 * (VEC_READQ + pl.rows)));
+        vec.load(a, pl, c);
     }
 };
 
@@ -378,63 +480,75 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             if (sl.live(i))
                 mid_store4<BF, 3>(sh.D[sl.col(i)], sl.row(i), D[i]);
         __builtin_amdgcn_s_setprio(2);
-        const auto chunk = [&](const ChainBack<BF, KF> &in, ChainBack<BF, KF> &next, int c) __attribute__((always_inline)) {
-            if (c > 0)
-                next.load(a, pl, c - 1);
+        const auto chunk = [&](const ChainIn<BF, KF, NT, true> &in, ChainIn<BF, KF, NT, true> &next, int c) __attribute__((always_inline)) {
+            Mid<BF, 3> op[KF][NT];
+            read_columns<BF, 3>(sh.D, S8, pl.quad, pl.l15, op);
+            hold();
+            Sum<BF, 3> kD[NT];
+#pragma unroll
+            for (int f = 0; f < KF; ++f)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    kD[j].add(in.k[f], op[f][j]);
+            const int after = c > 0 ? c - 1 : 0;
+            next.load(a, pl, after);
+            const Factors &w = sh.w[c & 1];
+            const v4f write = w.rows(VEC_WRITE, pl.rows), beta = w.rows(VEC_BETA, pl.rows);
 #pragma unroll
             for (int f = 0; f < KF; ++f)
                 sh.k.put(pl.row, 32 * f + 8 * pl.quad, in.k[f]);
-            const v4f read = in.w.gam * in.w.rk, write = in.w.end * in.w.rk;
-            v4f kD[NT];
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                kD[j] = v4f_zero();
+                mid_store4<BF, 3>(sh.W[16 * j + pl.l15], pl.rows,
+                                  write * kD[j].value() + beta * sh.po[pl.wave][j][lane]);
+            lds_barrier();
+            const v4f read = w.rows(VEC_READK, pl.rows);
+            Mid<BF, 3> ws[2][NT];
+            read_columns<BF, 3>(sh.W, S8, pl.quad, pl.l15, ws);
+            hold();
+            Sum<BF, 3> dv[NT];
 #pragma unroll
-            for (int f = 0; f < KF; ++f)
+            for (int f = 0; f < 2; ++f)
+                if (half_live<true>(pl.wave, f))
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    kD[j] = mma(in.k[f], mid_load<BF, 3>(sh.D[16 * j + pl.l15] + (4 * f + pl.quad) * S8), kD[j]);
+                    for (int j = 0; j < NT; ++j)
+                        dv[j].add(in.x[f], ws[f][j]);
+            next.load_x(a, pl, after);
+            store_state<KD, NV>(a, pl, sl, a.D1, pl.at(a, c), D);
+            In<BF> kd[2][Sl::MINE];
+            sl.template down<BF>(sh.k, kd);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const v4f du = write * kD[j] + sh.po[pl.wave][j][lane];
-                mid_store4<BF, 3>(sh.W[16 * j + pl.l15], pl.rows, in.w.beta * du);
+                const v4f d = dv[j].value();
+                mid_store4<BF, 3>(sh.V[16 * j + pl.l15], pl.rows, -read * d);
+                store_rows(a, pl, a.dV, c, j, d);
+                if (a.dv)
+                    store_values<BF>(a, pl, a.dv, c, j, d);
             }
-            store_state<KD, NV>(a, pl, sl, a.D1, pl.at(a, c), D);
             lds_barrier();
-            v4f dv[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                dv[j] = v4f_zero();
+            const float last = w.last;
+            Mid<BF, 3> vs[2][Sl::COLS];
+            read_columns<BF, 3>(sh.V + sl.col0(), S8, pl.quad, pl.l15, vs);
+            hold();
+            Sum<BF, 3> dD[Sl::MINE];
 #pragma unroll
             for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    dv[j] = mma(in.x[f], mid_load<BF, 3>(sh.W[16 * j + pl.l15] + (4 * f + pl.quad) * S8), dv[j]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-                mid_store4<BF, 3>(sh.V[16 * j + pl.l15], pl.rows, -read * dv[j]);
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                store_rows(a, pl, a.dV, c, j, dv[j]);
-                if (a.dv)
-                    store_values<BF>(a, pl, a.dv, c, j, dv[j]);
-            }
-            lds_barrier();
+                for (int i = 0; i < Sl::MINE; ++i)
+                    dD[i].add(kd[f][i], vs[f][i % Sl::COLS]);
 #pragma unroll
             for (int i = 0; i < Sl::MINE; ++i) {
-                if (!sl.live(i))
-                    continue;
-                D[i] = D[i] * in.w.last + sh.qo[pl.wave][i][lane];
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    D[i] = mma(sh.k.down(32 * f, sl.row16(i)), mid_load<BF, 3>(sh.V[sl.col(i)] + (4 * f + pl.quad) * S8), D[i]);
-                mid_store4<BF, 3>(sh.D[sl.col(i)], sl.row(i), D[i]);
+                D[i] = (D[i] * last + sh.qo[pl.wave][i][lane]) + dD[i].value();
+                if (sl.live(i))
+                    mid_store4<BF, 3>(sh.D[sl.col(i)], sl.row(i), D[i]);
             }
             lds_barrier();
         };
-        ChainBack<BF, KF> in[2];
-        if (pl.chunks)
+        ChainIn<BF, KF, NT, true> in[2];
+        if (pl.chunks) {
             in[0].load(a, pl, pl.chunks - 1);
+            in[0].load_x(a, pl, pl.chunks - 1);
+        }
         lds_barrier();
         lds_barrier();
         for (int c = pl.chunks - 1; c >= 0; c -= 2) {
@@ -446,16 +560,17 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             store_state<KD, NV>(a, pl, sl, a.dstate, pl.bh, D);
     } else {
         v4f qo[Sl::MINE];
-        // q and dO of a chunk to LDS
-        const auto spread = [&](const HelpBack<BF, KF, NT> &in) __attribute__((always_inline)) {
+        // q, dO and the factors of a chunk to LDS
+        const auto spread = [&](const HelpBack<BF, KF, NT> &in, int c) __attribute__((always_inline)) {
+            in.vec.store(sh.w[c & 1], pl.wave);
 #pragma unroll
             for (int f = 0; f < KF; ++f)
                 sh.q.put(pl.row, 32 * f + 8 * pl.quad, in.q[f]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const v4f o = {value(in.o[j][0]), value(in.o[j][1]), value(in.o[j][2]), value(in.o[j][3])};
+                const v4f o = values(in.o[j]);
                 mid_store4<BF, 1>(sh.O[16 * j + pl.l15], pl.rows, o);
-                mid_store4<BF, 3>(sh.Os[16 * j + pl.l15], pl.rows, in.w.gam * in.w.rq * a.scale * o);
+                mid_store4<BF, 3>(sh.Os[16 * j + pl.l15], pl.rows, in.read * o);
             }
         };
         // its parts P^T dO, to LDS, and Q^T dO, kept
@@ -465,6 +580,8 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
                 v4f o = v4f_zero();
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
+                    if (!half_live<true>(pl.wave, f))
+                        continue;
                     In<BF> d;
                     __builtin_memcpy(&d, __builtin_assume_aligned(sh.O[16 * j + pl.l15] + (4 * f + pl.quad) * mid8<BF, 1>, 16), sizeof d);
                     o = mma(in.p[f], d, o);
@@ -483,13 +600,12 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
         HelpBack<BF, KF, NT> in;
         if (pl.chunks) {
             in.load(a, pl, pl.chunks - 1);
-            spread(in);
+            spread(in, pl.chunks - 1);
         }
         lds_barrier();
         if (pl.chunks) {
             parts(in);
-            if (pl.chunks > 1)
-                in.load(a, pl, pl.chunks - 2);
+            in.load(a, pl, pl.chunks > 1 ? pl.chunks - 2 : 0);
         }
         lds_barrier();
         for (int c = pl.chunks - 1; c >= 0; --c) {
@@ -498,12 +614,11 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             for (int i = 0; i < Sl::MINE; ++i)
                 sh.qo[pl.wave][i][lane] = qo[i];
             if (c > 0)
-                spread(in);
+                spread(in, c - 1);
             lds_barrier();
             if (c > 0) {
                 parts(in);
-                if (c > 1)
-                    in.load(a, pl, c - 2);
+                in.load(a, pl, c > 1 ? c - 2 : 0);
             }
             lds_barrier();
             lds_barrier();

@@ -77,6 +77,59 @@ template <int PL> __device__ __forceinline__ v4f mma(const Mid<false, PL> &a, co
     return mma16(a.v, b.v, c);
 }
 
+// A result in parts: products of equal significance have a sum of their own, so
+// that no product waits for the one before it.
+template <bool BF, int PL> struct Sum {
+    v4f part[BF ? PL : 1];
+    __device__ __forceinline__ Sum()
+    {
+#pragma unroll
+        for (int j = 0; j < (BF ? PL : 1); ++j)
+            part[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __device__ __forceinline__ void add(const In<BF> &a, const Mid<BF, PL> &b)
+    {
+        if constexpr (BF) {
+#pragma unroll
+            for (int j = PL - 1; j >= 0; --j)
+                part[j] = mma16(a.v, b.p[j], part[j]);
+        } else {
+            part[0] = mma16(a.v, b.v, part[0]);
+        }
+    }
+    __device__ __forceinline__ void add(const Mid<BF, PL> &a, const In<BF> &b)
+    {
+        if constexpr (BF) {
+#pragma unroll
+            for (int j = PL - 1; j >= 0; --j)
+                part[j] = mma16(a.p[j], b.v, part[j]);
+        } else {
+            part[0] = mma16(a.v, b.v, part[0]);
+        }
+    }
+    __device__ __forceinline__ void add(const Mid<BF, PL> &a, const Mid<BF, PL> &b)
+    {
+        if constexpr (BF) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+#pragma unroll
+                for (int s = PL - 1; s >= i; --s)
+                    part[s] = mma16(a.p[i], b.p[s - i], part[s]);
+        } else {
+            part[0] = mma16(a.v, b.v, part[0]);
+        }
+    }
+    __device__ __forceinline__ v4f value() const
+    {
+        v4f v = part[BF ? PL - 1 : 0];
+        if constexpr (BF)
+#pragma unroll
+            for (int j = PL - 2; j >= 0; --j)
+                v += part[j];
+        return v;
+    }
+};
+
 __device__ __forceinline__ v4f v4f_zero() { return v4f{0.0f, 0.0f, 0.0f, 0.0f}; }
 
 // ---- memory
@@ -87,6 +140,8 @@ __device__ __forceinline__ v4f v4f_zero() { return v4f{0.0f, 0.0f, 0.0f, 0.0f}; 
 // before its value is used.
 
 constexpr unsigned NOWHERE = 0x80000000u;
+// a && b without the branch
+__device__ __forceinline__ bool both(bool a, bool b) { return (static_cast<int>(a) & static_cast<int>(b)) != 0; }
 struct Buf {
     __amdgpu_buffer_rsrc_t r;
     __device__ __forceinline__ Buf(const void *base, long long byte)
@@ -133,6 +188,12 @@ template <bool BF> __device__ __forceinline__ void put_at(void *p, long long o, 
 
 // ---- inputs
 
+template <bool BF> __device__ __forceinline__ In<BF> in_zero()
+{
+    In<BF> f;
+    __builtin_memset(&f, 0, sizeof f);
+    return f;
+}
 // 8 elements from element o (a multiple of 8) on, zeros where not live
 template <bool BF> __device__ __forceinline__ In<BF> in_load(const Buf &b, int o, bool live)
 {
@@ -177,14 +238,18 @@ template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_load(const
     __builtin_memcpy(&f, t, sizeof f);
     return f;
 }
-// ... in memory, at byte o
-template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_load(const Buf &b, unsigned o)
+// An operand of X or P in memory lies as a wave reads it, 16 bytes a lane after
+// 16 bytes a lane: rows of 64 values would have every lane of a load on a cache line
+// of its own, and the loads, not the products, set the chain's pace.
+template <bool BF, int PL> constexpr int frag_bytes = (BF ? PL : 2) * 1024;
+template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> frag_load(const Buf &b, int frag)
 {
     Mid<BF, PL> f;
     u32x4 t[BF ? PL : 2];
+    const unsigned at = frag * frag_bytes<BF, PL> + 16u * (threadIdx.x & 63);
 #pragma unroll
     for (int j = 0; j < (BF ? PL : 2); ++j)
-        t[j] = buf16(b, o + 16 * j);
+        t[j] = buf16(b, at + 1024 * j);
     __builtin_memcpy(&f, t, sizeof f);
     return f;
 }
@@ -228,6 +293,15 @@ template <bool BF, int PL> __device__ __forceinline__ void mid_store8(char *p, c
 #pragma unroll
     for (unsigned j = 0; j < sizeof f / 16; ++j)
         reinterpret_cast<u32x4 *>(p)[j] = t[j];
+}
+template <bool BF, int PL> __device__ __forceinline__ void frag_store(char *p, int frag, const float (&v)[8])
+{
+    const Mid<BF, PL> f = mid_split<BF, PL>(v);
+    u32x4 t[sizeof f / 16];
+    __builtin_memcpy(t, &f, sizeof f);
+#pragma unroll
+    for (unsigned j = 0; j < sizeof f / 16; ++j)
+        *reinterpret_cast<u32x4 *>(p + frag * frag_bytes<BF, PL> + 1024 * j + 16 * (threadIdx.x & 63)) = t[j];
 }
 // a result tile's column as a row of its transpose: 4 values at place k (a
 // multiple of 4) of the row at p

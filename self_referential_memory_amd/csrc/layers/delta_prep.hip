@@ -17,7 +17,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
 {
     constexpr int KF = KD / 32;
     __shared__ __attribute__((aligned(16))) float L[64][68], X[64][68];
-    __shared__ float ghi[64], glo[64], bet[64], rks[64], rqs[64];
+    __shared__ float ghi[64], glo[64], bet[64], rks[64], rqs[64], gam[64], end[64];
     const int c = blockIdx.x % a.N, bh = blockIdx.x / a.N;
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
     const int n = delta_tokens(a, b), tok0 = DELTA_CHUNK * c;
@@ -46,11 +46,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
         ghi[lane] = hi;
         glo[lane] = lo;
         bet[lane] = beta;
-        vec[VEC_GAM + lane] = expf(hi) * (1.0f + lo);
-        vec[VEC_END + lane] = expf(lhi) * (1.0f + static_cast<float>(left - lhi));
-        vec[VEC_BETA + lane] = beta;
-        vec[VEC_GHI + lane] = hi;
-        vec[VEC_GLO + lane] = lo;
+        gam[lane] = expf(hi) * (1.0f + lo);
+        end[lane] = expf(lhi) * (1.0f + static_cast<float>(left - lhi));
     }
 
     const long long tok = static_cast<long long>(b) * a.T + tok0;
@@ -80,10 +77,21 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
         const float rq = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(qq + a.eps) : 1.0f;
         rks[row] = rk;
         rqs[row] = rq;
-        vec[VEC_RK + row] = rk;
-        vec[VEC_RQ + row] = rq;
     }
     __syncthreads();
+    if (wave == 3) {
+        const float ga = gam[lane], en = end[lane], be = bet[lane], rk = rks[lane], rq = rqs[lane];
+        vec[VEC_GAM + lane] = ga;
+        vec[VEC_END + lane] = en;
+        vec[VEC_BETA + lane] = be;
+        vec[VEC_RK + lane] = rk;
+        vec[VEC_RQ + lane] = rq;
+        vec[VEC_GHI + lane] = ghi[lane];
+        vec[VEC_GLO + lane] = glo[lane];
+        vec[VEC_READK + lane] = ga * rk;
+        vec[VEC_WRITE + lane] = en * be * rk;
+        vec[VEC_READQ + lane] = a.scale * ga * rq;
+    }
 
     v4f p[4];
 #pragma unroll
@@ -162,8 +170,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
     __syncthreads();
     // P itself meets outputs alone, its transpose the states' gradients
     constexpr int PP = TRANSPOSED ? 3 : 2;
-    char *xo = a.X + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 8 * mid8<BF, 3>;
-    char *po = a.P + static_cast<long long>(blockIdx.x) * DELTA_SQUARE + row * 8 * mid8<BF, PP>;
+    char *xo = a.X + static_cast<long long>(blockIdx.x) * DELTA_SQUARE;
+    char *po = a.P + static_cast<long long>(blockIdx.x) * DELTA_SQUARE;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
         const int k = 32 * f + 8 * quad;
@@ -173,8 +181,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
             x[e] = TRANSPOSED ? X[k + e][row] : X[row][k + e];
             y[e] = TRANSPOSED ? L[k + e][row] : L[row][k + e];
         }
-        mid_store8<BF, 3>(xo + k / 8 * mid8<BF, 3>, x);
-        mid_store8<BF, PP>(po + k / 8 * mid8<BF, PP>, y);
+        frag_store<BF, 3>(xo, 2 * wave + f, x);
+        frag_store<BF, PP>(po, 2 * wave + f, y);
     }
 }
 
