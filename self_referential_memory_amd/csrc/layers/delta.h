@@ -53,6 +53,7 @@ struct DeltaArgs {
     float *dg, *dbeta, *dstate;
     float *dV;                   // [64][Dv]
     float *D1;                   // [Dk][Dv]
+    float *dq_part, *dk_part;    // [B][T][H][Dk], where heads share q and k
 };
 
 // The tokens of item b that count.

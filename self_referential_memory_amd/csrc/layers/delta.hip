@@ -6,7 +6,7 @@ namespace {
 
 using namespace srnl_i;
 
-constexpr long long MAX_BLOCKS = 1 << 23;       // of 256 threads, per launch
+constexpr long long MAX_BLOCKS = (1 << 23) - 1;  // of 512 threads, per launch
 
 srnl_status check_delta(const srnl_gated_delta_params *p)
 {
@@ -39,7 +39,7 @@ srnl_status check_delta(const srnl_gated_delta_params *p)
         if (static_cast<__int128>(p->B) * p->T * s >= (static_cast<__int128>(1) << 60))
             return fail(SRNL_ERR_ARG, "tensors too large");
     }
-    // a block per 16 columns or per 64 tokens of a head
+    // a block (of 512 threads at most) per 16 columns or per 64 tokens of a head
     const __int128 bh = static_cast<__int128>(p->B) * p->H;
     if (bh * ((p->Dv + 15) / 16) > MAX_BLOCKS || bh * ((p->T + 63LL) / 64) > MAX_BLOCKS)
         return fail(SRNL_ERR_ARG, "too many heads x tokens");
@@ -82,7 +82,12 @@ size_t state_bytes(const DeltaArgs &a) { return chunks_of(a) * a.Dk * a.Dv * 4; 
 
 size_t fwd_bytes(const DeltaArgs &a) { return 2 * square_bytes(a) + vec_bytes(a); }
 size_t record_bytes_of(const DeltaArgs &a) { return rows_bytes(a) + state_bytes(a); }
-size_t bwd_bytes(const DeltaArgs &a) { return fwd_bytes(a) + rows_bytes(a) + state_bytes(a); }
+// the parts of dq (or dk) of heads that share them
+size_t part_bytes(const DeltaArgs &a)
+{
+    return a.H > a.Hk ? static_cast<size_t>(a.B) * a.T * a.H * a.Dk * 4 : 0;
+}
+size_t bwd_bytes(const DeltaArgs &a) { return fwd_bytes(a) + rows_bytes(a) + state_bytes(a) + 2 * part_bytes(a); }
 
 char *place_squares(DeltaArgs &a, void *workspace)
 {
@@ -219,6 +224,8 @@ srnl_status srnl_gated_delta_bwd(const srnl_gated_delta_params *p, const void *d
     if (a.N) {
         a.dV = reinterpret_cast<float *>(place_squares(a, workspace));
         a.D1 = a.dV + rows_bytes(a) / 4;
+        a.dq_part = a.D1 + state_bytes(a) / 4;
+        a.dk_part = a.dq_part + part_bytes(a) / 4;
         place_record(a, record);
         s = launch_delta_prep(a, true, st);
         if (s != SRNL_OK)

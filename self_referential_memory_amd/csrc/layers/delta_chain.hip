@@ -42,14 +42,14 @@ template <int KD, int NV> struct Slab {
 // The operands that a wave reads of a transposed array in LDS: N reductions of 32
 // for each of NT columns of tiles, all at once, so that the products do not wait
 // for them one by one.
-template <bool BF, int PL, int N, int NT, int STRIDE>
-__device__ __forceinline__ void read_columns(const char (*p)[STRIDE], int step, int quad, int l15, Mid<BF, PL> (&f)[N][NT])
+template <bool BF, int PL, int ROWS, int K, int N, int NT>
+__device__ __forceinline__ void read_columns(const Split<BF, PL, ROWS, K> &p, int col0, int quad, int l15, Mid<BF, PL> (&f)[N][NT])
 {
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-            f[i][j] = mid_load<BF, PL>(p[16 * j + l15] + (4 * i + quad) * step);
+            f[i][j] = p.get(col0 + 16 * j + l15, 4 * i + quad);
 }
 // (A chunk's loads are issued without a condition, the last chunk's again at the end:
 // behind a branch that may have issued loads, a wait for earlier ones waits for all.)
@@ -152,7 +152,7 @@ __device__ __forceinline__ v4f values(const Column<true> &c)
     v4f v;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t other = __shfl_xor(c.w[i], 1);
+        const uint32_t other = beside(c.w[i]);
         // even: this lane's rows 0 and 1, the other's rows 2 and 3, low halves
         v[i] = odd ? bf16_hi(other) : bf16_lo(c.w[i]);
         v[2 + i] = odd ? bf16_hi(c.w[i]) : bf16_lo(other);
@@ -173,7 +173,7 @@ __device__ __forceinline__ void store_values(const DeltaArgs &a, const P &pl, vo
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float mine = odd ? v[2 + i] : v[i], give = odd ? v[i] : v[2 + i];
-            const float got = __shfl_xor(give, 1);
+            const float got = beside(give);
             const int r = pl.rows + 2 * odd + i;
             const uint32_t w = odd ? pack_bf16(got, mine) : pack_bf16(mine, got);
             const bool live = both(r < inside, pl.v0 + col < a.Dv);
@@ -262,8 +262,9 @@ __device__ __forceinline__ void store_state(const DeltaArgs &a, const Place<NV> 
 
 template <bool BF, int KD, int NV> struct FwdShared {
     __attribute__((aligned(16))) Rows<BF, KD> k;
-    __attribute__((aligned(16))) char S[NV][mid_row<BF, 3>(KD)];       // the state, transposed
-    __attribute__((aligned(16))) char R[NV][mid_row<BF, 3>(64)], U[NV][mid_row<BF, 2>(64)], W[NV][mid_row<BF, 3>(64)];
+    Split<BF, 3, NV, KD> S;                            // the state, transposed
+    Split<BF, 3, NV, 64> R, W;
+    Split<BF, 2, NV, 64> U;
     Factors w[2];
 };
 
@@ -299,7 +300,7 @@ template <bool BF, int KF> struct OutIn {
 
 template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512) void delta_chain_kernel(DeltaArgs a)
 {
-    constexpr int KF = KD / 32, NT = NV / 16, S8 = mid8<BF, 3>;
+    constexpr int KF = KD / 32, NT = NV / 16;
     using Sl = Slab<KD, NV>;
     __shared__ FwdShared<BF, KD, NV> sh;
     const Place<NV> pl(a);
@@ -310,11 +311,11 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
 #pragma unroll
         for (int i = 0; i < Sl::MINE; ++i)
             if (sl.live(i))
-                mid_store4<BF, 3>(sh.S[sl.col(i)], sl.row(i), S[i]);
+                sh.S.put4(sl.col(i), sl.row(i), S[i]);
         __builtin_amdgcn_s_setprio(2);
         const auto chunk = [&](const ChainIn<BF, KF, NT, false> &in, ChainIn<BF, KF, NT, false> &next, int c) __attribute__((always_inline)) {
             Mid<BF, 3> op[KF][NT];
-            read_columns<BF, 3>(sh.S, S8, pl.quad, pl.l15, op);
+            read_columns(sh.S, 0, pl.quad, pl.l15, op);
             hold();
             Sum<BF, 3> kS[NT];
 #pragma unroll
@@ -331,12 +332,12 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
                 sh.k.put(pl.row, 32 * f + 8 * pl.quad, in.k[f]);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                mid_store4<BF, 3>(sh.R[16 * j + pl.l15], pl.rows, values(in.v[j]) - read * kS[j].value());
+                sh.R.put4(16 * j + pl.l15, pl.rows, values(in.v[j]) - read * kS[j].value());
             }
             lds_barrier();
             const v4f write = w.rows(VEC_WRITE, pl.rows), beta = w.rows(VEC_BETA, pl.rows);
             Mid<BF, 3> rs[2][NT];
-            read_columns<BF, 3>(sh.R, S8, pl.quad, pl.l15, rs);
+            read_columns(sh.R, 0, pl.quad, pl.l15, rs);
             hold();
             Sum<BF, 3> err[NT];
 #pragma unroll
@@ -353,15 +354,15 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const v4f e = err[j].value();
-                mid_store4<BF, 3>(sh.W[16 * j + pl.l15], pl.rows, write * e);
-                mid_store4<BF, 2>(sh.U[16 * j + pl.l15], pl.rows, beta * e);
+                sh.W.put4(16 * j + pl.l15, pl.rows, write * e);
+                sh.U.put4(16 * j + pl.l15, pl.rows, beta * e);
                 if (RECORD)
                     store_rows(a, pl, a.E, c, j, e);
             }
             lds_barrier();
             const float last = w.last;
             Mid<BF, 3> ws[2][Sl::COLS];
-            read_columns<BF, 3>(sh.W + sl.col0(), S8, pl.quad, pl.l15, ws);
+            read_columns(sh.W, sl.col0(), pl.quad, pl.l15, ws);
             hold();
             Sum<BF, 3> dS[Sl::MINE];
 #pragma unroll
@@ -373,7 +374,7 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             for (int i = 0; i < Sl::MINE; ++i) {
                 S[i] = S[i] * last + dS[i].value();
                 if (sl.live(i))
-                    mid_store4<BF, 3>(sh.S[sl.col(i)], sl.row(i), S[i]);
+                    sh.S.put4(sl.col(i), sl.row(i), S[i]);
             }
             lds_barrier();
         };
@@ -397,14 +398,14 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             for (int f = 0; f < KF; ++f)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    qS[j].add(in.q[f], mid_load<BF, 2>(sh.S[16 * j + pl.l15] + (4 * f + pl.quad) * S8));
+                    qS[j].add(in.q[f], sh.S.template get<2>(16 * j + pl.l15, 4 * f + pl.quad));
             const v4f read = sh.w[c & 1].rows(VEC_READQ, pl.rows);
             lds_barrier();
             next.load(a, pl, c + 1);
             lds_barrier();
             in.vec.store(sh.w[(c + 1) & 1], pl.wave);
             Mid<BF, 2> us[2][NT];
-            read_columns<BF, 2>(sh.U, mid8<BF, 2>, pl.quad, pl.l15, us);
+            read_columns(sh.U, 0, pl.quad, pl.l15, us);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 Sum<BF, 2> pU;
@@ -438,10 +439,9 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
 template <bool BF, int KD, int NV> struct BwdShared {
     using Sl = Slab<KD, NV>;
     __attribute__((aligned(16))) Rows<BF, KD> k, q;
-    __attribute__((aligned(16))) char D[NV][mid_row<BF, 3>(KD)];       // the state's gradient, transposed
-    __attribute__((aligned(16))) char W[NV][mid_row<BF, 3>(64)], V[NV][mid_row<BF, 3>(64)];
-    __attribute__((aligned(16))) char Os[NV][mid_row<BF, 3>(64)];      // dO times scale e^G / |q|, transposed
-    __attribute__((aligned(16))) char O[NV][mid_row<BF, 1>(64)];       // dO, transposed
+    Split<BF, 3, NV, KD> D;                            // the state's gradient, transposed
+    Split<BF, 3, NV, 64> W, V, Os;                     // Os: dO times scale e^G / |q|
+    Split<BF, 1, NV, 64> O;                            // dO, transposed
     // what the helpers hand to the chain, as result tiles: P^T dO and Q^T dO
     v4f po[4][NV / 16][64], qo[4][Sl::MINE][64];
     Factors w[2];
@@ -466,7 +466,7 @@ template <bool BF, int KF, int NT> struct HelpBack {
 
 template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_chain_bwd_kernel(DeltaArgs a)
 {
-    constexpr int KF = KD / 32, NT = NV / 16, S8 = mid8<BF, 3>;
+    constexpr int KF = KD / 32, NT = NV / 16;
     using Sl = Slab<KD, NV>;
     __shared__ BwdShared<BF, KD, NV> sh;
     const Place<NV> pl(a);
@@ -478,11 +478,11 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
 #pragma unroll
         for (int i = 0; i < Sl::MINE; ++i)
             if (sl.live(i))
-                mid_store4<BF, 3>(sh.D[sl.col(i)], sl.row(i), D[i]);
+                sh.D.put4(sl.col(i), sl.row(i), D[i]);
         __builtin_amdgcn_s_setprio(2);
         const auto chunk = [&](const ChainIn<BF, KF, NT, true> &in, ChainIn<BF, KF, NT, true> &next, int c) __attribute__((always_inline)) {
             Mid<BF, 3> op[KF][NT];
-            read_columns<BF, 3>(sh.D, S8, pl.quad, pl.l15, op);
+            read_columns(sh.D, 0, pl.quad, pl.l15, op);
             hold();
             Sum<BF, 3> kD[NT];
 #pragma unroll
@@ -499,12 +499,12 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
                 sh.k.put(pl.row, 32 * f + 8 * pl.quad, in.k[f]);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
-                mid_store4<BF, 3>(sh.W[16 * j + pl.l15], pl.rows,
+                sh.W.put4(16 * j + pl.l15, pl.rows,
                                   write * kD[j].value() + beta * sh.po[pl.wave][j][lane]);
             lds_barrier();
             const v4f read = w.rows(VEC_READK, pl.rows);
             Mid<BF, 3> ws[2][NT];
-            read_columns<BF, 3>(sh.W, S8, pl.quad, pl.l15, ws);
+            read_columns(sh.W, 0, pl.quad, pl.l15, ws);
             hold();
             Sum<BF, 3> dv[NT];
 #pragma unroll
@@ -520,7 +520,7 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const v4f d = dv[j].value();
-                mid_store4<BF, 3>(sh.V[16 * j + pl.l15], pl.rows, -read * d);
+                sh.V.put4(16 * j + pl.l15, pl.rows, -read * d);
                 store_rows(a, pl, a.dV, c, j, d);
                 if (a.dv)
                     store_values<BF>(a, pl, a.dv, c, j, d);
@@ -528,7 +528,7 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             lds_barrier();
             const float last = w.last;
             Mid<BF, 3> vs[2][Sl::COLS];
-            read_columns<BF, 3>(sh.V + sl.col0(), S8, pl.quad, pl.l15, vs);
+            read_columns(sh.V, sl.col0(), pl.quad, pl.l15, vs);
             hold();
             Sum<BF, 3> dD[Sl::MINE];
 #pragma unroll
@@ -540,7 +540,7 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             for (int i = 0; i < Sl::MINE; ++i) {
                 D[i] = (D[i] * last + sh.qo[pl.wave][i][lane]) + dD[i].value();
                 if (sl.live(i))
-                    mid_store4<BF, 3>(sh.D[sl.col(i)], sl.row(i), D[i]);
+                    sh.D.put4(sl.col(i), sl.row(i), D[i]);
             }
             lds_barrier();
         };
@@ -569,8 +569,8 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const v4f o = values(in.o[j]);
-                mid_store4<BF, 1>(sh.O[16 * j + pl.l15], pl.rows, o);
-                mid_store4<BF, 3>(sh.Os[16 * j + pl.l15], pl.rows, in.read * o);
+                sh.O.put4(16 * j + pl.l15, pl.rows, o);
+                sh.Os.put4(16 * j + pl.l15, pl.rows, in.read * o);
             }
         };
         // its parts P^T dO, to LDS, and Q^T dO, kept
@@ -582,9 +582,7 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
                 for (int f = 0; f < 2; ++f) {
                     if (!half_live<true>(pl.wave, f))
                         continue;
-                    In<BF> d;
-                    __builtin_memcpy(&d, __builtin_assume_aligned(sh.O[16 * j + pl.l15] + (4 * f + pl.quad) * mid8<BF, 1>, 16), sizeof d);
-                    o = mma(in.p[f], d, o);
+                    o = mma(in.p[f], sh.O.get_in(16 * j + pl.l15, 4 * f + pl.quad), o);
                 }
                 sh.po[pl.wave][j][lane] = o;
             }
@@ -594,7 +592,7 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
                 if (sl.live(i))
 #pragma unroll
                     for (int f = 0; f < 2; ++f)
-                        qo[i] = mma(sh.q.down(32 * f, sl.row16(i)), mid_load<BF, 3>(sh.Os[sl.col(i)] + (4 * f + pl.quad) * S8), qo[i]);
+                        qo[i] = mma(sh.q.down(32 * f, sl.row16(i)), sh.Os.get(sl.col(i), 4 * f + pl.quad), qo[i]);
             }
         };
         HelpBack<BF, KF, NT> in;

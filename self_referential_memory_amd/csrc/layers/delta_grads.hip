@@ -14,13 +14,14 @@
 // dg sums what depends on g_t alone: taken as q.dq - k.dk summed over later tokens,
 // large terms would cancel. dk = (dk^ - k^ (k^.dk^)) / |k| at the end, likewise q.
 //
-// A block of eight waves takes a chunk of one q/k head and the v heads that share
-// it, one after the other. It walks the columns of v, 32 at a time: dO, E and dV go
-// to LDS, the next 32 columns on their way meanwhile; of the 64 x 64 parts a wave
-// forms 16 rows by 32 columns, of the products with the states 16 of the head's
-// columns (narrow heads: fewer rows), so that the states, the largest operands, are
-// read once, straight into registers. A, Y and the row factors then make the
-// matrices that multiply q and k, in the LDS that dO, E and dV leave.
+// A block of eight waves takes a chunk of one head. It walks the columns of v, 32 at
+// a time: dO, E and dV go to LDS, the next 32 columns on their way meanwhile; of the
+// 64 x 64 parts a wave forms 16 rows by 32 columns, of the products with the states
+// 16 of the head's columns (narrow heads: fewer rows), so that the states, the
+// largest operands, are read once, straight into registers. A, Y and the row factors
+// then make the matrices that multiply q and k, in the LDS that dO, E and dV leave.
+// Heads that share q and k write their parts in fp32, and a second kernel adds them
+// in order.
 #include "delta_mma.h"
 
 namespace {
@@ -28,109 +29,108 @@ namespace {
 using namespace srnl_i;
 
 template <bool BF, int KD> struct GradShared {
-    __attribute__((aligned(16))) Rows<BF, KD> k, q;
+    Rows<BF, KD> k, q;
     union {
         struct {
-            __attribute__((aligned(16))) char O[64][mid_row<BF, 1>(32)], E[64][mid_row<BF, 3>(32)], V[64][mid_row<BF, 3>(32)];
+            Split<BF, 1, 64, 32> O;
+            Split<BF, 3, 64, 32> E, V;
         } in[2];
         struct {
-            __attribute__((aligned(16))) char A[64][mid_row<BF, 2>(64)], At[64][mid_row<BF, 2>(64)], Z[64][mid_row<BF, 2>(64)];
+            Split<BF, 2, 64, 64> A, At, Z;
         } out;
     };
     float gam[64], end[64], beta[64], rk[64], rq[64], ghi[64], glo[64];
     float colF[4][64], rowF[2][64], diag[64], dot[2][8][64], sd[8];
 };
 
-template <bool BF, int KD> struct Columns {
-    static constexpr int CW = KD / 16, RW = 8 / CW;      // waves along columns, rows
-    static constexpr int RT = 4 / RW;                    // a wave's tiles: rows, in one column
-};
-
-__device__ __forceinline__ float sum16(float v)
-{
-#pragma unroll
-    for (int off = 8; off > 0; off >>= 1)
-        v += __shfl_xor(v, off);
-    return v;
-}
-
 template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a)
 {
     constexpr int KF = KD / 32;
-    using Sh = GradShared<BF, KD>;
-    using Co = Columns<BF, KD>;
-    constexpr int RT = Co::RT;
-    __shared__ Sh sh;
-    const int c = blockIdx.x % a.N, bk = blockIdx.x / a.N;
-    const int b = bk / a.Hk, hk = bk - b * a.Hk, per = a.H / a.Hk;
+    constexpr int CW = KD / 16, RW = 8 / CW;             // waves along columns, rows
+    constexpr int RT = 4 / RW;                           // a wave's tiles: rows, in one column
+    __shared__ GradShared<BF, KD> sh;
+    const int c = blockIdx.x % a.N, bh = blockIdx.x / a.N;
+    const int b = bh / a.H, h = bh - b * a.H, per = a.H / a.Hk, hk = h / per;
     const int n = delta_tokens(a, b), left = n - DELTA_CHUNK * c;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, quad = lane >> 4, l15 = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, quad = lane >> 4, l15 = lane & 15;
     const int band = wave & 3, half = wave >> 2;                        // of the 64 x 64 parts
     const int row = 16 * band + l15, rows = 16 * band + 4 * quad;
+    const int rt0 = wave / CW * RT, col0 = 16 * (wave % CW), mycol = col0 + l15;
     const long long tok = static_cast<long long>(b) * a.T + DELTA_CHUNK * c;
-    const int rt0 = wave / Co::CW * RT, col0 = 16 * (wave % Co::CW), mycol = col0 + l15;
     const int inside = a.T - DELTA_CHUNK * c < DELTA_CHUNK ? a.T - DELTA_CHUNK * c : DELTA_CHUNK;
+    // dq and dk: in place, or this head's part
+    const bool parts = per > 1;
+    const long long oqk = parts ? (tok * a.H + h) * a.Dk : (tok * a.Hk + hk) * a.Dk;
+    const int sqk = (parts ? a.H : a.Hk) * a.Dk;
+    const long long ogb = tok * a.H + h;
 
     if (left <= 0) {                   // past the end: zeros
         for (int i = threadIdx.x; i < inside * a.Dk; i += 512) {
-            const long long o = ((tok + i / a.Dk) * a.Hk + hk) * a.Dk + i % a.Dk;
-            if (a.dq)
-                put_at<BF>(a.dq, o, 0.0f);
-            if (a.dk)
-                put_at<BF>(a.dk, o, 0.0f);
+            const long long o = oqk + static_cast<long long>(i / a.Dk) * sqk + i % a.Dk;
+            if (parts) {
+                a.dq_part[o] = 0.0f;
+                a.dk_part[o] = 0.0f;
+            } else {
+                if (a.dq)
+                    put_at<BF>(a.dq, o, 0.0f);
+                if (a.dk)
+                    put_at<BF>(a.dk, o, 0.0f);
+            }
         }
-        for (int i = threadIdx.x; i < inside * per; i += 512) {
-            const long long o = (tok + i / per) * a.H + hk * per + i % per;
+        if (static_cast<int>(threadIdx.x) < inside) {
             if (a.dg)
-                a.dg[o] = 0.0f;
+                a.dg[ogb + static_cast<long long>(threadIdx.x) * a.H] = 0.0f;
             if (a.dbeta)
-                a.dbeta[o] = 0.0f;
+                a.dbeta[ogb + static_cast<long long>(threadIdx.x) * a.H] = 0.0f;
         }
         return;
     }
 
-    const long long head = static_cast<long long>(hk) * a.Dk;
-    const Buf rowsK(a.k, (tok * a.ks + head) * (BF ? 2 : 4)), rowsQ(a.q, (tok * a.qs + head) * (BF ? 2 : 4));
-#pragma unroll
-    for (int x = 0; x < KD / 64 + (KD < 64); ++x) {
-        // a thread's pieces of 8: every row, KD / 8 pieces
-        const int i = threadIdx.x + 512 * x, r = i / (KD / 8), k = i % (KD / 8) * 8;
-        if (r < 64) {
-            sh.k.put(r, k, in_load<BF>(rowsK, r * static_cast<int>(a.ks) + k, r < left && k < a.Dk));
-            sh.q.put(r, k, in_load<BF>(rowsQ, r * static_cast<int>(a.qs) + k, r < left && k < a.Dk));
+    const long long at = static_cast<long long>(bh) * a.N + c;
+    const Buf bS(a.S0, at * a.Dk * a.Dv * 4), bD(a.D1, at * a.Dk * a.Dv * 4);
+    // this thread's piece of 8 of E or dV, and of dO
+    const int pr = (threadIdx.x & 255) >> 2, pg = threadIdx.x & 3;
+    const bool ofE = wave < 4;
+    const Buf bEV(ofE ? a.E : a.dV, at * DELTA_CHUNK * a.Dv * 4);
+    const Buf bO(a.dout, (tok * a.H + h) * a.Dv * (BF ? 2 : 4));
+    struct Next {
+        float ev[8], s[8], d[8];
+        In<BF> o;
+    } next;
+    const auto fetch = [&](int v) __attribute__((always_inline)) {
+        const bool mine = v + 8 * pg < a.Dv, states = both(mycol < a.Dk, v + 8 * quad < a.Dv);
+        load8(bEV, pr * a.Dv + 8 * pg + v, mine, next.ev);
+        next.o = in_load<BF>(bO, pr * a.H * a.Dv + 8 * pg + v, both(both(ofE, mine), pr < left));
+        load8(bS, mycol * a.Dv + 8 * quad + v, states, next.s);
+        load8(bD, mycol * a.Dv + 8 * quad + v, states, next.d);
+    };
+    const auto spread = [&](int buf) __attribute__((always_inline)) {
+        if (ofE) {
+            sh.in[buf].E.put8(pr, pg, next.ev);
+            sh.in[buf].O.put_in(pr, pg, next.o);
+        } else {
+            sh.in[buf].V.put8(pr, pg, next.ev);
         }
-    }
-
-    v4f dq[RT], dk[RT];
+    };
+    fetch(0);
+    {
+        const long long head = static_cast<long long>(hk) * a.Dk;
+        const Buf rowsK(a.k, (tok * a.ks + head) * (BF ? 2 : 4)), rowsQ(a.q, (tok * a.qs + head) * (BF ? 2 : 4));
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-        dq[i] = dk[i] = v4f_zero();
-
-    for (int g = 0; g < per; ++g) {
-        const int h = hk * per + g;
-        const long long at = (static_cast<long long>(b) * a.H + h) * a.N + c;
-        const Buf bS(a.S0, at * a.Dk * a.Dv * 4), bD(a.D1, at * a.Dk * a.Dv * 4);
+        for (int x = 0; x < KD / 64 + (KD < 64); ++x) {
+            // a thread's pieces of 8: every row, KD / 8 pieces
+            const int i = threadIdx.x + 512 * x, r = i / (KD / 8), k = i % (KD / 8) * 8;
+            const bool live = both(r < left, k < a.Dk);
+            const In<BF> fk = in_load<BF>(rowsK, r * static_cast<int>(a.ks) + k, live);
+            const In<BF> fq = in_load<BF>(rowsQ, r * static_cast<int>(a.qs) + k, live);
+            if (r < 64) {
+                sh.k.put(r, k, fk);
+                sh.q.put(r, k, fq);
+            }
+        }
         const float *vec = a.vec + at * VEC_FLOATS;
-        // this thread's piece of 8 of E or dV, and of dO
-        const int pr = (threadIdx.x & 255) >> 2, pc = (threadIdx.x & 3) * 8;
-        const bool ofE = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
-        const Buf bEV(ofE ? a.E : a.dV, at * DELTA_CHUNK * a.Dv * 4);
-        const Buf bO(a.dout, (tok * a.H + h) * a.Dv * (BF ? 2 : 4));
-        struct { float ev[8], s[8], d[8]; In<BF> o; } next;
-        const auto fetch = [&](int v) __attribute__((always_inline)) {
-            load8(bEV, pr * a.Dv + pc + v, v + pc < a.Dv, next.ev);
-            next.o = in_load<BF>(bO, pr * a.H * a.Dv + pc + v, ofE && v + pc < a.Dv && pr < left);
-            load8(bS, mycol * a.Dv + 8 * quad + v, mycol < a.Dk && v + 8 * quad < a.Dv, next.s);
-            load8(bD, mycol * a.Dv + 8 * quad + v, mycol < a.Dk && v + 8 * quad < a.Dv, next.d);
-        };
-        const auto spread = [&](int buf) __attribute__((always_inline)) {
-            mid_store8<BF, 3>((ofE ? sh.in[buf].E[pr] : sh.in[buf].V[pr]) + pc / 8 * mid8<BF, 3>, next.ev);
-            if (ofE)
-                __builtin_memcpy(__builtin_assume_aligned(sh.in[buf].O[pr] + pc / 8 * mid8<BF, 1>, 16), &next.o, sizeof next.o);
-        };
-        fetch(0);
-        __syncthreads();               // the head before is done with the shared arrays
-        if (threadIdx.x < 64) {
+        if (wave == 0) {
             sh.gam[lane] = vec[VEC_GAM + lane];
             sh.end[lane] = vec[VEC_END + lane];
             sh.beta[lane] = vec[VEC_BETA + lane];
@@ -139,106 +139,94 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
             sh.ghi[lane] = vec[VEC_GHI + lane];
             sh.glo[lane] = vec[VEC_GLO + lane];
         }
-        spread(0);
+    }
+    spread(0);
 
-        v4f A[2], Y[2], oS[RT], vS[RT], eD[RT];
+    v4f A[2], Y[2], oS[RT], vS[RT], eD[RT];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-            A[x] = Y[x] = v4f_zero();
+    for (int x = 0; x < 2; ++x)
+        A[x] = Y[x] = v4f_zero();
 #pragma unroll
-        for (int ri = 0; ri < RT; ++ri)
-            oS[ri] = vS[ri] = eD[ri] = v4f_zero();
-        float sd = 0.0f;
-        int buf = 0;
+    for (int ri = 0; ri < RT; ++ri)
+        oS[ri] = vS[ri] = eD[ri] = v4f_zero();
+    float sd = 0.0f;
+    int buf = 0;
 #pragma unroll 1
-        for (int v = 0; v < a.Dv; v += 32, buf ^= 1) {
-            const Mid<BF, 3> s = mid_split<BF, 3>(next.s), d = mid_split<BF, 3>(next.d);
-            if (rt0 == 0)
+    for (int v = 0; v < a.Dv; v += 32, buf ^= 1) {
+        const Mid<BF, 3> s = mid_split<BF, 3>(next.s), d = mid_split<BF, 3>(next.d);
+        if (rt0 == 0)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sd = fmaf(next.s[e], next.d[e], sd);
-            if (v + 32 < a.Dv)
-                fetch(v + 32);
-            lds_barrier();
-            const auto rowO = [&](int r) __attribute__((always_inline)) {
-                In<BF> f;
-                __builtin_memcpy(&f, __builtin_assume_aligned(sh.in[buf].O[r] + quad * mid8<BF, 1>, 16), sizeof f);
-                return f;
-            };
-            {
-                const In<BF> o = rowO(row);
-                const Mid<BF, 3> y = mid_load<BF, 3>(sh.in[buf].V[row] + quad * mid8<BF, 3>);
+            for (int e = 0; e < 8; ++e)
+                sd = fmaf(next.s[e], next.d[e], sd);
+        fetch(v + 32 < a.Dv ? v + 32 : v);
+        lds_barrier();
+        const auto &in = sh.in[buf];
+        {
+            const In<BF> o = in.O.get_in(row, quad);
+            const Mid<BF, 3> y = in.V.get(row, quad);
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int j = 2 * half + x;
-                    if (j > band)
-                        continue;
-                    const Mid<BF, 3> e = mid_load<BF, 3>(sh.in[buf].E[16 * j + l15] + quad * mid8<BF, 3>);
-                    A[x] = mma(o, e, A[x]);
-                    Y[x] = mma(y, e, Y[x]);
-                }
+            for (int x = 0; x < 2; ++x) {
+                const int j = 2 * half + x;
+                if (j > band)
+                    continue;
+                const Mid<BF, 3> e = in.E.get(16 * j + l15, quad);
+                A[x] = mma(o, e, A[x]);
+                Y[x] = mma(y, e, Y[x]);
             }
-#pragma unroll
-            for (int ri = 0; ri < RT; ++ri) {
-                const int r = 16 * (rt0 + ri) + l15;
-                oS[ri] = mma(rowO(r), s, oS[ri]);
-                vS[ri] = mma(mid_load<BF, 3>(sh.in[buf].V[r] + quad * mid8<BF, 3>), s, vS[ri]);
-                eD[ri] = mma(mid_load<BF, 3>(sh.in[buf].E[r] + quad * mid8<BF, 3>), d, eD[ri]);
-            }
-            if (v + 32 < a.Dv)
-                spread(buf ^ 1);
         }
-        __syncthreads();               // dO, E and dV are read
+#pragma unroll
+        for (int ri = 0; ri < RT; ++ri) {
+            const int r = 16 * (rt0 + ri) + l15;
+            oS[ri] = mma(in.O.get_in(r, quad), s, oS[ri]);
+            vS[ri] = mma(in.V.get(r, quad), s, vS[ri]);
+            eD[ri] = mma(in.E.get(r, quad), d, eD[ri]);
+        }
+        if (v + 32 < a.Dv)
+            spread(buf ^ 1);
+    }
+    lds_barrier();                     // dO, E and dV are read
 
-        // ---- 64 x 64 parts: this wave's rows i against its columns j
-        float rowF[4] = {0, 0, 0, 0};
+    // ---- 64 x 64 parts: this wave's rows i against its columns j
+    float rowF[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int j = 2 * half + p, col = 16 * j + l15;
-            v4f wa = v4f_zero(), wat = v4f_zero(), zl = v4f_zero(), zu = v4f_zero();
-            float colF = 0.0f;
-            if (j <= band) {
-                v4f kk = v4f_zero(), qk = v4f_zero();
+    for (int p = 0; p < 2; ++p) {
+        const int j = 2 * half + p, col = 16 * j + l15;
+        v4f wa = v4f_zero(), wat = v4f_zero();
+        float colF = 0.0f;
+        if (j <= band) {
+            v4f kk = v4f_zero(), qk = v4f_zero(), zl, zu;
 #pragma unroll
-                for (int f = 0; f < KF; ++f) {
-                    const int k = 32 * f + 8 * quad;
-                    const In<BF> o = sh.k.across(col, k);
-                    kk = mma(sh.k.across(row, k), o, kk);
-                    qk = mma(sh.q.across(row, k), o, qk);
-                }
-                const float bj = sh.beta[col], rj = sh.rk[col];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = rows + e;
-                    const float d = decay(sh.ghi[i], sh.glo[i], sh.ghi[col], sh.glo[col]);
-                    const float ri = sh.rk[i], qi = sh.rq[i];
-                    const bool on = col <= i, below = col < i;
-                    const float x = on ? a.scale * d * A[p][e] : 0.0f;          // dP before beta
-                    const float y = below ? d * Y[p][e] : 0.0f;
-                    const float F = on ? x * qi * rj * qk[e] - (below ? y * ri * rj * kk[e] : 0.0f) : 0.0f;
-                    wa[e] = x * bj * rj;
-                    wat[e] = x * bj * qi;
-                    zl[e] = -y * bj * rj;
-                    zu[e] = -y * bj * ri;
-                    colF += F;
-                    // the diagonal is no decay's
-                    rowF[e] += below ? bj * F : 0.0f;
-                    if (on && !below)
-                        sh.diag[i] = F;
-                }
+            for (int f = 0; f < KF; ++f) {
+                const int k = 32 * f + 8 * quad;
+                const In<BF> o = sh.k.across(col, k);
+                kk = mma(sh.k.across(row, k), o, kk);
+                qk = mma(sh.q.across(row, k), o, qk);
             }
-            mid_store_rows<BF, 2>(sh.out.A[rows], sizeof sh.out.A[0], col, wa);
-            mid_store4<BF, 2>(sh.out.At[col], rows, wat);
+            const float bj = sh.beta[col], rj = sh.rk[col];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = rows + e;
+                const float d = decay(sh.ghi[i], sh.glo[i], sh.ghi[col], sh.glo[col]);
+                const float ri = sh.rk[i], qi = sh.rq[i];
+                const bool on = col <= i, below = col < i;
+                const float x = on ? a.scale * d * A[p][e] : 0.0f;          // dP before beta
+                const float y = below ? d * Y[p][e] : 0.0f;
+                const float F = on ? x * qi * rj * qk[e] - (below ? y * ri * rj * kk[e] : 0.0f) : 0.0f;
+                wa[e] = x * bj * rj;
+                wat[e] = x * bj * qi;
+                zl[e] = -y * bj * rj;
+                zu[e] = -y * bj * ri;
+                colF += F;
+                // the diagonal is no decay's
+                rowF[e] += below ? bj * F : 0.0f;
+                if (on && !below)
+                    sh.diag[i] = F;
+            }
             // Z's two triangles: rows i > j from here, its mirror from the same values
             if (j < band) {
-                mid_store_rows<BF, 2>(sh.out.Z[rows], sizeof sh.out.Z[0], col, zl);
-                mid_store4<BF, 2>(sh.out.Z[col], rows, zu);
-            }
-            colF += __shfl_xor(colF, 16);
-            colF += __shfl_xor(colF, 32);
-            if (quad == 0)
-                sh.colF[band][col] = colF;
-            if (j == band) {
+                sh.out.Z.put_rows(rows, col, zl);
+                sh.out.Z.put4(col, rows, zu);
+            } else {
                 // the diagonal tile is both: its upper half comes from the lanes across
                 v4f z;
 #pragma unroll
@@ -250,91 +238,97 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                     const float up = (l15 & 2) ? ((l15 & 1) ? u3 : u2) : ((l15 & 1) ? u1 : u0);
                     z[e] = l15 < 4 * quad + e ? zl[e] : l15 > 4 * quad + e ? up : 0.0f;
                 }
-                mid_store_rows<BF, 2>(sh.out.Z[rows], sizeof sh.out.Z[0], col, z);
+                sh.out.Z.put_rows(rows, col, z);
             }
         }
+        sh.out.A.put_rows(rows, col, wa);
+        sh.out.At.put4(col, rows, wat);
+        colF += __shfl_xor(colF, 16);
+        colF += __shfl_xor(colF, 32);
+        if (quad == 0)
+            sh.colF[band][col] = colF;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float s = sum16(rowF[e]);
+        if (l15 == 0)
+            sh.rowF[half][rows + e] = s;
+    }
+    // ---- the states' terms, while the matrices come together
+    v4f dq[RT], dk[RT];
+#pragma unroll
+    for (int ri = 0; ri < RT; ++ri)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float s = sum16(rowF[e]);
-            if (l15 == 0)
-                sh.rowF[half][rows + e] = s;
-        }
-        __syncthreads();
-        // ---- products with the head's width: this wave's columns
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            const int o = (4 * f + quad) * mid8<BF, 2>;
-            const In<BF> kd = sh.k.down(32 * f, col0), qd = sh.q.down(32 * f, col0);
-#pragma unroll
-            for (int ri = 0; ri < RT; ++ri) {
-                const int r = 16 * (rt0 + ri) + l15;
-                dq[ri] = mma(mid_load<BF, 2>(sh.out.A[r] + o), kd, dq[ri]);
-                dk[ri] = mma(mid_load<BF, 2>(sh.out.At[r] + o), qd, dk[ri]);
-                dk[ri] = mma(mid_load<BF, 2>(sh.out.Z[r] + o), kd, dk[ri]);
+            const int i = 16 * (rt0 + ri) + 4 * quad + e;
+            const float x = a.scale * sh.gam[i] * oS[ri][e];
+            const float y = -sh.gam[i] * vS[ri][e];
+            const float w = sh.end[i] * eD[ri][e];
+            const float kh = sh.rk[i] * sh.k.at(i, mycol), qh = sh.rq[i] * sh.q.at(i, mycol);
+            const float s = sum16(fmaf(qh, x, kh * y)), t = sum16(kh * w);
+            if (l15 == 0) {
+                sh.dot[0][wave % CW][i] = s;
+                sh.dot[1][wave % CW][i] = t;
             }
+            dq[ri][e] = x;
+            dk[ri][e] = fmaf(sh.beta[i], w, y);
         }
 #pragma unroll
-        for (int ri = 0; ri < RT; ++ri)
+    for (int off = 32; off > 0; off >>= 1)
+        sd += __shfl_xor(sd, off);
+    if (lane == 0)
+        sh.sd[wave] = sd;
+    lds_barrier();
+
+    // ---- products with the head's width: this wave's columns
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * (rt0 + ri) + 4 * quad + e;
-                const float x = a.scale * sh.gam[i] * oS[ri][e];
-                const float y = -sh.gam[i] * vS[ri][e];
-                const float w = sh.end[i] * eD[ri][e];
-                const float kh = sh.rk[i] * sh.k.at(i, mycol), qh = sh.rq[i] * sh.q.at(i, mycol);
-                const float s = sum16(fmaf(qh, x, kh * y)), t = sum16(kh * w);
-                if (l15 == 0) {
-                    sh.dot[0][wave % Co::CW][i] = s;
-                    sh.dot[1][wave % Co::CW][i] = t;
-                }
-                dq[ri][e] += x;
-                dk[ri][e] += fmaf(sh.beta[i], w, y);
-            }
+    for (int f = 0; f < 2; ++f) {
+        const In<BF> kd = sh.k.down(32 * f, col0), qd = sh.q.down(32 * f, col0);
 #pragma unroll
-        for (int off = 32; off > 0; off >>= 1)
-            sd += __shfl_xor(sd, off);
-        if (lane == 0)
-            sh.sd[wave] = sd;
-        __syncthreads();
-        if (wave == 0) {
-            float s = 0.0f, w = 0.0f, col = 0.0f;
+        for (int ri = 0; ri < RT; ++ri) {
+            const int r = 16 * (rt0 + ri) + l15;
+            dq[ri] = mma(sh.out.A.get(r, 4 * f + quad), kd, dq[ri]);
+            dk[ri] = mma(sh.out.At.get(r, 4 * f + quad), qd, dk[ri]);
+            dk[ri] = mma(sh.out.Z.get(r, 4 * f + quad), kd, dk[ri]);
+        }
+    }
+    if (wave == 0) {
+        float s = 0.0f, w = 0.0f, col = 0.0f, inner = 0.0f;
 #pragma unroll
-            for (int x = 0; x < Co::CW; ++x) {
-                s += sh.dot[0][x][lane];
-                w += sh.dot[1][x][lane];
-            }
+        for (int x = 0; x < CW; ++x) {
+            s += sh.dot[0][x][lane];
+            w += sh.dot[1][x][lane];
+        }
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                col += x >= lane / 16 ? sh.colF[x][lane] : 0.0f;
-            const float beta = sh.beta[lane];
-            const float dbeta = w + col;
-            w *= beta;
-            // tokens after this one and itself; tokens before this one
-            float after = (sh.rowF[0][lane] + sh.rowF[1][lane]) - beta * (col - sh.diag[lane]) + s, before = w;
+        for (int x = 0; x < 4; ++x)
+            col += x >= lane / 16 ? sh.colF[x][lane] : 0.0f;
 #pragma unroll
-            for (int off = 1; off < 64; off <<= 1) {
-                const float x = __shfl_down(after, off), y = __shfl_up(before, off);
-                after += lane + off < 64 ? x : 0.0f;
-                before += lane >= off ? y : 0.0f;
-            }
-            float inner = 0.0f;
+        for (int x = 0; x < 8; ++x)
+            inner += sh.sd[x];
+        const float beta = sh.beta[lane];
+        const float dbeta = w + col;
+        w *= beta;
+        // tokens after this one and itself; tokens before this one
+        float after = (sh.rowF[0][lane] + sh.rowF[1][lane]) - beta * (col - sh.diag[lane]) + s, before = w;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                inner += sh.sd[x];
-            const float dg = after + (before - w) + sh.gam[63] * inner;
-            if (lane < inside) {
-                const long long o = (tok + lane) * a.H + h;
-                if (a.dg)
-                    a.dg[o] = lane < left ? dg : 0.0f;
-                if (a.dbeta)
-                    a.dbeta[o] = lane < left ? dbeta : 0.0f;
-            }
+        for (int off = 1; off < 64; off <<= 1) {
+            const float x = __shfl_down(after, off), y = __shfl_up(before, off);
+            after += lane + off < 64 ? x : 0.0f;
+            before += lane >= off ? y : 0.0f;
+        }
+        const float dg = after + (before - w) + sh.gam[63] * inner;
+        if (lane < inside) {
+            const long long o = ogb + static_cast<long long>(lane) * a.H;
+            if (a.dg)
+                a.dg[o] = lane < left ? dg : 0.0f;
+            if (a.dbeta)
+                a.dbeta[o] = lane < left ? dbeta : 0.0f;
         }
     }
 
     // ---- through the normalisation, and out
     if (a.eps > 0.0f) {
-        __syncthreads();               // the last head's sums are read
+        lds_barrier();                 // the sums for dg are read
 #pragma unroll
         for (int ri = 0; ri < RT; ++ri)
 #pragma unroll
@@ -343,37 +337,70 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                 const float x = sum16(sh.q.at(i, mycol) * dq[ri][e]);
                 const float y = sum16(sh.k.at(i, mycol) * dk[ri][e]);
                 if (l15 == 0) {
-                    sh.dot[0][wave % Co::CW][i] = x;
-                    sh.dot[1][wave % Co::CW][i] = y;
+                    sh.dot[0][wave % CW][i] = x;
+                    sh.dot[1][wave % CW][i] = y;
                 }
             }
-        __syncthreads();
+        lds_barrier();
+#pragma unroll
+        for (int ri = 0; ri < RT; ++ri)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 16 * (rt0 + ri) + 4 * quad + e;
+                const float rq = sh.rq[i], rk = sh.rk[i];
+                float xs = 0.0f, ys = 0.0f;
+#pragma unroll
+                for (int w = 0; w < CW; ++w) {
+                    xs += sh.dot[0][w][i];
+                    ys += sh.dot[1][w][i];
+                }
+                dq[ri][e] = rq * (dq[ri][e] - rq * sh.q.at(i, mycol) * (rq * xs));
+                dk[ri][e] = rk * (dk[ri][e] - rk * sh.k.at(i, mycol) * (rk * ys));
+            }
     }
+    const Buf oq(parts ? a.dq_part : a.dq, oqk * (parts || !BF ? 4 : 2));
+    const Buf ok(parts ? a.dk_part : a.dk, oqk * (parts || !BF ? 4 : 2));
 #pragma unroll
     for (int ri = 0; ri < RT; ++ri)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = 16 * (rt0 + ri) + 4 * quad + e;
-            float x = dq[ri][e], y = dk[ri][e];
-            if (a.eps > 0.0f) {
-                const float rq = sh.rq[i], rk = sh.rk[i];
-                float xs = 0.0f, ys = 0.0f;
-#pragma unroll
-                for (int w = 0; w < Co::CW; ++w) {
-                    xs += sh.dot[0][w][i];
-                    ys += sh.dot[1][w][i];
-                }
-                x = rq * (x - rq * sh.q.at(i, mycol) * (rq * xs));
-                y = rk * (y - rk * sh.k.at(i, mycol) * (rk * ys));
+            const int i = 16 * (rt0 + ri) + 4 * quad + e, o = i * sqk + mycol;
+            const bool live = both(i < inside, mycol < a.Dk);
+            const float x = i < left ? dq[ri][e] : 0.0f, y = i < left ? dk[ri][e] : 0.0f;
+            if (parts) {
+                put_value<false>(oq, o, live, x);
+                put_value<false>(ok, o, live, y);
+            } else {
+                put_value<BF>(oq, o, both(live, a.dq != nullptr), x);
+                put_value<BF>(ok, o, both(live, a.dk != nullptr), y);
             }
-            if (i >= inside || mycol >= a.Dk)
-                continue;
-            const long long o = ((tok + i) * a.Hk + hk) * a.Dk + mycol;
-            if (a.dq)
-                put_at<BF>(a.dq, o, i < left ? x : 0.0f);
-            if (a.dk)
-                put_at<BF>(a.dk, o, i < left ? y : 0.0f);
         }
+}
+
+// dq and dk over the heads that share them, from fp32 parts [B][T][H][Dk]: 8 values a
+// thread, the heads in order.
+template <bool BF> __global__ __launch_bounds__(256) void delta_heads_kernel(DeltaArgs a)
+{
+    const int per = a.H / a.Hk, pieces = a.Dk / 8;
+    const long long total = static_cast<long long>(a.B) * a.T * a.Hk * pieces;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < 2 * total; i += 256LL * gridDim.x) {
+        const bool ofK = i >= total;
+        const long long x = ofK ? i - total : i, row = x / pieces;       // token and q/k head
+        void *out = ofK ? a.dk : a.dq;
+        if (!out)
+            continue;
+        const float *part = (ofK ? a.dk_part : a.dq_part) + row * per * a.Dk + x % pieces * 8;
+        float s[8];
+        load_f32<8, true>(part, s);
+        for (int g = 1; g < per; ++g) {
+            float v[8];
+            load_f32<8, true>(part + static_cast<long long>(g) * a.Dk, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s[e] += v[e];
+        }
+        store_row<8, true>(out, BF, row * a.Dk + x % pieces * 8, 8, s);
+    }
 }
 
 }  // namespace
@@ -382,9 +409,17 @@ namespace srnl_i {
 
 srnl_status launch_delta_grads(const DeltaArgs &a, hipStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.Hk * a.N));
+    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.H * a.N));
 #define SRNL_DELTA_GRADS(BF, KD) hipLaunchKernelGGL((delta_grads_kernel<BF, KD>), grid, dim3(512), 0, st, a)
     SRNL_DELTA_DISPATCH(a, SRNL_DELTA_GRADS);
+    if (a.H > a.Hk && (a.dq || a.dk)) {
+        const long long blocks = (static_cast<long long>(a.B) * a.T * a.Hk * (a.Dk / 8) * 2 + 255) / 256;
+        const dim3 heads(static_cast<unsigned>(blocks < 1 << 16 ? blocks : 1 << 16));
+        if (a.bf)
+            hipLaunchKernelGGL(delta_heads_kernel<true>, heads, dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL(delta_heads_kernel<false>, heads, dim3(256), 0, st, a);
+    }
     return launched("delta_grads_kernel");
 }
 

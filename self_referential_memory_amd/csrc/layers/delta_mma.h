@@ -10,7 +10,7 @@
 // where only bf16 outputs depend on them; three, right to 2^-26, where states and
 // fp32 gradients do (with two those were off by 4e-6 to 7e-6, with three by 2e-7 to
 // 5e-7, as the fp32 path). A product of two leaves out the pairs of words below its
-// smallest kept one. 8 values lie together, one plane of 16 bytes after the other.
+// smallest kept one.
 #ifndef SRNL_LAYERS_DELTA_MMA_H
 #define SRNL_LAYERS_DELTA_MMA_H
 
@@ -23,10 +23,6 @@ template <bool BF> struct In { bf16x8 v; };
 template <> struct In<false> { float v[8]; };
 template <bool BF, int PL> struct Mid { bf16x8 p[PL]; };
 template <int PL> struct Mid<false, PL> { float v[8]; };
-// bytes of 8 values, and of a row of n with the pad that spreads 16 rows over the banks
-template <bool BF, int PL> constexpr int mid8 = BF ? 16 * PL : 32;
-template <bool BF, int PL> constexpr int mid_row(int n) { return n / 8 * mid8<BF, PL> + 16; }
-
 __device__ __forceinline__ v4f mma16(bf16x8 a, bf16x8 b, v4f c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -130,6 +126,28 @@ template <bool BF, int PL> struct Sum {
     }
 };
 
+// the value of the lane beside (lane ^ 1), and sums over the 16 lanes of a row
+__device__ __forceinline__ float beside(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));
+}
+__device__ __forceinline__ uint32_t beside(uint32_t v)
+{
+    return __builtin_amdgcn_mov_dpp(static_cast<int>(v), 0xB1, 0xF, 0xF, true);
+}
+template <int CTRL> __device__ __forceinline__ float turned(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float sum16(float v)
+{
+    v += turned<0x128>(v);            // row_ror 8, 4, 2, 1
+    v += turned<0x124>(v);
+    v += turned<0x122>(v);
+    v += turned<0x121>(v);
+    return v;
+}
+
 __device__ __forceinline__ v4f v4f_zero() { return v4f{0.0f, 0.0f, 0.0f, 0.0f}; }
 
 // ---- memory
@@ -227,17 +245,6 @@ __device__ __forceinline__ float in_squares(const In<false> &f)
 
 // ---- split values
 
-// 8 values of the first PL planes at p in LDS, 16-byte aligned
-template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_load(const char *p)
-{
-    Mid<BF, PL> f;
-    u32x4 t[BF ? PL : 2];
-#pragma unroll
-    for (int j = 0; j < (BF ? PL : 2); ++j)
-        t[j] = reinterpret_cast<const u32x4 *>(p)[j];
-    __builtin_memcpy(&f, t, sizeof f);
-    return f;
-}
 // An operand of X or P in memory lies as a wave reads it, 16 bytes a lane after
 // 16 bytes a lane: rows of 64 values would have every lane of a load on a cache line
 // of its own, and the loads, not the products, set the chain's pace.
@@ -284,16 +291,6 @@ template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_split(cons
     }
     return f;
 }
-// 8 fp32 values to p
-template <bool BF, int PL> __device__ __forceinline__ void mid_store8(char *p, const float (&v)[8])
-{
-    const Mid<BF, PL> f = mid_split<BF, PL>(v);
-    u32x4 t[sizeof f / 16];
-    __builtin_memcpy(t, &f, sizeof f);
-#pragma unroll
-    for (unsigned j = 0; j < sizeof f / 16; ++j)
-        reinterpret_cast<u32x4 *>(p)[j] = t[j];
-}
 template <bool BF, int PL> __device__ __forceinline__ void frag_store(char *p, int frag, const float (&v)[8])
 {
     const Mid<BF, PL> f = mid_split<BF, PL>(v);
@@ -303,47 +300,95 @@ template <bool BF, int PL> __device__ __forceinline__ void frag_store(char *p, i
     for (unsigned j = 0; j < sizeof f / 16; ++j)
         *reinterpret_cast<u32x4 *>(p + frag * frag_bytes<BF, PL> + 1024 * j + 16 * (threadIdx.x & 63)) = t[j];
 }
-// a result tile's column as a row of its transpose: 4 values at place k (a
-// multiple of 4) of the row at p
-template <bool BF, int PL> __device__ __forceinline__ void mid_store4(char *p, int k, v4f v)
-{
-    char *q = p + k / 8 * mid8<BF, PL>;
-    if constexpr (BF) {
-        uint32_t a[PL], b[PL];
-        split_pair<PL>(v[0], v[1], a);
-        split_pair<PL>(v[2], v[3], b);
+// ROWS rows of K split values in LDS, a plane for each word. Rows are 32 bytes longer
+// than their values, so that 16 rows' reads of one piece of 16 bytes meet no bank
+// twice (with 16 bytes, or with the planes of a piece side by side, a read took half
+// as long again).
+template <bool BF, int PL, int ROWS, int K> struct Split {
+    static constexpr int PLANES = BF ? PL : 1, ROW = K * (BF ? 2 : 4) + 32;
+    __attribute__((aligned(16))) char b[PLANES][ROWS][ROW];
+
+    // 8 values of row r from piece g on, the first N words of them
+    template <int N = PL> __device__ __forceinline__ Mid<BF, N> get(int r, int g) const
+    {
+        Mid<BF, N> f;
+        u32x4 t[BF ? N : 2];
+        if constexpr (BF) {
 #pragma unroll
-        for (int j = 0; j < PL; ++j)
-            *reinterpret_cast<u32x2 *>(q + 16 * j + (k & 4) * 2) = u32x2{a[j], b[j]};
-    } else {
-        *reinterpret_cast<v4f *>(q + (k & 4) * 4) = v;
-    }
-}
-// a result tile as it lies: this lane's 4 rows, `stride` bytes apart from the row
-// at p, at column col. Lanes of neighbouring columns exchange, so that each
-// writes whole words: two rows of both columns. All lanes of a pair call it.
-template <bool BF, int PL> __device__ __forceinline__ void mid_store_rows(char *p, int stride, int col, v4f v)
-{
-    char *q = p + col / 8 * mid8<BF, PL>;
-    if constexpr (BF) {
-        const int odd = col & 1;
-        // the even lane takes rows 0 and 1, the odd one 2 and 3
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float mine = odd ? v[2 + i] : v[i], give = odd ? v[i] : v[2 + i];
-            const float got = __shfl_xor(give, 1);
-            uint32_t w[PL];
-            split_pair<PL>(odd ? got : mine, odd ? mine : got, w);
-#pragma unroll
-            for (int j = 0; j < PL; ++j)
-                *reinterpret_cast<uint32_t *>(q + (2 * odd + i) * stride + 16 * j + (col & 6) * 2) = w[j];
+            for (int p = 0; p < N; ++p)
+                t[p] = *reinterpret_cast<const u32x4 *>(&b[p][r][16 * g]);
+        } else {
+            t[0] = *reinterpret_cast<const u32x4 *>(&b[0][r][32 * g]);
+            t[1] = *reinterpret_cast<const u32x4 *>(&b[0][r][32 * g + 16]);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float *>(q + i * stride + (col & 7) * 4) = v[i];
+        __builtin_memcpy(&f, t, sizeof f);
+        return f;
     }
-}
+    // one-word values: inputs
+    __device__ __forceinline__ In<BF> get_in(int r, int g) const
+    {
+        In<BF> f;
+        __builtin_memcpy(&f, __builtin_assume_aligned(&b[0][r][(BF ? 16 : 32) * g], 16), sizeof f);
+        return f;
+    }
+    __device__ __forceinline__ void put_in(int r, int g, const In<BF> &f)
+    {
+        __builtin_memcpy(__builtin_assume_aligned(&b[0][r][(BF ? 16 : 32) * g], 16), &f, sizeof f);
+    }
+    // 8 fp32 values to piece g of row r
+    __device__ __forceinline__ void put8(int r, int g, const float (&v)[8])
+    {
+        const Mid<BF, PL> f = mid_split<BF, PL>(v);
+        u32x4 t[sizeof f / 16];
+        __builtin_memcpy(t, &f, sizeof f);
+        if constexpr (BF) {
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+                *reinterpret_cast<u32x4 *>(&b[p][r][16 * g]) = t[p];
+        } else {
+            *reinterpret_cast<u32x4 *>(&b[0][r][32 * g]) = t[0];
+            *reinterpret_cast<u32x4 *>(&b[0][r][32 * g + 16]) = t[1];
+        }
+    }
+    // a result tile's column as a row of its transpose: 4 values of row r at place k,
+    // a multiple of 4
+    __device__ __forceinline__ void put4(int r, int k, v4f v)
+    {
+        if constexpr (BF) {
+            uint32_t x[PL], y[PL];
+            split_pair<PL>(v[0], v[1], x);
+            split_pair<PL>(v[2], v[3], y);
+#pragma unroll
+            for (int p = 0; p < PL; ++p)
+                *reinterpret_cast<u32x2 *>(&b[p][r][2 * k]) = u32x2{x[p], y[p]};
+        } else {
+            *reinterpret_cast<v4f *>(&b[0][r][4 * k]) = v;
+        }
+    }
+    // a result tile as it lies: this lane's rows r .. r + 3 at column k. Lanes of
+    // neighbouring columns exchange, so that each writes whole words: two rows of
+    // both columns. All lanes of a pair call it.
+    __device__ __forceinline__ void put_rows(int r, int k, v4f v)
+    {
+        if constexpr (BF) {
+            const int odd = k & 1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float mine = odd ? v[2 + i] : v[i], give = odd ? v[i] : v[2 + i];
+                const float got = beside(give);
+                uint32_t w[PL];
+                split_pair<PL>(odd ? got : mine, odd ? mine : got, w);
+#pragma unroll
+                for (int p = 0; p < PL; ++p)
+                    *reinterpret_cast<uint32_t *>(&b[p][r + 2 * odd + i][2 * (k - odd)]) = w[p];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float *>(&b[0][r + i][4 * k]) = v[i];
+        }
+    }
+};
 // 8 fp32 values from memory, o in values, zeros where not live
 __device__ __forceinline__ void load8(const Buf &b, int o, bool live, float (&v)[8])
 {
@@ -354,10 +399,10 @@ __device__ __forceinline__ void load8(const Buf &b, int o, bool live, float (&v)
 
 // ---- a chunk's rows of q or k in LDS, read down the tokens
 
-// Elements of a row: KD and a pad that spreads a transposing read's four rows
-// over the banks.
+// Elements of a row: KD and a pad that spreads over the banks the four rows of a
+// transposing read and the 16 of a plain one.
 template <bool BF, int KD> struct Rows {
-    static constexpr int LD = BF ? KD + 24 : KD + 4;
+    static constexpr int LD = BF ? KD + 16 : KD + 4;
     typename std::conditional<BF, uint16_t, float>::type e[64][LD];
 
     // this lane's 8 elements of row r from element k on
