@@ -7,9 +7,12 @@
 //   dx = rstd (d - mean(d) - n mean(d n)) [+ add]
 //   dgain = sum of dz n,  dbias = sum of dz, over items and cells
 //
-// An item's map is cut into slabs of cells. A thread keeps a column of V
-// channels and walks the slab's cells, a block of 256 threads side by side, so
-// every access is a wide piece of a row.
+// Two ways. Where items and groups make enough blocks, a block takes all the cells of
+// a slice of whole groups: one kernel each way, which holds the slice in registers if
+// it fits and otherwise reads it again, from the L2 cache. Else an item's map is cut
+// into slabs of cells whose sums a second kernel joins and a third applies. A thread
+// keeps a column of V channels and walks the cells, threads side by side along the
+// channels, so every access is a wide piece of a row.
 #include "linear.h"
 
 namespace {
@@ -34,6 +37,7 @@ struct GnArgs {
     int slabs;
     long long rows;         // cells of a slab
     int tiles;              // blocks side by side along the channels
+    int slice;              // channels of a slice, 0: slabs
 };
 
 template <int V> __device__ __forceinline__ void load_piece(const void *p, bool bf, long long o, float (&v)[V])
@@ -99,11 +103,17 @@ template <int V> struct Place {
     __device__ __forceinline__ int wide(const GnArgs &a) const { return a.C / V < 256 ? a.C / V : 256; }
 };
 
-// Cells that lane l of `lanes` walks between first and last.
-__device__ __forceinline__ long long cells_of(long long cells, int lanes, int l)
-{
-    return cells > l ? (cells - l + lanes - 1) / lanes : 0;
-}
+// Cells of a slab that lane l walks.
+struct Shares {
+    long long each;
+    int more;               // the first lanes have one more
+    __device__ __forceinline__ Shares(long long cells, int lanes)
+        : each(cells / lanes), more(static_cast<int>(cells - each * lanes))
+    {
+    }
+    __device__ __forceinline__ long long of(int l) const { return each + (l < more); }
+    __device__ __forceinline__ float part(int l, float cells) const { return static_cast<float>(of(l)) / cells; }
+};
 
 // Mean and sum of squares about it, per channel of a slab. A thread sums
 // distances from its first cell, so an offset costs no digits: what is lost is
@@ -113,8 +123,9 @@ template <int V> __global__ __launch_bounds__(256) void gn_stats_kernel(GnArgs a
     __shared__ float lds[256][2 * V];
     const Place<V> pl(a);
     const long long cells = pl.last - pl.first;
+    const Shares shares(cells, pl.lanes);
     if (pl.live) {
-        const long long mine = cells_of(cells, pl.lanes, pl.lane);
+        const long long mine = shares.of(pl.lane);
         float from[V], s1[V], s2[V];
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -146,18 +157,21 @@ template <int V> __global__ __launch_bounds__(256) void gn_stats_kernel(GnArgs a
     const int c0 = blockIdx.x % a.tiles * 256 * V;
     for (int j = threadIdx.x; j < wide * V && c0 + j < a.C; j += 256) {
         const int piece = j / V, e = j % V;
-        // about the first lane's mean, so that a constant map's mean is exact
-        const float ref = lds[piece][e];
+        // about the first lane's mean, so that a constant map's mean is exact; lanes
+        // are full (or one cell short) but where the slab has fewer cells than lanes
+        const float ref = lds[piece][e], all = static_cast<float>(cells);
+        const float w0 = shares.part(pl.lanes - 1, all), w1 = shares.part(0, all);
+        const float n0 = static_cast<float>(shares.of(pl.lanes - 1)), n1 = static_cast<float>(shares.of(0));
+        const int used = shares.each ? pl.lanes : shares.more;
         float mean = 0.0f, m2 = 0.0f;
-        for (int l = 1; l < pl.lanes; ++l) {
-            const float n = static_cast<float>(cells_of(cells, pl.lanes, l));
-            mean = n > 0.0f ? fmaf(lds[l * wide + piece][e] - ref, n / static_cast<float>(cells), mean) : mean;
-        }
+#pragma unroll 8
+        for (int l = 0; l < used; ++l)
+            mean = fmaf(lds[l * wide + piece][e] - ref, l < shares.more ? w1 : w0, mean);
         mean += ref;
-        for (int l = 0; l < pl.lanes; ++l) {
+#pragma unroll 8
+        for (int l = 0; l < used; ++l) {
             const float d = lds[l * wide + piece][e] - mean;
-            const float n = static_cast<float>(cells_of(cells, pl.lanes, l));
-            m2 += n > 0.0f ? fmaf(n * d, d, lds[l * wide + piece][V + e]) : 0.0f;
+            m2 += fmaf((l < shares.more ? n1 : n0) * d, d, lds[l * wide + piece][V + e]);
         }
         part[c0 + j] = mean;
         part[a.C + c0 + j] = m2;
@@ -172,36 +186,80 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// A wave joins one group's channels and slabs.
+// f(row, channel) over rows x channels by the threads i of n side by side along the
+// channels (no division inside, loads in flight together)
+template <class F> __device__ __forceinline__ void each_of_group(int i, int n, int rows, int channels, F f)
+{
+    const int wide = channels < n ? channels : n, high = n / wide;
+    const int r0 = i / wide, c0 = i - r0 * wide;
+    if (r0 < high)
+        for (int c = c0; c < channels; c += wide)
+#pragma unroll 8
+            for (int r = r0; r < rows; r += high)
+                f(r, c);
+}
+// the sum over a block of 256 threads
+__device__ __forceinline__ float block_sum(float v, float (&red)[4])
+{
+    v = wave_sum(v);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// A block joins one group's channels and slabs.
 __global__ __launch_bounds__(256) void gn_join_kernel(GnArgs a)
 {
-    const long long group = blockIdx.x * 4LL + (threadIdx.x >> 6);
-    if (group >= static_cast<long long>(a.B) * a.G)
-        return;
-    const int b = static_cast<int>(group / a.G), cpg = a.C / a.G, c0 = static_cast<int>(group % a.G) * cpg;
-    const int lane = threadIdx.x & 63;
+    __shared__ float red[4];
+    const int group = blockIdx.x, b = group / a.G, cpg = a.C / a.G, c0 = group % a.G * cpg;
     const float *part = a.part + static_cast<long long>(b) * a.slabs * 2 * a.C;
-    const long long entries = static_cast<long long>(a.slabs) * cpg;
     const float total = static_cast<float>(a.S) * static_cast<float>(cpg);
     const float ref = part[c0];
+    const float whole = static_cast<float>(a.rows), rest = static_cast<float>(a.S - (a.slabs - 1) * a.rows);
     float mean = 0.0f;
-    for (long long i = lane; i < entries; i += 64) {
-        const long long slab = i / cpg;
-        const long long cells = slab + 1 < a.slabs ? a.rows : a.S - slab * a.rows;
-        mean = fmaf(part[slab * 2 * a.C + c0 + i % cpg] - ref, static_cast<float>(cells) / total, mean);
-    }
-    mean = ref + wave_sum(mean);
+    each_of_group(threadIdx.x, 256, a.slabs, cpg, [&](int r, int c) {
+        mean = fmaf(part[r * 2LL * a.C + c0 + c] - ref, (r + 1 < a.slabs ? whole : rest) / total, mean);
+    });
+    mean = ref + block_sum(mean, red);
     float m2 = 0.0f;
-    for (long long i = lane; i < entries; i += 64) {
-        const long long slab = i / cpg;
-        const long long cells = slab + 1 < a.slabs ? a.rows : a.S - slab * a.rows;
-        const float d = part[slab * 2 * a.C + c0 + i % cpg] - mean;
-        m2 += fmaf(static_cast<float>(cells) * d, d, part[slab * 2 * a.C + a.C + c0 + i % cpg]);
-    }
-    m2 = wave_sum(m2);
-    if (lane == 0) {
+    each_of_group(threadIdx.x, 256, a.slabs, cpg, [&](int r, int c) {
+        const float d = part[r * 2LL * a.C + c0 + c] - mean;
+        m2 += fmaf((r + 1 < a.slabs ? whole : rest) * d, d, part[r * 2LL * a.C + a.C + c0 + c]);
+    });
+    m2 = block_sum(m2, red);
+    if (threadIdx.x == 0) {
         a.mean[group] = mean;
         a.rstd[group] = 1.0f / sqrtf(m2 / total + a.eps);
+    }
+}
+
+// The groups of V channels from c on, counted from channel 0 (one division).
+template <int V> struct Groups {
+    int g[V];
+    __device__ __forceinline__ Groups(int c, int cpg)
+    {
+        int of = c / cpg, in = c - of * cpg;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            g[e] = of;
+            if (++in == cpg) {
+                in = 0;
+                ++of;
+            }
+        }
+    }
+};
+// V channels' parameters, `other` without any
+template <int V> __device__ __forceinline__ void load_channels(const float *p, int c, float other, float (&v)[V])
+{
+    if (p) {
+        load_piece<V>(p, false, c, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            v[e] = other;
     }
 }
 
@@ -210,15 +268,15 @@ template <int V> struct Channels {
     float mean[V], rstd[V], gain[V], bias[V];
     __device__ __forceinline__ Channels(const GnArgs &a, const Place<V> &pl)
     {
-        const int cpg = a.C / a.G;
+        const Groups<V> gr(pl.c, a.C / a.G);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const long long group = static_cast<long long>(pl.b) * a.G + (pl.c + e) / cpg;
+            const long long group = static_cast<long long>(pl.b) * a.G + gr.g[e];
             mean[e] = a.mean[group];
             rstd[e] = a.rstd[group];
-            gain[e] = a.gain ? a.gain[pl.c + e] : 1.0f;
-            bias[e] = a.bias ? a.bias[pl.c + e] : 0.0f;
         }
+        load_channels<V>(a.gain, pl.c, 1.0f, gain);
+        load_channels<V>(a.bias, pl.c, 0.0f, bias);
     }
 };
 
@@ -318,27 +376,22 @@ template <int V> __global__ __launch_bounds__(256) void gn_bwd_sums_kernel(GnArg
 
 __global__ __launch_bounds__(256) void gn_bwd_join_kernel(GnArgs a)
 {
-    const long long group = blockIdx.x * 4LL + (threadIdx.x >> 6);
-    if (group >= static_cast<long long>(a.B) * a.G)
-        return;
-    const int b = static_cast<int>(group / a.G), cpg = a.C / a.G, c0 = static_cast<int>(group % a.G) * cpg;
-    const int lane = threadIdx.x & 63;
+    __shared__ float red[4];
+    const int group = blockIdx.x, b = group / a.G, cpg = a.C / a.G, c0 = group % a.G * cpg;
     const float *part = a.part + static_cast<long long>(b) * a.slabs * 2 * a.C;
-    const long long entries = static_cast<long long>(a.slabs) * cpg;
     float sn = 0.0f, sd = 0.0f;
-    for (long long i = lane; i < entries; i += 64) {
-        const int c = c0 + static_cast<int>(i % cpg);
-        const float *p = part + i / cpg * 2 * a.C;
-        const float gain = a.gain ? a.gain[c] : 1.0f;
-        sn = fmaf(p[c], gain, sn);
-        sd = fmaf(p[a.C + c], gain, sd);
-    }
-    sn = wave_sum(sn);
-    sd = wave_sum(sd);
-    if (lane == 0) {
+    each_of_group(threadIdx.x, 256, a.slabs, cpg, [&](int r, int c) {
+        const float *p = part + r * 2LL * a.C + c0 + c;
+        const float gain = a.gain ? a.gain[c0 + c] : 1.0f;
+        sn = fmaf(p[0], gain, sn);
+        sd = fmaf(p[a.C], gain, sd);
+    });
+    sn = block_sum(sn, red);
+    sd = block_sum(sd, red);
+    if (threadIdx.x == 0) {
         const float total = static_cast<float>(a.S) * static_cast<float>(cpg);
-        a.means[2 * group] = sd / total;
-        a.means[2 * group + 1] = sn / total;
+        a.means[2LL * group] = sd / total;
+        a.means[2LL * group + 1] = sn / total;
     }
 }
 
@@ -349,11 +402,12 @@ template <int V> __global__ __launch_bounds__(256) void gn_bwd_apply_kernel(GnAr
         return;
     const Channels<V> ch(a, pl);
     float md[V], mn[V];
+    const Groups<V> gr(pl.c, a.C / a.G);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const long long group = static_cast<long long>(pl.b) * a.G + (pl.c + e) / (a.C / a.G);
-        md[e] = a.means[2 * group];
-        mn[e] = a.means[2 * group + 1];
+        const long long group = static_cast<long long>(pl.b) * a.G + gr.g[e];
+        md[e] = a.means[2LL * group];
+        mn[e] = a.means[2LL * group + 1];
     }
 #pragma unroll 4
     for (long long s = pl.first + pl.lane; s < pl.last; s += pl.lanes) {
@@ -378,10 +432,367 @@ template <int V> __global__ __launch_bounds__(256) void gn_bwd_apply_kernel(GnAr
     }
 }
 
+// ------------------------------------------------------------------ slices
+
+constexpr int SLICE_THREADS = 512;
+
+// A block's slice: all cells of `slice` channels of one item. Of every eight items
+// each goes to one XCD (blocks go round the eight), so that slices that share cache
+// lines share an L2.
+template <int V> struct Slice {
+    int b, c0, c, lanes, lane, used;
+    bool live;
+    __device__ __forceinline__ explicit Slice(const GnArgs &a)
+    {
+        const int slices = a.C / a.slice, full = a.B / 8 * 8;
+        const int i = blockIdx.x, rest = i - full * slices;
+        b = rest < 0 ? i % 8 + i / (8 * slices) * 8 : full + rest / slices;
+        c0 = (rest < 0 ? i / 8 % slices : rest % slices) * a.slice;
+        const int wide = a.slice / V;
+        lanes = SLICE_THREADS / wide;
+        lane = threadIdx.x / wide;
+        c = c0 + V * (threadIdx.x % wide);
+        used = a.S < lanes ? static_cast<int>(a.S) : lanes;      // lanes that have cells
+        live = lane < used;
+    }
+    __device__ __forceinline__ long long at(const GnArgs &a, long long s) const { return (b * a.S + s) * a.C + c; }
+};
+
+// A piece as it lies in memory, at most 16 bytes: 8 channels are bf16 words, fewer
+// either type's.
+template <int V> struct Held {
+    uint32_t w[V == 8 ? 4 : V];
+    __device__ __forceinline__ void load(const void *p, bool bf, long long o)
+    {
+        if (V == 8 || bf) {
+            const uint16_t *q = static_cast<const uint16_t *>(p) + o;
+            if constexpr (V == 8) {
+                const u32x4 t = *reinterpret_cast<const u32x4 *>(q);
+                w[0] = t[0], w[1] = t[1], w[2] = t[2], w[3] = t[3];
+            } else if constexpr (V == 4) {
+                const u32x2 t = *reinterpret_cast<const u32x2 *>(q);
+                w[0] = t[0], w[1] = t[1];
+            } else if constexpr (V == 2) {
+                w[0] = *reinterpret_cast<const uint32_t *>(q);
+            } else {
+                w[0] = *q;
+            }
+        } else if constexpr (V < 8) {
+            float v[V];
+            load_piece<V>(p, false, o, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                w[e] = __float_as_uint(v[e]);
+        }
+    }
+    __device__ __forceinline__ void get(bool bf, float (&v)[V]) const
+    {
+        if (V == 8 || bf) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = __uint_as_float(w[V == 8 ? 0 : e]);
+        }
+    }
+};
+
+// The slice's cells as a thread walks them: its NV pieces are held, or (NV = 0) each
+// is read whenever it is wanted.
+template <int V, int NV> struct Cells {
+    Held<V> v[NV > 0 ? NV : 1];
+    __device__ __forceinline__ void load(const GnArgs &a, const Slice<V> &sl, const void *p, bool bf)
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const long long s = sl.lane + static_cast<long long>(k) * sl.lanes;
+            if (sl.live && s < a.S)
+                v[k].load(p, bf, sl.at(a, s));
+        }
+    }
+};
+// f(piece, cell) for every cell of this thread
+template <int V, int NV, class F>
+__device__ __forceinline__ void each_cell(const GnArgs &a, const Slice<V> &sl, const Cells<V, NV> &x, F f)
+{
+    float v[V];
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const long long s = sl.lane + static_cast<long long>(k) * sl.lanes;
+            if (sl.live && s < a.S) {
+                x.v[k].get(a.xbf, v);
+                f(v, s);
+            }
+        }
+    } else if (sl.live) {
+#pragma unroll 4
+        for (long long s = sl.lane; s < a.S; s += sl.lanes) {
+            load_piece<V>(a.x, V == 8 || a.xbf, sl.at(a, s), v);
+            f(v, s);
+        }
+    }
+}
+template <int V, int NV, class F>
+__device__ __forceinline__ void each_cell(const GnArgs &a, const Slice<V> &sl, const Cells<V, NV> &x,
+                                          const Cells<V, NV> &d, F f)
+{
+    float v[V], w[V];
+    if constexpr (NV > 0) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const long long s = sl.lane + static_cast<long long>(k) * sl.lanes;
+            if (sl.live && s < a.S) {
+                x.v[k].get(a.xbf, v);
+                d.v[k].get(a.dbf, w);
+                f(v, w, s);
+            }
+        }
+    } else if (sl.live) {
+#pragma unroll 2
+        for (long long s = sl.lane; s < a.S; s += sl.lanes) {
+            load_piece<V>(a.x, V == 8 || a.xbf, sl.at(a, s), v);
+            load_piece<V>(a.dout, V == 8 || a.dbf, sl.at(a, s), w);
+            f(v, w, s);
+        }
+    }
+}
+
+// Sums over a block, per group of its slice: every thread's V channels' terms go to
+// buf [used lanes][slice]; a wave adds up a group's.
+template <int V>
+__device__ __forceinline__ void group_totals(const GnArgs &a, const Slice<V> &sl, const float (&t)[V], float *buf,
+                                             float *totals)
+{
+    __syncthreads();
+    if (sl.live)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            buf[sl.lane * a.slice + sl.c - sl.c0 + e] = t[e];
+    __syncthreads();
+    const int cpg = a.C / a.G, wave = threadIdx.x >> 6;
+    for (int g = wave; g < a.slice / cpg; g += SLICE_THREADS / 64) {
+        float s = 0.0f;
+        each_of_group(threadIdx.x & 63, 64, sl.used, cpg, [&](int r, int c) { s += buf[r * a.slice + g * cpg + c]; });
+        s = wave_sum(s);
+        if ((threadIdx.x & 63) == 0)
+            totals[g] = s;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ long long b_first(const GnArgs &a, int b, int c) { return b * a.S * a.C + c; }
+
+template <int V, int NV> __global__ __launch_bounds__(SLICE_THREADS) void gn_slice_kernel(GnArgs a)
+{
+    __shared__ float buf[SLICE_THREADS * V], totals[SLICE_THREADS * V], firsts[SLICE_THREADS * V];
+    const Slice<V> sl(a);
+    const int cpg = a.C / a.G, groups = a.slice / cpg;
+    const Groups<V> gr(sl.c - sl.c0, cpg);
+    Cells<V, NV> x;
+    x.load(a, sl, a.x, a.xbf);
+    // Distances from the group's first value, so that a constant group's mean is
+    // exact and an offset costs no digits; then squares of distances from the mean.
+    for (int g = threadIdx.x; g < groups; g += SLICE_THREADS) {
+        float v[1];
+        load_piece<1>(a.x, a.xbf, b_first(a, sl.b, sl.c0 + g * cpg), v);
+        firsts[g] = v[0];
+    }
+    __syncthreads();
+    const float n = static_cast<float>(a.S) * static_cast<float>(cpg);
+    float mean[V], rstd[V], t[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        t[e] = 0.0f;
+        mean[e] = sl.live ? firsts[gr.g[e]] : 0.0f;
+    }
+    each_cell<V, NV>(a, sl, x, [&](const float (&v)[V], long long) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            t[e] += v[e] - mean[e];
+    });
+    group_totals<V>(a, sl, t, buf, totals);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        t[e] = 0.0f;
+        if (sl.live)
+            mean[e] += totals[gr.g[e]] / n;
+    }
+    if (threadIdx.x < static_cast<unsigned>(groups) && a.mean)
+        a.mean[static_cast<long long>(sl.b) * a.G + sl.c0 / cpg + threadIdx.x] = firsts[threadIdx.x] + totals[threadIdx.x] / n;
+    each_cell<V, NV>(a, sl, x, [&](const float (&v)[V], long long) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            t[e] = fmaf(v[e] - mean[e], v[e] - mean[e], t[e]);
+    });
+    group_totals<V>(a, sl, t, buf, totals);
+    if (threadIdx.x < static_cast<unsigned>(groups) && a.rstd)
+        a.rstd[static_cast<long long>(sl.b) * a.G + sl.c0 / cpg + threadIdx.x] = 1.0f / sqrtf(totals[threadIdx.x] / n + a.eps);
+    if (!sl.live)
+        return;
+    float gain[V], bias[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        rstd[e] = 1.0f / sqrtf(totals[gr.g[e]] / n + a.eps);
+    }
+    load_channels<V>(a.gain, sl.c, 1.0f, gain);
+    load_channels<V>(a.bias, sl.c, 0.0f, bias);
+    each_cell<V, NV>(a, sl, x, [&](const float (&v)[V], long long s) __attribute__((always_inline)) {
+        float y[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            y[e] = fmaf((v[e] - mean[e]) * rstd[e], gain[e], bias[e]);
+        act_piece<V>(y, a.act);
+        store_piece<V>(a.out, a.obf, sl.at(a, s), y);
+    });
+}
+
+template <int V, int NV> __global__ __launch_bounds__(SLICE_THREADS) void gn_slice_bwd_kernel(GnArgs a)
+{
+    __shared__ float buf[2][SLICE_THREADS * V], sums[2][SLICE_THREADS * V];
+    const Slice<V> sl(a);
+    const int cpg = a.C / a.G;
+    Cells<V, NV> x, d;
+    x.load(a, sl, a.x, a.xbf);
+    d.load(a, sl, a.dout, a.dbf);
+    const Groups<V> gr(sl.c - sl.c0, cpg);
+    float mean[V], rstd[V], gain[V], bias[V], tn[V], td[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        tn[e] = td[e] = 0.0f;
+        mean[e] = rstd[e] = gain[e] = bias[e] = 0.0f;
+        if (sl.live) {
+            const long long group = static_cast<long long>(sl.b) * a.G + sl.c0 / cpg + gr.g[e];
+            mean[e] = a.mean[group];
+            rstd[e] = a.rstd[group];
+        }
+    }
+    if (sl.live) {
+        load_channels<V>(a.gain, sl.c, 1.0f, gain);
+        load_channels<V>(a.bias, sl.c, 0.0f, bias);
+    }
+    // n and dz of a cell
+    const auto form = [&](const float (&v)[V], const float (&w)[V], float (&n)[V], float (&dz)[V]) __attribute__((always_inline)) {
+        float z[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            n[e] = (v[e] - mean[e]) * rstd[e];
+            z[e] = fmaf(n[e], gain[e], bias[e]);
+            dz[e] = w[e];
+        }
+        slope_piece<V>(z, a.act, dz);
+    };
+    each_cell<V, NV>(a, sl, x, d, [&](const float (&v)[V], const float (&w)[V], long long) __attribute__((always_inline)) {
+        float n[V], dz[V];
+        form(v, w, n, dz);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            tn[e] = fmaf(dz[e], n[e], tn[e]);
+            td[e] += dz[e];
+        }
+    });
+    if (sl.live)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            buf[0][sl.lane * a.slice + sl.c - sl.c0 + e] = tn[e];
+            buf[1][sl.lane * a.slice + sl.c - sl.c0 + e] = td[e];
+        }
+    __syncthreads();
+    // a channel's sums: a wave each
+    for (int i = threadIdx.x >> 6; i < 2 * a.slice; i += SLICE_THREADS / 64) {
+        const int which = i >= a.slice, c = i - which * a.slice;
+        float s = 0.0f;
+        for (int l = threadIdx.x & 63; l < sl.used; l += 64)
+            s += buf[which][l * a.slice + c];
+        s = wave_sum(s);
+        if ((threadIdx.x & 63) == 0) {
+            sums[which][c] = s;
+            if (a.part)
+                a.part[static_cast<long long>(sl.b) * 2 * a.C + which * a.C + sl.c0 + c] = s;
+        }
+    }
+    __syncthreads();
+    if (!a.out)
+        return;
+    // a group's means: its channels' sums times their gains
+    for (int g = threadIdx.x; g < a.slice / cpg; g += SLICE_THREADS) {
+        float sn = 0.0f, sd = 0.0f;
+        for (int c = g * cpg; c < (g + 1) * cpg; ++c) {
+            const float w = a.gain ? a.gain[sl.c0 + c] : 1.0f;
+            sn = fmaf(sums[0][c], w, sn);
+            sd = fmaf(sums[1][c], w, sd);
+        }
+        const float n = static_cast<float>(a.S) * static_cast<float>(cpg);
+        buf[0][g] = sn / n;
+        buf[1][g] = sd / n;
+    }
+    __syncthreads();
+    if (!sl.live)
+        return;
+    float mn[V], md[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        mn[e] = buf[0][gr.g[e]];
+        md[e] = buf[1][gr.g[e]];
+    }
+    each_cell<V, NV>(a, sl, x, d, [&](const float (&v)[V], const float (&w)[V], long long s) __attribute__((always_inline)) {
+        float n[V], dz[V];
+        form(v, w, n, dz);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            n[e] = rstd[e] * (dz[e] * gain[e] - md[e] - n[e] * mn[e]);
+        if (a.add) {
+            float add[V];
+            load_piece<V>(a.add, a.xbf, sl.at(a, s), add);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                n[e] += add[e];
+        }
+        store_piece<V>(a.out, a.obf, sl.at(a, s), n);
+    });
+}
+
 // ------------------------------------------------------------------ launches
 
 // The widest piece that divides a row.
 int piece_of(int C) { return C % 8 == 0 ? 8 : C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1; }
+
+// A slice's pieces are 16 bytes at most of the wider type that it holds.
+int slice_piece(const GnArgs &a)
+{
+    const int v = piece_of(a.C);
+    return v == 8 && !(a.xbf && (!a.dout || a.dbf)) ? 4 : v;
+}
+// The pieces of V channels that a thread holds of a slice of w, 0: it reads them again.
+// Backward there are two arrays to hold: eight pieces of each leave two waves a SIMD,
+// and reading again is faster (64 x 3136 x 64 bf16 30.9 us, 39.8 held).
+int held(long long S, int w, int v, bool backward = false)
+{
+    const int lanes = SLICE_THREADS / (w / v);
+    return S <= 2LL * lanes ? 2 : S <= 8LL * lanes && !backward ? 8 : 0;
+}
+// The slice: whole groups and pieces, wider while that leaves a block for every CU and
+// the cells in registers. None (slabs instead) where it is wider than a block's
+// threads, or where the slices are too few to fill the card and long. The same for
+// every type: pieces of 4 at most are counted.
+void cut_slices(GnArgs &a)
+{
+    const int v = piece_of(a.C), v4 = v < 4 ? v : 4, cpg = a.C / a.G;
+    int w = cpg;
+    while (w % v)
+        w += cpg;
+    a.slice = 0;
+    if (w / v4 > SLICE_THREADS)
+        return;
+    while (a.C % (2 * w) == 0 && static_cast<long long>(a.B) * (a.C / (2 * w)) >= 256 && 2 * w <= 64 &&
+           held(a.S, 2 * w, v4) == held(a.S, w, v4))
+        w *= 2;
+    if (static_cast<long long>(a.B) * (a.C / w) < 128 && a.S > 32LL * (SLICE_THREADS / (w / v4)))
+        return;
+    a.slice = w;
+}
 
 // Slabs of at least 8 cells a lane, as many as make about 4 blocks per CU.
 void cut_map(GnArgs &a)
@@ -397,7 +808,8 @@ void cut_map(GnArgs &a)
     a.slabs = static_cast<int>((a.S + a.rows - 1) / a.rows);
 }
 
-size_t part_floats(const GnArgs &a) { return static_cast<size_t>(a.B) * a.slabs * 2 * a.C; }
+// slices take none forward; backward a sum of every item's channels
+size_t part_floats(const GnArgs &a) { return static_cast<size_t>(a.B) * (a.slice ? 1 : a.slabs) * 2 * a.C; }
 size_t group_floats(const GnArgs &a) { return 2 * static_cast<size_t>(a.B) * a.G; }
 
 #define SRNL_GN_LAUNCH(kernel, a, st)                                                                  \
@@ -411,9 +823,28 @@ size_t group_floats(const GnArgs &a) { return 2 * static_cast<size_t>(a.B) * a.G
         }                                                                                              \
     } while (0)
 
+#define SRNL_GN_SLICE_NV(kernel, V, MORE, a, st)                                                       \
+    do {                                                                                               \
+        const dim3 grid(static_cast<unsigned>(static_cast<long long>((a).B) * ((a).C / (a).slice)));   \
+        const int nv = held((a).S, (a).slice, V, (a).dout != nullptr);                                 \
+        if (nv == 2)                                                                                   \
+            hipLaunchKernelGGL((kernel<V, 2>), grid, dim3(SLICE_THREADS), 0, st, a);                   \
+        else if (nv == MORE)                                                                           \
+            hipLaunchKernelGGL((kernel<V, MORE>), grid, dim3(SLICE_THREADS), 0, st, a);                \
+        else                                                                                           \
+            hipLaunchKernelGGL((kernel<V, 0>), grid, dim3(SLICE_THREADS), 0, st, a);                   \
+    } while (0)
+#define SRNL_GN_SLICE(kernel, MORE, a, st)                          \
+    switch (slice_piece(a)) {                                       \
+    case 8: SRNL_GN_SLICE_NV(kernel, 8, MORE, a, st); break;             \
+    case 4: SRNL_GN_SLICE_NV(kernel, 4, MORE, a, st); break;             \
+    case 2: SRNL_GN_SLICE_NV(kernel, 2, MORE, a, st); break;             \
+    default: SRNL_GN_SLICE_NV(kernel, 1, MORE, a, st); break;            \
+    }
+
 dim3 join_grid(const GnArgs &a)
 {
-    return dim3(static_cast<unsigned>((static_cast<long long>(a.B) * a.G + 3) / 4));
+    return dim3(static_cast<unsigned>(a.B * a.G));
 }
 
 srnl_status check_gn(int B, long long S, int C, int G, srnl_dtype x, srnl_dtype out, float eps, int act)
@@ -424,7 +855,7 @@ srnl_status check_gn(int B, long long S, int C, int G, srnl_dtype x, srnl_dtype 
         return fail(SRNL_ERR_ARG, "C must be >= 1 and a multiple of groups");
     if (C > 1 << 20 || static_cast<__int128>(B) * S * C >= (static_cast<__int128>(1) << 60) || S >= 1LL << 40)
         return fail(SRNL_ERR_ARG, "map too large");
-    // an item and tile of channels is a block, a group a wave
+    // an item and tile of channels is a block, and so is a group
     if (static_cast<__int128>(B) * C > 1 << 23)
         return fail(SRNL_ERR_ARG, "B x C is too large");
     if (!valid_dtype(x) || !valid_dtype(out))
@@ -450,7 +881,9 @@ GnArgs gn_args(const void *x, int B, long long S, int C, int G, srnl_dtype x_dty
     a.bias = bias;
     a.eps = eps;
     a.act = act;
-    cut_map(a);
+    cut_slices(a);
+    if (!a.slice)
+        cut_map(a);
     return a;
 }
 
@@ -463,7 +896,7 @@ size_t srnl_group_norm_fwd_workspace_bytes(int B, long long S, int C, int groups
     if (check_gn(B, S, C, groups, SRNL_F32, SRNL_F32, 1.0f, 0) != SRNL_OK || B == 0 || S == 0)
         return 0;
     const GnArgs a = gn_args(nullptr, B, S, C, groups, SRNL_F32, nullptr, nullptr, 1.0f, 0);
-    return (part_floats(a) + group_floats(a)) * sizeof(float);
+    return a.slice ? 0 : (part_floats(a) + group_floats(a)) * sizeof(float);
 }
 
 srnl_status srnl_group_norm_fwd(const void *x, int B, long long S, int C, int groups, srnl_dtype in_dtype,
@@ -483,21 +916,27 @@ srnl_status srnl_group_norm_fwd(const void *x, int B, long long S, int C, int gr
             s = zero_fill(mean, static_cast<long long>(B) * groups, st);
         return s == SRNL_OK ? zero_fill(rstd, static_cast<long long>(B) * groups, st) : s;
     }
-    if (!workspace || workspace_bytes < srnl_group_norm_fwd_workspace_bytes(B, S, C, groups))
+    GnArgs a = gn_args(x, B, S, C, groups, in_dtype, gain, bias, eps, act);
+    if (!a.slice && (!workspace || workspace_bytes < srnl_group_norm_fwd_workspace_bytes(B, S, C, groups)))
         return fail(SRNL_ERR_WORKSPACE, "workspace smaller than srnl_group_norm_fwd_workspace_bytes");
     const PtrArg ptrs[] = {{x, "x", false},       {out, "out", false},  {gain, "gain", true},
                            {bias, "bias", true},  {mean, "mean", true}, {rstd, "rstd", true},
-                           {workspace, "workspace", false}};
+                           {a.slice ? nullptr : workspace, "workspace", true}};
     s = check_ptrs(ptrs, 7);
     if (s != SRNL_OK)
         return s;
-    GnArgs a = gn_args(x, B, S, C, groups, in_dtype, gain, bias, eps, act);
+    a.out = out;
+    a.obf = out_dtype == SRNL_BF16;
+    if (a.slice) {
+        a.mean = mean;
+        a.rstd = rstd;
+        SRNL_GN_SLICE(gn_slice_kernel, 8, a, st);
+        return launched("gn_slice_kernel");
+    }
     a.part = static_cast<float *>(workspace);
     float *own = a.part + part_floats(a);
     a.mean = mean ? mean : own;
     a.rstd = rstd ? rstd : own + static_cast<long long>(B) * groups;
-    a.out = out;
-    a.obf = out_dtype == SRNL_BF16;
     SRNL_GN_LAUNCH(gn_stats_kernel, a, st);
     hipLaunchKernelGGL(gn_join_kernel, join_grid(a), dim3(256), 0, st, a);
     SRNL_GN_LAUNCH(gn_apply_kernel, a, st);
@@ -506,7 +945,10 @@ srnl_status srnl_group_norm_fwd(const void *x, int B, long long S, int C, int gr
 
 size_t srnl_group_norm_bwd_workspace_bytes(int B, long long S, int C, int groups)
 {
-    return srnl_group_norm_fwd_workspace_bytes(B, S, C, groups);
+    if (check_gn(B, S, C, groups, SRNL_F32, SRNL_F32, 1.0f, 0) != SRNL_OK || B == 0 || S == 0)
+        return 0;
+    const GnArgs a = gn_args(nullptr, B, S, C, groups, SRNL_F32, nullptr, nullptr, 1.0f, 0);
+    return (part_floats(a) + (a.slice ? 0 : group_floats(a))) * sizeof(float);
 }
 
 srnl_status srnl_group_norm_bwd(const void *dout, srnl_dtype out_dtype, const void *x, int B, long long S, int C,
@@ -545,6 +987,13 @@ srnl_status srnl_group_norm_bwd(const void *dout, srnl_dtype out_dtype, const vo
     a.add = dx_add;
     a.out = dx;
     a.obf = a.xbf;
+    if (a.slice) {
+        SRNL_GN_SLICE(gn_slice_bwd_kernel, 2, a, st);
+        s = launched("gn_slice_bwd_kernel");
+        if (s != SRNL_OK || (!dgain && !dbias))
+            return s;
+        return sum_rows(a.part, a.B, 2LL * C, 2LL * C, C, dgain, dbias, st);
+    }
     SRNL_GN_LAUNCH(gn_bwd_sums_kernel, a, st);
     if (dx) {
         hipLaunchKernelGGL(gn_bwd_join_kernel, join_grid(a), dim3(256), 0, st, a);
