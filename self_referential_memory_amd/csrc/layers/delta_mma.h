@@ -224,25 +224,6 @@ template <bool BF> __device__ __forceinline__ In<BF> in_load(const Buf &b, int o
     __builtin_memcpy(&f, t, sizeof f);
     return f;
 }
-__device__ __forceinline__ float in_squares(const In<true> &f)
-{
-    u32x4 w;
-    __builtin_memcpy(&w, &f, 16);
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        s = fmaf(bf16_lo(w[j]), bf16_lo(w[j]), fmaf(bf16_hi(w[j]), bf16_hi(w[j]), s));
-    return s;
-}
-__device__ __forceinline__ float in_squares(const In<false> &f)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        s = fmaf(f.v[j], f.v[j], s);
-    return s;
-}
-
 // ---- split values
 
 // An operand of X or P in memory lies as a wave reads it, 16 bytes a lane after

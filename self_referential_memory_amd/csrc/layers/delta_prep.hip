@@ -12,25 +12,49 @@ namespace {
 
 using namespace srnl_i;
 
+template <bool BF, int KD> struct PrepShared {
+    union {
+        Rows<BF, KD> k;                // until the products are formed
+        struct {
+            __attribute__((aligned(16))) float L[64][68], X[64][68];
+        } m;
+    };
+    float ghi[64], glo[64], beta[64], rk[64], rq[64], gam[64], end[64];
+};
+
 template <bool BF, int KD, bool TRANSPOSED>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
 {
     constexpr int KF = KD / 32;
-    __shared__ __attribute__((aligned(16))) float L[64][68], X[64][68];
-    __shared__ float ghi[64], glo[64], bet[64], rks[64], rqs[64], gam[64], end[64];
+    __shared__ PrepShared<BF, KD> sh;
+    auto &L = sh.m.L, &X = sh.m.X;
     const int c = blockIdx.x % a.N, bh = blockIdx.x / a.N;
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
     const int n = delta_tokens(a, b), tok0 = DELTA_CHUNK * c;
     if (tok0 >= n)
         return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, quad = lane >> 4, l15 = lane & 15;
-    float *vec = a.vec + static_cast<long long>(blockIdx.x) * VEC_FLOATS;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, quad = lane >> 4, l15 = lane & 15;
+    const long long tok = static_cast<long long>(b) * a.T + tok0;
+    const int row = 16 * wave + l15;
 
+    In<BF> kf[KF], qf[KF];
+    {
+        const Buf bk(a.k, (tok * a.ks + static_cast<long long>(hk) * a.Dk) * (BF ? 2 : 4));
+        const Buf bq(a.q, (tok * a.qs + static_cast<long long>(hk) * a.Dk) * (BF ? 2 : 4));
+#pragma unroll
+        for (int f = 0; f < KF; ++f) {
+            const int k = 32 * f + 8 * quad;
+            const bool live = both(tok0 + row < n, k < a.Dk);
+            kf[f] = in_load<BF>(bk, row * static_cast<int>(a.ks) + k, live);
+            qf[f] = in_load<BF>(bq, row * static_cast<int>(a.qs) + k, live);
+        }
+    }
     if (wave == 0) {
         // sums in 64 bits: what matters later is their differences. Below -1000 a
         // factor is 0 either way; -infinity would make NaN of a difference.
         const bool live = tok0 + lane < n;
-        const long long at = (static_cast<long long>(b) * a.T + tok0 + lane) * a.H + h;
+        const long long at = (tok + lane) * a.H + h;
         const float g = live ? a.g[at] : 0.0f;
         double G = g < -1000.0f ? -1000.0 : static_cast<double>(g);
 #pragma unroll
@@ -40,85 +64,84 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
                 G += o;
         }
         const float hi = static_cast<float>(G), lo = static_cast<float>(G - hi);
-        const float beta = live ? a.beta[at] : 0.0f;
         const double left = __shfl(G, 63) - G;
         const float lhi = static_cast<float>(left);
-        ghi[lane] = hi;
-        glo[lane] = lo;
-        bet[lane] = beta;
-        gam[lane] = expf(hi) * (1.0f + lo);
-        end[lane] = expf(lhi) * (1.0f + static_cast<float>(left - lhi));
+        sh.ghi[lane] = hi;
+        sh.glo[lane] = lo;
+        sh.beta[lane] = live ? a.beta[at] : 0.0f;
+        sh.gam[lane] = expf(hi) * (1.0f + lo);
+        sh.end[lane] = expf(lhi) * (1.0f + static_cast<float>(left - lhi));
     }
-
-    const long long tok = static_cast<long long>(b) * a.T + tok0;
-    const Buf bk(a.k, (tok * a.ks + static_cast<long long>(hk) * a.Dk) * (BF ? 2 : 4));
-    const Buf bq(a.q, (tok * a.qs + static_cast<long long>(hk) * a.Dk) * (BF ? 2 : 4));
-    const int ks = static_cast<int>(a.ks), qs = static_cast<int>(a.qs);
-    const int row = 16 * wave + l15;
-    In<BF> kf[KF], qf[KF];
-    float kk = 0.0f, qq = 0.0f;
 #pragma unroll
-    for (int f = 0; f < KF; ++f) {
-        const int k = 32 * f + 8 * quad;
-        const bool live = tok0 + row < n && k < a.Dk;
-        kf[f] = in_load<BF>(bk, row * ks + k, live);
-        qf[f] = in_load<BF>(bq, row * qs + k, live);
-        kk += in_squares(kf[f]);
-        qq += in_squares(qf[f]);
+    for (int f = 0; f < KF; ++f)
+        sh.k.put(row, 32 * f + 8 * quad, kf[f]);
+    __syncthreads();
+
+    // k_i.k_j and q_i.k_j of this wave's rows, and q_i.q_i: the norms are diagonals
+    v4f m[4], p[4], qq = v4f_zero();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m[j] = p[j] = v4f_zero();
+        if (j <= wave)
+#pragma unroll
+            for (int f = 0; f < KF; ++f) {
+                const In<BF> o = sh.k.across(16 * j + l15, 32 * f + 8 * quad);
+                m[j] = mma(kf[f], o, m[j]);
+                p[j] = mma(qf[f], o, p[j]);
+            }
     }
-    kk += __shfl_xor(kk, 16);
-    kk += __shfl_xor(kk, 32);
-    qq += __shfl_xor(qq, 16);
-    qq += __shfl_xor(qq, 32);
-    if (quad == 0) {
+    if (a.eps > 0.0f) {
+#pragma unroll
+        for (int f = 0; f < KF; ++f)
+            qq = mma(qf[f], qf[f], qq);
+    }
+    if (quad == l15 >> 2) {
         // a row past the end has no direction: its factor is 0, not 1 / sqrt(eps)
+        const v4f kk = wave == 0 ? m[0] : wave == 1 ? m[1] : wave == 2 ? m[2] : m[3];
+        const int e = l15 & 3;
+        const float k2 = e == 0 ? kk[0] : e == 1 ? kk[1] : e == 2 ? kk[2] : kk[3];
+        const float q2 = e == 0 ? qq[0] : e == 1 ? qq[1] : e == 2 ? qq[2] : qq[3];
         const bool live = tok0 + row < n;
-        const float rk = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
-        const float rq = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(qq + a.eps) : 1.0f;
-        rks[row] = rk;
-        rqs[row] = rq;
+        sh.rk[row] = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(k2 + a.eps) : 1.0f;
+        sh.rq[row] = !live ? 0.0f : a.eps > 0.0f ? 1.0f / sqrtf(q2 + a.eps) : 1.0f;
     }
     __syncthreads();
-    if (wave == 3) {
-        const float ga = gam[lane], en = end[lane], be = bet[lane], rk = rks[lane], rq = rqs[lane];
+    if (wave == 0) {
+        float *vec = a.vec + static_cast<long long>(blockIdx.x) * VEC_FLOATS;
+        const float ga = sh.gam[lane], en = sh.end[lane], be = sh.beta[lane], rk = sh.rk[lane], rq = sh.rq[lane];
         vec[VEC_GAM + lane] = ga;
         vec[VEC_END + lane] = en;
         vec[VEC_BETA + lane] = be;
         vec[VEC_RK + lane] = rk;
         vec[VEC_RQ + lane] = rq;
-        vec[VEC_GHI + lane] = ghi[lane];
-        vec[VEC_GLO + lane] = glo[lane];
+        vec[VEC_GHI + lane] = sh.ghi[lane];
+        vec[VEC_GLO + lane] = sh.glo[lane];
         vec[VEC_READK + lane] = ga * rk;
         vec[VEC_WRITE + lane] = en * be * rk;
         vec[VEC_READQ + lane] = a.scale * ga * rq;
     }
-
-    v4f p[4];
+    {
+        const int i0 = 16 * wave + 4 * quad;
+        const v4f ihi = *reinterpret_cast<const v4f *>(&sh.ghi[i0]), ilo = *reinterpret_cast<const v4f *>(&sh.glo[i0]);
+        const v4f ri = *reinterpret_cast<const v4f *>(&sh.rk[i0]);
+        const v4f qi = *reinterpret_cast<const v4f *>(&sh.rq[i0]) * a.scale;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        p[j] = v4f_zero();
-        if (j > wave) {
+        for (int j = 0; j < 4; ++j) {
+            const int col = 16 * j + l15;
+            if (j > wave) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                X[16 * wave + 4 * quad + r][16 * j + l15] = 0.0f;
-            continue;
-        }
-        const int col = 16 * j + l15;
-        v4f m = v4f_zero();
+                for (int r = 0; r < 4; ++r)
+                    X[i0 + r][col] = 0.0f;
+                continue;
+            }
+            const float jhi = sh.ghi[col], jlo = sh.glo[col], rj = sh.rk[col], bj = sh.beta[col];
 #pragma unroll
-        for (int f = 0; f < KF; ++f) {
-            const int k = 32 * f + 8 * quad;
-            const In<BF> o = in_load<BF>(bk, col * ks + k, tok0 + col < n && k < a.Dk);
-            m = mma(kf[f], o, m);
-            p[j] = mma(qf[f], o, p[j]);
-        }
-        const float jhi = ghi[col], jlo = glo[col], rj = rks[col], bj = bet[col];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * wave + 4 * quad + r;
-            const float d = decay(ghi[i], glo[i], jhi, jlo) * rj;
-            L[i][col] = col < i ? m[r] * rks[i] * d * bj : 0.0f;
-            p[j][r] = col <= i ? p[j][r] * rqs[i] * d * a.scale : 0.0f;
+            for (int r = 0; r < 4; ++r) {
+                const float d = decay(ihi[r], ilo[r], jhi, jlo) * rj;
+                const float x = m[j][r] * ri[r] * (d * bj), y = p[j][r] * qi[r] * d;
+                L[i0 + r][col] = j < wave || col < i0 + r ? x : 0.0f;
+                p[j][r] = j < wave || col <= i0 + r ? y : 0.0f;
+            }
         }
     }
     __syncthreads();
@@ -168,12 +191,15 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a)
         for (int r = 0; r < 4; ++r)
             L[16 * wave + 4 * quad + r][16 * j + l15] = p[j][r];
     __syncthreads();
-    // P itself meets outputs alone, its transpose the states' gradients
+    // P itself meets outputs alone, its transpose the states' gradients. The half of a
+    // row that is zero is not written: nobody reads it.
     constexpr int PP = TRANSPOSED ? 3 : 2;
     char *xo = a.X + static_cast<long long>(blockIdx.x) * DELTA_SQUARE;
     char *po = a.P + static_cast<long long>(blockIdx.x) * DELTA_SQUARE;
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
+        if (f == (TRANSPOSED ? 0 : 1) && (TRANSPOSED ? wave >= 2 : wave < 2))
+            continue;
         const int k = 32 * f + 8 * quad;
         float x[8], y[8];
 #pragma unroll

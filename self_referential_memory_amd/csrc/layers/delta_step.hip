@@ -9,60 +9,76 @@
 // the rows serves both, the norms and q.k.
 //
 // The call is bound by the state: 2 x 4 bytes per entry, read once and written
-// once; a block keeps a 64-column slab of it in registers over all its tokens.
+// once; a block keeps a slab of its columns in registers over all its tokens. q and
+// k of a token go through LDS: read from memory by every thread that needs them,
+// their loads, one per row, would outnumber the state's (256 sequences, 16 heads of
+// 128 x 128: 198 us, 101 us so, as fast as a copy).
 #include "delta.h"
+#include "linear.h"
 
 namespace {
 
 using namespace srnl_i;
 
-__device__ __forceinline__ float element(const void *p, bool bf, long long o)
+// 256 threads: 256 / LANES row groups x LANES lanes of 4 columns; a thread holds R
+// rows one after the other.
+template <int R, int LANES> __global__ __launch_bounds__(256, 4) void delta_step_kernel(DeltaArgs a)
 {
-    return bf ? bf16_one(static_cast<const uint16_t *>(p)[o]) : static_cast<const float *>(p)[o];
-}
-
-// 256 threads: 16 row groups x 16 lanes of 4 columns; a thread holds rows
-// group, group + 16, ... (R of them).
-template <int R>
-__global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a)
-{
-    __shared__ float part[2][4][16][8];
+    constexpr int GROUPS = 256 / LANES, WIDTH = 4 * LANES;
+    __shared__ float part[2][4][LANES][8];
     __shared__ float dots[2][4][3];
-    const int tiles = (a.Dv + 63) / 64;
+    __shared__ __attribute__((aligned(16))) float kq[2][2][GROUPS * R];
+    const int tiles = (a.Dv + WIDTH - 1) / WIDTH;
     const int bh = blockIdx.x / tiles, tile = blockIdx.x - bh * tiles;
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
-    const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    const int col = 64 * tile + 4 * lane;
+    const int lane = threadIdx.x % LANES, grp = threadIdx.x / LANES, wave = threadIdx.x >> 6;
+    const int col = WIDTH * tile + 4 * lane, row0 = grp * R;
     const bool mine = col < a.Dv;                       // Dv is a multiple of 8
     const long long base = static_cast<long long>(bh) * a.Dk * a.Dv + col;
     const int n = delta_tokens(a, b);
 
+    // a token's k (threads 0 ..) and q (threads 128 ..), 4 values a thread
+    const int half = threadIdx.x >> 7, piece = 4 * (threadIdx.x & 127);
+    const bool fetches = piece < GROUPS * R;
+    float ahead[4] = {0, 0, 0, 0};
+    const auto fetch = [&](int t) __attribute__((always_inline)) {
+        const long long tok = static_cast<long long>(b) * a.T + t;
+        if (piece < a.Dk) {
+            if (half == 0)
+                load_row<4, true>(a.k, a.bf, tok * a.ks + hk * a.Dk + piece, 4, ahead);
+            else
+                load_row<4, true>(a.q, a.bf, tok * a.qs + hk * a.Dk + piece, 4, ahead);
+        }
+    };
+    if (n > 0)
+        fetch(0);
     f32x4 S[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int row = grp + 16 * i;
         S[i] = f32x4{0, 0, 0, 0};
-        if (a.state && mine && row < a.Dk)
-            S[i] = *reinterpret_cast<const f32x4 *>(a.state + base + static_cast<long long>(row) * a.Dv);
+        if (a.state && mine && row0 + i < a.Dk)
+            S[i] = *reinterpret_cast<const f32x4 *>(a.state + base + static_cast<long long>(row0 + i) * a.Dv);
     }
     for (int t = 0; t < n; ++t) {
         const long long tok = static_cast<long long>(b) * a.T + t;
-        float kr[R], qr[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = grp + 16 * i;
-            kr[i] = qr[i] = 0.0f;
-            if (row < a.Dk) {
-                kr[i] = element(a.k, a.bf, tok * a.ks + hk * a.Dk + row);
-                qr[i] = element(a.q, a.bf, tok * a.qs + hk * a.Dk + row);
-            }
-        }
+        const int buf = t & 1;
+        if (fetches)
+            *reinterpret_cast<f32x4 *>(&kq[buf][half][piece]) = f32x4{ahead[0], ahead[1], ahead[2], ahead[3]};
         float v[4] = {0, 0, 0, 0};
         if (mine)
             load_row<4, true>(a.v, a.bf, tok * a.vs + static_cast<long long>(h) * a.Dv + col, 4, v);
         const float dec = expf(a.g[tok * a.H + h]), beta = a.beta[tok * a.H + h];
+        if (t + 1 < n)
+            fetch(t + 1);
+        lds_barrier();
+        float kr[R], qr[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            kr[i] = kq[buf][0][row0 + i];
+            qr[i] = kq[buf][1][row0 + i];
+        }
         f32x4 sk = {0, 0, 0, 0}, sq = {0, 0, 0, 0};
-        float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+        float kk = 0.0f, qq = 0.0f, kq1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
 #pragma unroll
@@ -72,25 +88,24 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a)
             }
             kk = fmaf(kr[i], kr[i], kk);
             qq = fmaf(qr[i], qr[i], qq);
-            kq = fmaf(kr[i], qr[i], kq);
+            kq1 = fmaf(kr[i], qr[i], kq1);
         }
-        // over the wave's 4 row groups, then over the 4 waves; two buffers, so
-        // one barrier per token is enough
-        float red[11] = {sk[0], sk[1], sk[2], sk[3], sq[0], sq[1], sq[2], sq[3], kk, qq, kq};
+        // over the wave's row groups, then over the 4 waves; two buffers, so that two
+        // barriers per token are enough
+        float red[11] = {sk[0], sk[1], sk[2], sk[3], sq[0], sq[1], sq[2], sq[3], kk, qq, kq1};
 #pragma unroll
-        for (int j = 0; j < 11; ++j) {
-            red[j] += __shfl_xor(red[j], 16);
-            red[j] += __shfl_xor(red[j], 32);
-        }
-        const int buf = t & 1;
-        if ((threadIdx.x & 63) < 16) {
+        for (int j = 0; j < 11; ++j)
+#pragma unroll
+            for (int off = LANES; off < 64; off <<= 1)
+                red[j] += __shfl_xor(red[j], off);
+        if ((threadIdx.x & 63) < LANES) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 part[buf][wave][lane][j] = red[j];
             if (lane < 3)
                 dots[buf][wave][lane] = lane == 0 ? red[8] : lane == 1 ? red[9] : red[10];
         }
-        __syncthreads();
+        lds_barrier();
         float sum[8], dot[3];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -121,12 +136,23 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a)
     }
     if (a.state_out && mine) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int row = grp + 16 * i;
-            if (row < a.Dk)
-                *reinterpret_cast<f32x4 *>(a.state_out + base + static_cast<long long>(row) * a.Dv) = S[i];
-        }
+        for (int i = 0; i < R; ++i)
+            if (row0 + i < a.Dk)
+                *reinterpret_cast<f32x4 *>(a.state_out + base + static_cast<long long>(row0 + i) * a.Dv) = S[i];
     }
+}
+
+template <int LANES> void launch_step(const DeltaArgs &a, hipStream_t st)
+{
+    constexpr int GROUPS = 256 / LANES;
+    const long long tiles = (a.Dv + 4 * LANES - 1) / (4 * LANES);
+    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.H * tiles));
+    if (a.Dk <= 32)
+        hipLaunchKernelGGL((delta_step_kernel<32 / GROUPS, LANES>), grid, dim3(256), 0, st, a);
+    else if (a.Dk <= 64)
+        hipLaunchKernelGGL((delta_step_kernel<64 / GROUPS, LANES>), grid, dim3(256), 0, st, a);
+    else
+        hipLaunchKernelGGL((delta_step_kernel<128 / GROUPS, LANES>), grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
@@ -135,13 +161,11 @@ namespace srnl_i {
 
 srnl_status launch_delta_step(const DeltaArgs &a, hipStream_t st)
 {
-    const dim3 grid(static_cast<unsigned>(static_cast<long long>(a.B) * a.H * ((a.Dv + 63) / 64)));
-    if (a.Dk <= 32)
-        hipLaunchKernelGGL(delta_step_kernel<2>, grid, dim3(256), 0, st, a);
-    else if (a.Dk <= 64)
-        hipLaunchKernelGGL(delta_step_kernel<4>, grid, dim3(256), 0, st, a);
+    // 64 columns a block; 32 where that leaves compute units idle
+    if (static_cast<long long>(a.B) * a.H * ((a.Dv + 63) / 64) >= 256)
+        launch_step<16>(a, st);
     else
-        hipLaunchKernelGGL(delta_step_kernel<8>, grid, dim3(256), 0, st, a);
+        launch_step<8>(a, st);
     return launched("delta_step_kernel");
 }
 
