@@ -997,7 +997,8 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     return step
 
 
-def _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream):
+def _delta_shapes(q, k, v, g, beta, state, lengths):
+    """(B, T, Hk, H, Dk, Dv) of a call whose shapes and types agree."""
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if t.dim() != 4:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [B, T, heads, D]")
@@ -1009,10 +1010,14 @@ def _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream):
     _expect(beta, (B, T, H), torch.float32, "beta")
     _expect(state, (B, H, Dk, Dv), torch.float32, "state")
     _expect(lengths, (B,), torch.int32, "lengths")
+    return B, T, Hk, H, Dk, Dv
+
+
+def _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream):
     return GatedDeltaParams(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(beta), _ptr(state), _ptr(lengths),
-        B, T, Hk, H, Dk, Dv, _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
-        _dtype_code(q), Dk ** -0.5 if scale is None else scale, norm_eps, _stream(stream, q))
+        *sizes, _token_stride(q, "q"), _token_stride(k, "k"), _token_stride(v, "v"),
+        _dtype_code(q), sizes[4] ** -0.5 if scale is None else scale, norm_eps, _stream(stream, q))
 
 
 def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -1025,12 +1030,12 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     Returns (out [B, T, H, Dv] in q's dtype, the states after the last token):
     state [B, H, Dk, Dv] itself, updated in place, unless state_out is given.
     scale: 1 / sqrt(Dk) when None."""
-    B, T, H, Dv = v.shape if v.dim() == 4 else (0, 0, 0, 0)
+    sizes = _delta_shapes(q, k, v, g, beta, state, lengths)
     with _on(q, k, v, g, beta, state, lengths):
-        p = _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
+        p = _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
         state_out = state if state_out is None else _new(state_out, state.shape, torch.float32,
                                                          q.device, "state_out")
-        out = _new(out, (B, T, H, Dv), q.dtype, q.device)
+        out = _new(out, v.shape, q.dtype, q.device)
         _check(lib().srnl_gated_delta_step(ctypes.byref(p), _ptr(out), _ptr(state_out)),
                "srnl_gated_delta_step")
     return out, state_out
@@ -1045,12 +1050,13 @@ def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     """srnl_gated_delta_fwd: whole sequences, arguments as gated_delta_step's
     (state None: zeros). Returns (out, the states after the last token); with
     record also the record that gated_delta_bwd takes."""
-    B, T, H, Dv = v.shape if v.dim() == 4 else (0, 0, 0, 0)
     L = lib()
+    sizes = _delta_shapes(q, k, v, g, beta, state, lengths)
+    B, T, Hk, H, Dk, Dv = sizes
     with _on(q, k, v, g, beta, state, lengths):
-        p = _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
-        state_out = _new(state_out, (B, H, q.shape[3], Dv), torch.float32, q.device, "state_out")
-        out = _new(out, (B, T, H, Dv), q.dtype, q.device)
+        p = _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
+        state_out = _new(state_out, (B, H, Dk, Dv), torch.float32, q.device, "state_out")
+        out = _new(out, v.shape, q.dtype, q.device)
         rec = None
         if record:
             rec = torch.empty(L.srnl_gated_delta_record_bytes(ctypes.byref(p)), dtype=torch.uint8,
@@ -1073,12 +1079,14 @@ def gated_delta_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: tor
     Returns (dq, dk, dv in q's dtype, dg, dbeta fp32, the gradient of state, or
     None without one)."""
     L = lib()
+    sizes = _delta_shapes(q, k, v, g, beta, state, lengths)
+    B, T, Hk, H, Dk, Dv = sizes
+    _expect(dout, v.shape, q.dtype, "dout")
+    _expect(dstate, (B, H, Dk, Dv), torch.float32, "dstate")
+    if record.dtype != torch.uint8 or record.dim() != 1:
+        raise ValueError("record must be the one that gated_delta_fwd(record=True) returned")
     with _on(q, k, v, g, beta, state, lengths, dout, record, dstate):
-        p = _delta_params(q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
-        _expect(dout, v.shape, q.dtype, "dout")
-        _expect(dstate, (p.B, p.H, p.Dk, p.Dv), torch.float32, "dstate")
-        if record.dtype != torch.uint8 or record.dim() != 1:
-            raise ValueError("record must be the one that gated_delta_fwd(record=True) returned")
+        p = _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
         dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         dk = torch.empty_like(dq)
         dv = torch.empty(v.shape, dtype=q.dtype, device=q.device)

@@ -59,7 +59,9 @@ def step_tol(T, Dk):
 STEP = [  # B, T, Hk, H, Dk, Dv, norm, lengths
     (1, 1, 1, 1, 8, 8, True, None), (3, 1, 2, 4, 128, 128, True, None), (2, 5, 1, 3, 64, 72, True, (5, 2)),
     (4, 3, 2, 2, 40, 200, False, (0, 1, 3, 9)), (2, 2, 1, 2, 120, 256, True, (-4, 2)), (2, 7, 3, 3, 16, 64, False, None),
-    (1, 4, 1, 1, 104, 8, True, None)]
+    (1, 4, 1, 1, 104, 8, True, None),
+    # enough heads for the wider blocks
+    (64, 2, 2, 4, 128, 72, True, None), (64, 1, 4, 4, 32, 64, False, None), (64, 3, 4, 4, 64, 40, True, None)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -99,7 +101,9 @@ CHUNKED = [  # B, T, Hk, H, Dk, Dv, norm, lengths
     (1, 1, 1, 1, 8, 8, True, None), (2, 2, 1, 2, 32, 32, True, None), (1, 63, 2, 2, 64, 64, False, None),
     (2, 64, 1, 3, 128, 128, True, None), (1, 65, 2, 4, 40, 72, True, None), (2, 200, 2, 2, 24, 200, True, (200, 131)),
     (5, 130, 1, 2, 96, 48, False, (0, 1, 64, 65, 130)), (1, 257, 3, 6, 128, 256, True, None),
-    (3, 90, 1, 1, 16, 8, True, (500, -3, 89)), (2, 129, 2, 2, 56, 40, False, None)]
+    (3, 90, 1, 1, 16, 8, True, (500, -3, 89)), (2, 129, 2, 2, 56, 40, False, None),
+    # enough heads for slabs of 32 columns
+    (64, 70, 2, 4, 32, 32, True, None), (65, 65, 4, 4, 64, 40, False, None), (33, 66, 4, 8, 128, 48, True, None)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])

@@ -115,7 +115,11 @@ def check(B, S, C, G, x_t, y_t, kind, scale=2.0, offset=3.0):
 
 SIZES = [(1, 1, 8, 8), (1, 1, 1, 1), (2, 1, 24, 3), (3, 7, 10, 5), (1, 49, 512, 32), (2, 196, 256, 16), (2, 63, 210, 7),
          (1, 3136, 64, 16), (3, 5, 4096, 4), (2, 9, 2500, 10), (1, 2000, 3, 1), (2, 33, 20, 20), (70, 17, 36, 6),
-         (1, 401, 777, 1), (2, 50, 192, 192)]
+         (1, 401, 777, 1), (2, 50, 192, 192),
+         # long maps of few items, by slabs: every width of piece
+         (1, 9000, 64, 16), (1, 40000, 24, 2), (2, 20011, 20, 4), (1, 30000, 6, 3), (1, 33001, 3, 1), (1, 2000, 4104, 1),
+         # many items, by slices: held and read again
+         (64, 100, 96, 12), (40, 700, 64, 16), (130, 3000, 12, 3)]
 
 
 @pytest.mark.parametrize("B,S,C,G", SIZES)
@@ -194,3 +198,42 @@ def test_autograd_matches_differences_and_repeats():
         assert abs(num - ana) <= 1e-4 * (g.double().norm() * v.norm()).item()
     again = torch.autograd.grad((srnl.group_norm(leaves[0], 3, leaves[1], leaves[2], act="gelu") * w).sum(), leaves)
     assert all(torch.equal(a, b) for a, b in zip(grads, again))
+
+
+def test_other_streams_graphs_and_alignment():
+    x, gain, bias = rnd(1, 3, 200, 64), rnd(2, 64), rnd(3, 64)
+    dout = rnd(4, 3, 200, 64)
+
+    def both(**kw):
+        y, m, r = srnl.group_norm_fwd(x, 8, gain, bias, act="silu", stats=True, **kw)
+        return (y, m, r, *srnl.group_norm_bwd(dout, x, 8, gain, bias, m, r, act="silu", **kw))
+
+    want = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = both(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    long = rnd(5, 1, 9000, 64)
+    for src in (x, long):
+        with torch.cuda.stream(side):
+            srnl.group_norm_fwd(src, 8, gain, bias)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y, m, r = srnl.group_norm_fwd(src, 8, gain, bias, act="gelu", stats=True)
+            g = srnl.group_norm_bwd(y, src, 8, gain, bias, m, r, act="gelu")
+        for seed in range(3):
+            src.copy_(rnd(10 + seed, *src.shape))
+            graph.replay()
+            torch.cuda.synchronize()
+            y2, m2, r2 = srnl.group_norm_fwd(src, 8, gain, bias, act="gelu", stats=True)
+            g2 = srnl.group_norm_bwd(y2, src, 8, gain, bias, m2, r2, act="gelu")
+            assert all(torch.equal(a, b) for a, b in zip((y, *g), (y2, *g2)))
+    flat = rnd(6, 3 * 200 * 64 + 1)[1:].view(3, 200, 64)
+    with pytest.raises(srnl.SrnlError, match="aligned"):
+        srnl.group_norm_fwd(flat, 8, gain, bias)
+    with pytest.raises(ValueError, match="contiguous"):
+        srnl.group_norm_fwd(x.transpose(1, 2), 8, None, None)
+    y = srnl.group_norm(flat.clone().requires_grad_(), 8, gain, bias)
+    y.backward(flat)                       # an incoming gradient may start anywhere
