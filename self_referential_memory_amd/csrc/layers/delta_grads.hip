@@ -39,8 +39,16 @@ template <bool BF, int KD> struct GradShared {
             Split<BF, 2, 64, 64> A, At, Z;
         } out;
     };
-    float gam[64], end[64], beta[64], rk[64], rq[64], ghi[64], glo[64];
-    float colF[4][64], rowF[2][64], diag[64], dot[2][8][64], sd[8];
+    // a chunk's row factors, as they lie in memory from VEC_BETA on
+    __attribute__((aligned(16))) float vec[VEC_FLOATS - VEC_BETA];
+    __attribute__((aligned(16))) float norm[2][64];
+    float colF[4][64], diag[64], sd[8];
+    __attribute__((aligned(16))) float rowF[2][64], dot[2][8][64];
+    __device__ __forceinline__ float at(int which, int r) const { return vec[which - VEC_BETA + r]; }
+    __device__ __forceinline__ v4f four(int which, int r) const
+    {
+        return *reinterpret_cast<const v4f *>(&vec[which - VEC_BETA + r]);
+    }
 };
 
 template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a)
@@ -129,16 +137,9 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                 sh.q.put(r, k, fq);
             }
         }
-        const float *vec = a.vec + at * VEC_FLOATS;
-        if (wave == 0) {
-            sh.gam[lane] = vec[VEC_GAM + lane];
-            sh.end[lane] = vec[VEC_END + lane];
-            sh.beta[lane] = vec[VEC_BETA + lane];
-            sh.rk[lane] = vec[VEC_RK + lane];
-            sh.rq[lane] = vec[VEC_RQ + lane];
-            sh.ghi[lane] = vec[VEC_GHI + lane];
-            sh.glo[lane] = vec[VEC_GLO + lane];
-        }
+        if (threadIdx.x < (VEC_FLOATS - VEC_BETA) / 4)
+            *reinterpret_cast<v4f *>(&sh.vec[4 * threadIdx.x]) =
+                *reinterpret_cast<const v4f *>(a.vec + at * VEC_FLOATS + VEC_BETA + 4 * threadIdx.x);
     }
     spread(0);
 
@@ -187,7 +188,9 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
     lds_barrier();                     // dO, E and dV are read
 
     // ---- 64 x 64 parts: this wave's rows i against its columns j
-    float rowF[4] = {0, 0, 0, 0};
+    v4f rowF = v4f_zero();
+    const v4f ihi = sh.four(VEC_GHI, rows), ilo = sh.four(VEC_GLO, rows);
+    const v4f ri = sh.four(VEC_RK, rows), qi = sh.four(VEC_RQ, rows);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const int j = 2 * half + p, col = 16 * j + l15;
@@ -202,26 +205,28 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                 kk = mma(sh.k.across(row, k), o, kk);
                 qk = mma(sh.q.across(row, k), o, qk);
             }
-            const float bj = sh.beta[col], rj = sh.rk[col];
+            const float bj = sh.at(VEC_BETA, col), rj = sh.at(VEC_RK, col);
+            const float jhi = sh.at(VEC_GHI, col), jlo = sh.at(VEC_GLO, col);
+            v4f F;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int i = rows + e;
-                const float d = decay(sh.ghi[i], sh.glo[i], sh.ghi[col], sh.glo[col]);
-                const float ri = sh.rk[i], qi = sh.rq[i];
-                const bool on = col <= i, below = col < i;
+                const bool on = j < band || col <= rows + e, below = j < band || col < rows + e;
+                const float d = decay(ihi[e], ilo[e], jhi, jlo);
                 const float x = on ? a.scale * d * A[p][e] : 0.0f;          // dP before beta
                 const float y = below ? d * Y[p][e] : 0.0f;
-                const float F = on ? x * qi * rj * qk[e] - (below ? y * ri * rj * kk[e] : 0.0f) : 0.0f;
-                wa[e] = x * bj * rj;
-                wat[e] = x * bj * qi;
-                zl[e] = -y * bj * rj;
-                zu[e] = -y * bj * ri;
-                colF += F;
+                const float xf = x * qi[e] * rj * qk[e], yf = y * ri[e] * rj * kk[e];
+                F[e] = (on ? xf : 0.0f) - (below ? yf : 0.0f);
+                const float xb = x * bj, yb = -y * bj;
+                wa[e] = xb * rj;
+                wat[e] = xb * qi[e];
+                zl[e] = yb * rj;
+                zu[e] = yb * ri[e];
                 // the diagonal is no decay's
-                rowF[e] += below ? bj * F : 0.0f;
-                if (on && !below)
-                    sh.diag[i] = F;
+                rowF[e] += below ? bj * F[e] : 0.0f;
             }
+            colF = (F[0] + F[1]) + (F[2] + F[3]);
+            if (j == band && quad == l15 >> 2)
+                sh.diag[col] = (l15 & 2) ? ((l15 & 1) ? F[3] : F[2]) : ((l15 & 1) ? F[1] : F[0]);
             // Z's two triangles: rows i > j from here, its mirror from the same values
             if (j < band) {
                 sh.out.Z.put_rows(rows, col, zl);
@@ -248,31 +253,25 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
         if (quad == 0)
             sh.colF[band][col] = colF;
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float s = sum16(rowF[e]);
-        if (l15 == 0)
-            sh.rowF[half][rows + e] = s;
-    }
+    rowF = sum16(rowF);
+    if (l15 == 0)
+        *reinterpret_cast<v4f *>(&sh.rowF[half][rows]) = rowF;
     // ---- the states' terms, while the matrices come together
     v4f dq[RT], dk[RT];
 #pragma unroll
-    for (int ri = 0; ri < RT; ++ri)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * (rt0 + ri) + 4 * quad + e;
-            const float x = a.scale * sh.gam[i] * oS[ri][e];
-            const float y = -sh.gam[i] * vS[ri][e];
-            const float w = sh.end[i] * eD[ri][e];
-            const float kh = sh.rk[i] * sh.k.at(i, mycol), qh = sh.rq[i] * sh.q.at(i, mycol);
-            const float s = sum16(fmaf(qh, x, kh * y)), t = sum16(kh * w);
-            if (l15 == 0) {
-                sh.dot[0][wave % CW][i] = s;
-                sh.dot[1][wave % CW][i] = t;
-            }
-            dq[ri][e] = x;
-            dk[ri][e] = fmaf(sh.beta[i], w, y);
+    for (int t = 0; t < RT; ++t) {
+        const int r0 = 16 * (rt0 + t), r = r0 + 4 * quad;
+        const v4f gam = sh.four(VEC_GAM, r);
+        const v4f x = a.scale * gam * oS[t], y = -gam * vS[t], w = sh.four(VEC_END, r) * eD[t];
+        const v4f kh = sh.four(VEC_RK, r) * sh.k.tile(r0, col0), qh = sh.four(VEC_RQ, r) * sh.q.tile(r0, col0);
+        const v4f s = sum16(qh * x + kh * y), v = sum16(kh * w);
+        if (l15 == 0) {
+            *reinterpret_cast<v4f *>(&sh.dot[0][wave % CW][r]) = s;
+            *reinterpret_cast<v4f *>(&sh.dot[1][wave % CW][r]) = v;
         }
+        dq[t] = x;
+        dk[t] = sh.four(VEC_BETA, r) * w + y;
+    }
 #pragma unroll
     for (int off = 32; off > 0; off >>= 1)
         sd += __shfl_xor(sd, off);
@@ -305,7 +304,7 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
 #pragma unroll
         for (int x = 0; x < 8; ++x)
             inner += sh.sd[x];
-        const float beta = sh.beta[lane];
+        const float beta = sh.at(VEC_BETA, lane);
         const float dbeta = w + col;
         w *= beta;
         // tokens after this one and itself; tokens before this one
@@ -316,7 +315,7 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
             after += lane + off < 64 ? x : 0.0f;
             before += lane >= off ? y : 0.0f;
         }
-        const float dg = after + (before - w) + sh.gam[63] * inner;
+        const float dg = after + (before - w) + sh.at(VEC_GAM, 63) * inner;
         if (lane < inside) {
             const long long o = ogb + static_cast<long long>(lane) * a.H;
             if (a.dg)
@@ -330,33 +329,31 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
     if (a.eps > 0.0f) {
         lds_barrier();                 // the sums for dg are read
 #pragma unroll
-        for (int ri = 0; ri < RT; ++ri)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * (rt0 + ri) + 4 * quad + e;
-                const float x = sum16(sh.q.at(i, mycol) * dq[ri][e]);
-                const float y = sum16(sh.k.at(i, mycol) * dk[ri][e]);
-                if (l15 == 0) {
-                    sh.dot[0][wave % CW][i] = x;
-                    sh.dot[1][wave % CW][i] = y;
-                }
+        for (int t = 0; t < RT; ++t) {
+            const int r0 = 16 * (rt0 + t), r = r0 + 4 * quad;
+            const v4f x = sum16(sh.q.tile(r0, col0) * dq[t]), y = sum16(sh.k.tile(r0, col0) * dk[t]);
+            if (l15 == 0) {
+                *reinterpret_cast<v4f *>(&sh.dot[0][wave % CW][r]) = x;
+                *reinterpret_cast<v4f *>(&sh.dot[1][wave % CW][r]) = y;
             }
+        }
+        lds_barrier();
+        if (threadIdx.x < 128) {
+            const int which = threadIdx.x >> 6;
+            float s = 0.0f;
+#pragma unroll
+            for (int w = 0; w < CW; ++w)
+                s += sh.dot[which][w][lane];
+            const float r = sh.at(which ? VEC_RK : VEC_RQ, lane);
+            sh.norm[which][lane] = r * r * s;          // r q^.dq^, likewise k
+        }
         lds_barrier();
 #pragma unroll
-        for (int ri = 0; ri < RT; ++ri)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = 16 * (rt0 + ri) + 4 * quad + e;
-                const float rq = sh.rq[i], rk = sh.rk[i];
-                float xs = 0.0f, ys = 0.0f;
-#pragma unroll
-                for (int w = 0; w < CW; ++w) {
-                    xs += sh.dot[0][w][i];
-                    ys += sh.dot[1][w][i];
-                }
-                dq[ri][e] = rq * (dq[ri][e] - rq * sh.q.at(i, mycol) * (rq * xs));
-                dk[ri][e] = rk * (dk[ri][e] - rk * sh.k.at(i, mycol) * (rk * ys));
-            }
+        for (int t = 0; t < RT; ++t) {
+            const int r0 = 16 * (rt0 + t), r = r0 + 4 * quad;
+            dq[t] = sh.four(VEC_RQ, r) * (dq[t] - sh.q.tile(r0, col0) * *reinterpret_cast<const v4f *>(&sh.norm[0][r]));
+            dk[t] = sh.four(VEC_RK, r) * (dk[t] - sh.k.tile(r0, col0) * *reinterpret_cast<const v4f *>(&sh.norm[1][r]));
+        }
     }
     const Buf oq(parts ? a.dq_part : a.dq, oqk * (parts || !BF ? 4 : 2));
     const Buf ok(parts ? a.dk_part : a.dk, oqk * (parts || !BF ? 4 : 2));

@@ -147,6 +147,13 @@ __device__ __forceinline__ float sum16(float v)
     v += turned<0x121>(v);
     return v;
 }
+__device__ __forceinline__ v4f sum16(v4f v)
+{
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        v[e] = sum16(v[e]);
+    return v;
+}
 
 __device__ __forceinline__ v4f v4f_zero() { return v4f{0.0f, 0.0f, 0.0f, 0.0f}; }
 
@@ -398,12 +405,23 @@ template <bool BF, int KD> struct Rows {
         __builtin_memcpy(&f, __builtin_assume_aligned(&e[r][k], 16), sizeof f);
         return f;
     }
-    __device__ __forceinline__ float at(int r, int k) const
+    // as a result tile lies: rows row0 + 4 quad .. + 3 of column col0 + (lane & 15)
+    __device__ __forceinline__ v4f tile(int row0, int col0) const
     {
-        if constexpr (BF)
-            return bf16_one(e[r][k]);
-        else
-            return e[r][k];
+        const int l = threadIdx.x & 63, quad = l >> 4, l15 = l & 15;
+        v4f v;
+        if constexpr (BF) {
+            const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) s16x4 *)(const_cast<uint16_t *>(
+                    &e[row0 + 4 * quad + (l15 >> 2)][col0 + 4 * (l15 & 3)])));
+            const u32x2 w = __builtin_bit_cast(u32x2, t);
+            v = v4f{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = e[row0 + 4 * quad + i][col0 + l15];
+        }
+        return v;
     }
     // operand: columns col0 .. + 15, reduction over tokens tok0 .. + 31
     __device__ __forceinline__ In<BF> down(int tok0, int col0) const
