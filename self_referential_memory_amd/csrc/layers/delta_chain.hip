@@ -257,14 +257,36 @@ __device__ __forceinline__ void store_state(const DeltaArgs &a, const Place<NV> 
             put_value<false>(b, (sl.row(i) + e) * a.Dv + sl.col(i), live, S[i][e]);
     }
 }
+// The state's slab from its words in LDS, which hold all its 24 bits, by the helpers.
+template <bool BF, int KD, int NV>
+__device__ __forceinline__ void store_words(const DeltaArgs &a, const Place<NV> &pl, const Split<BF, 3, NV, KD> &s, float *p,
+                                            long long at)
+{
+    constexpr int KF = KD / 32, ALL = KF * (NV / 16);
+    const Buf b(p, (at * a.Dk * a.Dv + pl.v0) * 4);
+#pragma unroll
+    for (int i = 0; i < (ALL + 3) / 4; ++i) {
+        const int u = pl.wave + 4 * i;
+        if (ALL % 4 && u >= ALL)
+            break;
+        const int row = 32 * (u % KF) + 8 * pl.quad, col = 16 * (u / KF) + pl.l15;
+        float v[8];
+        join_words(s.get(col, row / 8), v);
+        const bool live = both(row < a.Dk, pl.v0 + col < a.Dv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            put_value<false>(b, (row + e) * a.Dv + col, live, v[e]);
+    }
+}
 
 // ------------------------------------------------------------------- forward
 
-template <bool BF, int KD, int NV> struct FwdShared {
+template <bool BF, int KD, int NV, bool RECORD> struct FwdShared {
     __attribute__((aligned(16))) Rows<BF, KD> k;
     Split<BF, 3, NV, KD> S;                            // the state, transposed
     Split<BF, 3, NV, 64> R, W;
     Split<BF, 2, NV, 64> U;
+    v4f e[RECORD ? 4 : 1][NV / 16][64];                // E as result tiles, for the helpers to record
     Factors w[2];
 };
 
@@ -302,8 +324,9 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
 {
     constexpr int KF = KD / 32, NT = NV / 16;
     using Sl = Slab<KD, NV>;
-    __shared__ FwdShared<BF, KD, NV> sh;
+    __shared__ FwdShared<BF, KD, NV, RECORD> sh;
     const Place<NV> pl(a);
+    const int lane = threadIdx.x & 63;
     if (!pl.helper) {
         const Sl sl{pl.wave, pl.quad, pl.l15};
         v4f S[Sl::MINE];
@@ -347,8 +370,6 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
                     for (int j = 0; j < NT; ++j)
                         err[j].add(in.x[f], rs[f][j]);
             next.load_x(a, pl, after);
-            if (RECORD)
-                store_state<KD, NV>(a, pl, sl, a.S0, pl.at(a, c), S);
             In<BF> kd[2][Sl::MINE];
             sl.template down<BF>(sh.k, kd);
 #pragma unroll
@@ -357,7 +378,7 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
                 sh.W.put4(16 * j + pl.l15, pl.rows, write * e);
                 sh.U.put4(16 * j + pl.l15, pl.rows, beta * e);
                 if (RECORD)
-                    store_rows(a, pl, a.E, c, j, e);
+                    sh.e[pl.wave][j][lane] = e;
             }
             lds_barrier();
             const float last = w.last;
@@ -402,6 +423,8 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             const v4f read = sh.w[c & 1].rows(VEC_READQ, pl.rows);
             lds_barrier();
             next.load(a, pl, c + 1);
+            if (RECORD)
+                store_words<BF, KD, NV>(a, pl, sh.S, a.S0, pl.at(a, c));
             lds_barrier();
             in.vec.store(sh.w[(c + 1) & 1], pl.wave);
             Mid<BF, 2> us[2][NT];
@@ -414,6 +437,8 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
                     if (half_live<false>(pl.wave, f))
                         pU.add(in.p[f], us[f][j]);
                 store_values<BF>(a, pl, a.out, c, j, read * qS[j].value() + pU.value());
+                if (RECORD)
+                    store_rows(a, pl, a.E, c, j, sh.e[pl.wave][j][lane]);
             }
             lds_barrier();
         };
@@ -444,6 +469,7 @@ template <bool BF, int KD, int NV> struct BwdShared {
     Split<BF, 1, NV, 64> O;                            // dO, transposed
     // what the helpers hand to the chain, as result tiles: P^T dO and Q^T dO
     v4f po[4][NV / 16][64], qo[4][Sl::MINE][64];
+    v4f dv[4][NV / 16][64];                            // and the chain to them: dV
     Factors w[2];
 };
 
@@ -514,16 +540,13 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
                     for (int j = 0; j < NT; ++j)
                         dv[j].add(in.x[f], ws[f][j]);
             next.load_x(a, pl, after);
-            store_state<KD, NV>(a, pl, sl, a.D1, pl.at(a, c), D);
             In<BF> kd[2][Sl::MINE];
             sl.template down<BF>(sh.k, kd);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const v4f d = dv[j].value();
                 sh.V.put4(16 * j + pl.l15, pl.rows, -read * d);
-                store_rows(a, pl, a.dV, c, j, d);
-                if (a.dv)
-                    store_values<BF>(a, pl, a.dv, c, j, d);
+                sh.dv[pl.wave][j][lane] = d;
             }
             lds_barrier();
             const float last = w.last;
@@ -613,12 +636,20 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
                 sh.qo[pl.wave][i][lane] = qo[i];
             if (c > 0)
                 spread(in, c - 1);
+            store_words<BF, KD, NV>(a, pl, sh.D, a.D1, pl.at(a, c));
             lds_barrier();
             if (c > 0) {
                 parts(in);
                 in.load(a, pl, c > 1 ? c - 2 : 0);
             }
             lds_barrier();
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const v4f d = sh.dv[pl.wave][j][lane];
+                store_rows(a, pl, a.dV, c, j, d);
+                if (a.dv)
+                    store_values<BF>(a, pl, a.dv, c, j, d);
+            }
             lds_barrier();
         }
     }

@@ -279,6 +279,18 @@ template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_split(cons
     }
     return f;
 }
+// and back: three words hold all bits of a normal fp32 value
+__device__ __forceinline__ void join_words(const Mid<true, 3> &f, float (&v)[8])
+{
+    u32x4 t[3];
+    __builtin_memcpy(t, &f, sizeof f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = (bf16_lo(t[2][j]) + bf16_lo(t[1][j])) + bf16_lo(t[0][j]);
+        v[2 * j + 1] = (bf16_hi(t[2][j]) + bf16_hi(t[1][j])) + bf16_hi(t[0][j]);
+    }
+}
+__device__ __forceinline__ void join_words(const Mid<false, 3> &f, float (&v)[8]) { __builtin_memcpy(v, &f, sizeof f); }
 template <bool BF, int PL> __device__ __forceinline__ void frag_store(char *p, int frag, const float (&v)[8])
 {
     const Mid<BF, PL> f = mid_split<BF, PL>(v);
