@@ -7,10 +7,10 @@
 // Four of the block's waves do only those, each 16 of the chunk's rows (or its
 // share of the state's); four more do what the chain need not wait for, in the
 // slots it leaves: forward the outputs, backward the parts P^T dO and Q^T dO of the
-// chunk before. States, errors and their scaled copies pass from wave to wave
-// through LDS, transposed; operands that are rows of q, k, X and P come straight
-// from memory in the layout the matrix units want, a chunk ahead. Three barriers a
-// chunk.
+// chunk before, and what is recorded. States, errors and their scaled copies pass
+// from wave to wave through LDS, transposed; operands that are rows of q, k, X and P
+// come straight from memory in the layout the matrix units want, a chunk ahead. Three
+// barriers a chunk.
 #include "delta_mma.h"
 
 namespace {
@@ -52,7 +52,9 @@ __device__ __forceinline__ void read_columns(const Split<BF, PL, ROWS, K> &p, in
             f[i][j] = p.get(col0 + 16 * j + l15, 4 * i + quad);
 }
 // (A chunk's loads are issued without a condition, the last chunk's again at the end:
-// behind a branch that may have issued loads, a wait for earlier ones waits for all.)
+// behind a branch that may have issued loads, a wait for earlier ones waits for all.
+// They go between the operands' reads and the products, in the time that the reads
+// take: behind the products they cost a chunk 8 % more.)
 __device__ __forceinline__ void hold() { __builtin_amdgcn_sched_barrier(0); }
 
 // What every wave of a block knows.
@@ -160,7 +162,8 @@ __device__ __forceinline__ v4f values(const Column<true> &c)
     return v;
 }
 __device__ __forceinline__ v4f values(const Column<false> &c) { return v4f{c.v[0], c.v[1], c.v[2], c.v[3]}; }
-// ... and its outputs; tokens past the item's length get zeros
+// ... and its outputs; tokens past the item's length get zeros. bf16 ones pass the
+// caches, as what is recorded does (16384 tokens x 16 heads of 128: 423 -> 411 us).
 template <bool BF, class P>
 __device__ __forceinline__ void store_values(const DeltaArgs &a, const P &pl, void *p, int c, int j, v4f v)
 {
@@ -178,7 +181,7 @@ __device__ __forceinline__ void store_values(const DeltaArgs &a, const P &pl, vo
             const uint32_t w = odd ? pack_bf16(got, mine) : pack_bf16(mine, got);
             const bool live = both(r < inside, pl.v0 + col < a.Dv);
             __builtin_amdgcn_raw_buffer_store_b32(r < left ? w : 0u, b.r,
-                                                  live ? 2u * (r * a.H * a.Dv + col - odd) : NOWHERE, 0, 0);
+                                                  live ? 2u * (r * a.H * a.Dv + col - odd) : NOWHERE, 0, NT_STORE);
         }
     } else {
 #pragma unroll
@@ -186,14 +189,6 @@ __device__ __forceinline__ void store_values(const DeltaArgs &a, const P &pl, vo
             put_value<false>(b, (pl.rows + e) * a.H * a.Dv + col, both(pl.rows + e < inside, pl.v0 + col < a.Dv),
                              pl.rows + e < left ? v[e] : 0.0f);
     }
-}
-// this wave's rows of a [64][Dv] fp32 array
-template <class P> __device__ __forceinline__ void store_rows(const DeltaArgs &a, const P &pl, float *p, int c, int j, v4f v)
-{
-    const Buf b(p, (pl.at(a, c) * DELTA_CHUNK * a.Dv + pl.v0) * 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        put_value<false>(b, (pl.rows + e) * a.Dv + 16 * j + pl.l15, pl.v0 + 16 * j + pl.l15 < a.Dv, v[e]);
 }
 template <bool BF, int NV> __device__ __forceinline__ void zero_values(const DeltaArgs &a, const Place<NV> &pl, void *p)
 {
@@ -257,26 +252,37 @@ __device__ __forceinline__ void store_state(const DeltaArgs &a, const Place<NV> 
             put_value<false>(b, (sl.row(i) + e) * a.Dv + sl.col(i), live, S[i][e]);
     }
 }
-// The state's slab from its words in LDS, which hold all its 24 bits, by the helpers.
+// What is recorded, by the helpers, 16 bytes a lane, in panels of 8 columns (record_at),
+// so that a wave writes 512 bytes side by side. The state's slab comes from its words
+// in LDS, which hold all its 24 bits: a lane has 8 columns of a row.
 template <bool BF, int KD, int NV>
 __device__ __forceinline__ void store_words(const DeltaArgs &a, const Place<NV> &pl, const Split<BF, 3, NV, KD> &s, float *p,
                                             long long at)
 {
-    constexpr int KF = KD / 32, ALL = KF * (NV / 16);
-    const Buf b(p, (at * a.Dk * a.Dv + pl.v0) * 4);
+    constexpr int PER = 512 / NV, ALL = KD / PER;      // rows a wave has at once; times
+    const Buf b(p, at * a.Dk * a.Dv * 4);
+    const int g = pl.quad % (NV / 8), tile = 16 * (pl.quad / (NV / 8));
 #pragma unroll
     for (int i = 0; i < (ALL + 3) / 4; ++i) {
         const int u = pl.wave + 4 * i;
         if (ALL % 4 && u >= ALL)
             break;
-        const int row = 32 * (u % KF) + 8 * pl.quad, col = 16 * (u / KF) + pl.l15;
         float v[8];
-        join_words(s.get(col, row / 8), v);
-        const bool live = both(row < a.Dk, pl.v0 + col < a.Dv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            put_value<false>(b, (row + e) * a.Dv + col, live, v[e]);
+        s.down(8 * g, PER * u + tile, v);
+        const int row = PER * u + tile + pl.l15;
+        put8(b, record_at(row, pl.v0 + 8 * g, a.Dk), both(row < a.Dk, pl.v0 + 8 * g < a.Dv), v);
     }
+}
+// this wave's 16 rows of a [64][Dv] fp32 array, from its result tile in LDS
+template <class P> __device__ __forceinline__ void store_rows(const DeltaArgs &a, const P &pl, float *p, int c, int j, const v4f (&t)[64])
+{
+    const Buf b(p, pl.at(a, c) * DELTA_CHUNK * a.Dv * 4);
+    const int lane = threadIdx.x & 63, r = lane >> 2, col = 16 * j + 4 * (lane & 3);
+    v4f v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = reinterpret_cast<const float *>(&t[16 * (r >> 2) + (col & 15) + i])[r & 3];
+    put4(b, record_at(16 * pl.wave + r, pl.v0 + col, DELTA_CHUNK), pl.v0 + col < a.Dv, v);
 }
 
 // ------------------------------------------------------------------- forward
@@ -339,6 +345,8 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
         const auto chunk = [&](const ChainIn<BF, KF, NT, false> &in, ChainIn<BF, KF, NT, false> &next, int c) __attribute__((always_inline)) {
             Mid<BF, 3> op[KF][NT];
             read_columns(sh.S, 0, pl.quad, pl.l15, op);
+            const int after = c + 1 < pl.chunks ? c + 1 : c;
+            next.load(a, pl, after);
             hold();
             Sum<BF, 3> kS[NT];
 #pragma unroll
@@ -346,8 +354,6 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     kS[j].add(in.k[f], op[f][j]);
-            const int after = c + 1 < pl.chunks ? c + 1 : c;
-            next.load(a, pl, after);
             const Factors &w = sh.w[c & 1];
             const v4f read = w.rows(VEC_READK, pl.rows);
 #pragma unroll
@@ -361,6 +367,7 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             const v4f write = w.rows(VEC_WRITE, pl.rows), beta = w.rows(VEC_BETA, pl.rows);
             Mid<BF, 3> rs[2][NT];
             read_columns(sh.R, 0, pl.quad, pl.l15, rs);
+            next.load_x(a, pl, after);
             hold();
             Sum<BF, 3> err[NT];
 #pragma unroll
@@ -369,7 +376,6 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
                         err[j].add(in.x[f], rs[f][j]);
-            next.load_x(a, pl, after);
             In<BF> kd[2][Sl::MINE];
             sl.template down<BF>(sh.k, kd);
 #pragma unroll
@@ -438,7 +444,7 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
                         pU.add(in.p[f], us[f][j]);
                 store_values<BF>(a, pl, a.out, c, j, read * qS[j].value() + pU.value());
                 if (RECORD)
-                    store_rows(a, pl, a.E, c, j, sh.e[pl.wave][j][lane]);
+                    store_rows(a, pl, a.E, c, j, sh.e[pl.wave][j]);
             }
             lds_barrier();
         };
@@ -509,6 +515,8 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
         const auto chunk = [&](const ChainIn<BF, KF, NT, true> &in, ChainIn<BF, KF, NT, true> &next, int c) __attribute__((always_inline)) {
             Mid<BF, 3> op[KF][NT];
             read_columns(sh.D, 0, pl.quad, pl.l15, op);
+            const int after = c > 0 ? c - 1 : 0;
+            next.load(a, pl, after);
             hold();
             Sum<BF, 3> kD[NT];
 #pragma unroll
@@ -516,8 +524,6 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     kD[j].add(in.k[f], op[f][j]);
-            const int after = c > 0 ? c - 1 : 0;
-            next.load(a, pl, after);
             const Factors &w = sh.w[c & 1];
             const v4f write = w.rows(VEC_WRITE, pl.rows), beta = w.rows(VEC_BETA, pl.rows);
 #pragma unroll
@@ -531,6 +537,7 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             const v4f read = w.rows(VEC_READK, pl.rows);
             Mid<BF, 3> ws[2][NT];
             read_columns(sh.W, 0, pl.quad, pl.l15, ws);
+            next.load_x(a, pl, after);
             hold();
             Sum<BF, 3> dv[NT];
 #pragma unroll
@@ -539,7 +546,6 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
                         dv[j].add(in.x[f], ws[f][j]);
-            next.load_x(a, pl, after);
             In<BF> kd[2][Sl::MINE];
             sl.template down<BF>(sh.k, kd);
 #pragma unroll
@@ -645,10 +651,9 @@ template <bool BF, int KD, int NV> __global__ __launch_bounds__(512) void delta_
             lds_barrier();
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const v4f d = sh.dv[pl.wave][j][lane];
-                store_rows(a, pl, a.dV, c, j, d);
+                store_rows(a, pl, a.dV, c, j, sh.dv[pl.wave][j]);
                 if (a.dv)
-                    store_values<BF>(a, pl, a.dv, c, j, d);
+                    store_values<BF>(a, pl, a.dv, c, j, sh.dv[pl.wave][j][lane]);
             }
             lds_barrier();
         }

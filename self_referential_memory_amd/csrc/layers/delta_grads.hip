@@ -108,10 +108,10 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
     } next;
     const auto fetch = [&](int v) __attribute__((always_inline)) {
         const bool mine = v + 8 * pg < a.Dv, states = both(mycol < a.Dk, v + 8 * quad < a.Dv);
-        load8(bEV, pr * a.Dv + 8 * pg + v, mine, next.ev);
+        load8(bEV, record_at(pr, 8 * pg + v, DELTA_CHUNK), mine, next.ev);
         next.o = in_load<BF>(bO, pr * a.H * a.Dv + 8 * pg + v, both(both(ofE, mine), pr < left));
-        load8(bS, mycol * a.Dv + 8 * quad + v, states, next.s);
-        load8(bD, mycol * a.Dv + 8 * quad + v, states, next.d);
+        load8(bS, record_at(mycol, 8 * quad + v, a.Dk), states, next.s);
+        load8(bD, record_at(mycol, 8 * quad + v, a.Dk), states, next.d);
     };
     const auto spread = [&](int buf) __attribute__((always_inline)) {
         if (ofE) {

@@ -202,6 +202,23 @@ template <bool BF> __device__ __forceinline__ void put_value(const Buf &b, int o
     else
         __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), b.r, live ? 4u * o : NOWHERE, 0, 0);
 }
+// The states and errors that forward records, and their gradients, lie in panels of 8
+// columns: element of a row and column, of rows rows.
+__device__ __forceinline__ int record_at(int row, int col, int rows) { return ((col >> 3) * rows + row) * 8 + (col & 7); }
+// They are stored past the caches (the nt bit): written as others are, they put q, k, X
+// and P, which a head's blocks share, out of the L2, and the chain takes 168 us forward
+// and 196 back at 4 x 4096 x 8 heads of 128, not 149 and 174.
+constexpr int NT_STORE = 2;
+// four or eight fp32 values from o on, a multiple of 4
+__device__ __forceinline__ void put4(const Buf &b, int o, bool live, v4f v)
+{
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), b.r, live ? 4u * o : NOWHERE, 0, NT_STORE);
+}
+__device__ __forceinline__ void put8(const Buf &b, int o, bool live, const float (&v)[8])
+{
+    put4(b, o, live, v4f{v[0], v[1], v[2], v[3]});
+    put4(b, o + 4, live, v4f{v[4], v[5], v[6], v[7]});
+}
 // a value by its address, for what no loop waits for
 template <bool BF> __device__ __forceinline__ void put_at(void *p, long long o, float v)
 {
@@ -279,18 +296,6 @@ template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_split(cons
     }
     return f;
 }
-// and back: three words hold all bits of a normal fp32 value
-__device__ __forceinline__ void join_words(const Mid<true, 3> &f, float (&v)[8])
-{
-    u32x4 t[3];
-    __builtin_memcpy(t, &f, sizeof f);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        v[2 * j] = (bf16_lo(t[2][j]) + bf16_lo(t[1][j])) + bf16_lo(t[0][j]);
-        v[2 * j + 1] = (bf16_hi(t[2][j]) + bf16_hi(t[1][j])) + bf16_hi(t[0][j]);
-    }
-}
-__device__ __forceinline__ void join_words(const Mid<false, 3> &f, float (&v)[8]) { __builtin_memcpy(v, &f, sizeof f); }
 template <bool BF, int PL> __device__ __forceinline__ void frag_store(char *p, int frag, const float (&v)[8])
 {
     const Mid<BF, PL> f = mid_split<BF, PL>(v);
@@ -323,6 +328,38 @@ template <bool BF, int PL, int ROWS, int K> struct Split {
         }
         __builtin_memcpy(&f, t, sizeof f);
         return f;
+    }
+    // 8 rows from r0 on of element k0 + (lane & 15), as fp32: three words hold all bits
+    // of a normal fp32 value. Lanes of a quad have r0 and k0 in common.
+    __device__ __forceinline__ void down(int r0, int k0, float (&v)[8]) const
+    {
+        const int l15 = threadIdx.x & 15;
+        if constexpr (BF) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                u32x2 w[PL];
+#pragma unroll
+                for (int p = 0; p < PL; ++p)
+                    w[p] = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                        (__attribute__((address_space(3))) s16x4 *)(const_cast<char *>(
+                            &b[p][r0 + 4 * h + (l15 >> 2)][2 * (k0 + 4 * (l15 & 3))]))));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float lo = bf16_lo(w[PL - 1][j]), hi = bf16_hi(w[PL - 1][j]);
+#pragma unroll
+                    for (int p = PL - 2; p >= 0; --p) {
+                        lo += bf16_lo(w[p][j]);
+                        hi += bf16_hi(w[p][j]);
+                    }
+                    v[4 * h + 2 * j] = lo;
+                    v[4 * h + 2 * j + 1] = hi;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = *reinterpret_cast<const float *>(&b[0][r0 + j][4 * (k0 + l15)]);
+        }
     }
     // one-word values: inputs
     __device__ __forceinline__ In<BF> get_in(int r, int g) const
