@@ -775,7 +775,9 @@ int held(long long S, int w, int v, bool backward = false)
 }
 // The slice: whole groups and pieces, wider while that leaves a block for every CU and
 // the cells in registers. None (slabs instead) where it is wider than a block's
-// threads, or where the slices are too few to fill the card and long. The same for
+// threads, or where the slices are too few to fill the card and long: forward and
+// back, 32 slices of 2048 cells of 8 take 26 us (slabs 36), 16 of 3136 32 us (45), but
+// 32 of 4096 in fp32 68 us (38) and 35 of 1551 cells of 30 102 us (40). The same for
 // every type: pieces of 4 at most are counted.
 void cut_slices(GnArgs &a)
 {
@@ -789,7 +791,7 @@ void cut_slices(GnArgs &a)
     while (a.C % (2 * w) == 0 && static_cast<long long>(a.B) * (a.C / (2 * w)) >= 256 && 2 * w <= 64 &&
            held(a.S, 2 * w, v4) == held(a.S, w, v4))
         w *= 2;
-    if (static_cast<long long>(a.B) * (a.C / w) < 128 && a.S > 32LL * (SLICE_THREADS / (w / v4)))
+    if (static_cast<long long>(a.B) * (a.C / w) < 128 && a.S > 14LL * (SLICE_THREADS / (w / v4)))
         return;
     a.slice = w;
 }
@@ -834,12 +836,12 @@ size_t group_floats(const GnArgs &a) { return 2 * static_cast<size_t>(a.B) * a.G
         else                                                                                           \
             hipLaunchKernelGGL((kernel<V, 0>), grid, dim3(SLICE_THREADS), 0, st, a);                   \
     } while (0)
-#define SRNL_GN_SLICE(kernel, MORE, a, st)                          \
-    switch (slice_piece(a)) {                                       \
-    case 8: SRNL_GN_SLICE_NV(kernel, 8, MORE, a, st); break;             \
-    case 4: SRNL_GN_SLICE_NV(kernel, 4, MORE, a, st); break;             \
-    case 2: SRNL_GN_SLICE_NV(kernel, 2, MORE, a, st); break;             \
-    default: SRNL_GN_SLICE_NV(kernel, 1, MORE, a, st); break;            \
+#define SRNL_GN_SLICE(kernel, MORE, a, st)                    \
+    switch (slice_piece(a)) {                                 \
+    case 8: SRNL_GN_SLICE_NV(kernel, 8, MORE, a, st); break;  \
+    case 4: SRNL_GN_SLICE_NV(kernel, 4, MORE, a, st); break;  \
+    case 2: SRNL_GN_SLICE_NV(kernel, 2, MORE, a, st); break;  \
+    default: SRNL_GN_SLICE_NV(kernel, 1, MORE, a, st); break; \
     }
 
 dim3 join_grid(const GnArgs &a)
