@@ -175,12 +175,20 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                 Y[x] = mma(y, e, Y[x]);
             }
         }
+        // a tile's operands are read while the one before is multiplied (205 us without, 200)
+        In<BF> ro[2];
+        Mid<BF, 3> rv[2], re[2];
+        ro[0] = in.O.get_in(16 * rt0 + l15, quad), rv[0] = in.V.get(16 * rt0 + l15, quad), re[0] = in.E.get(16 * rt0 + l15, quad);
 #pragma unroll
         for (int ri = 0; ri < RT; ++ri) {
-            const int r = 16 * (rt0 + ri) + l15;
-            oS[ri] = mma(in.O.get_in(r, quad), s, oS[ri]);
-            vS[ri] = mma(in.V.get(r, quad), s, vS[ri]);
-            eD[ri] = mma(in.E.get(r, quad), d, eD[ri]);
+            if (ri + 1 < RT) {
+                const int r = 16 * (rt0 + ri + 1) + l15, n = (ri + 1) & 1;
+                ro[n] = in.O.get_in(r, quad), rv[n] = in.V.get(r, quad), re[n] = in.E.get(r, quad);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            oS[ri] = mma(ro[ri & 1], s, oS[ri]);
+            vS[ri] = mma(rv[ri & 1], s, vS[ri]);
+            eD[ri] = mma(re[ri & 1], d, eD[ri]);
         }
         if (v + 32 < a.Dv)
             spread(buf ^ 1);
