@@ -296,14 +296,19 @@ template <bool BF, int PL> __device__ __forceinline__ Mid<BF, PL> mid_split(cons
     }
     return f;
 }
-template <bool BF, int PL> __device__ __forceinline__ void frag_store(char *p, int frag, const float (&v)[8])
+// past: past the caches
+template <bool BF, int PL> __device__ __forceinline__ void frag_store(const Buf &b, int frag, const float (&v)[8], bool past)
 {
     const Mid<BF, PL> f = mid_split<BF, PL>(v);
     u32x4 t[sizeof f / 16];
     __builtin_memcpy(t, &f, sizeof f);
+    const unsigned at = frag * frag_bytes<BF, PL> + 16u * (threadIdx.x & 63);
 #pragma unroll
     for (unsigned j = 0; j < sizeof f / 16; ++j)
-        *reinterpret_cast<u32x4 *>(p + frag * frag_bytes<BF, PL> + 1024 * j + 16 * (threadIdx.x & 63)) = t[j];
+        if (past)
+            __builtin_amdgcn_raw_buffer_store_b128(t[j], b.r, at + 1024 * j, 0, NT_STORE);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(t[j], b.r, at + 1024 * j, 0, 0);
 }
 // ROWS rows of K split values in LDS, a plane for each word. Rows are 32 bytes longer
 // than their values, so that 16 rows' reads of one piece of 16 bytes meet no bank
