@@ -595,7 +595,8 @@ srnl_status srnl_dropout_bwd(const void *dout, srnl_dtype out_dtype, long long c
  *   head h / (H / Hk). Tokens of q, k and v may lie q_stride, k_stride, v_stride
  *   elements apart (slices of one projection), at most 2^22; item b starts T strides on.
  *   g, beta [B][T][H], states [B][H][Dk][Dv], fp32.
- *   Dk and Dv multiples of 8, up to 128 and 256; H a multiple of Hk.
+ *   Dk and Dv multiples of 8, up to 128 and 256; H a multiple of Hk; H Dk and H Dv
+ *   at most 2^22.
  *   lengths [B] or NULL: tokens at or past an item's length (held to 0..T) are
  *   not read and change nothing; their outputs and gradients are zero.
  * g is at most 0 in use and may be -infinity (the state starts anew); beta is
@@ -625,8 +626,9 @@ srnl_status srnl_gated_delta_step(const srnl_gated_delta_params *params, void *o
  * srnl_gated_delta_fwd -- the rule over whole sequences, 64 tokens at a time.
  * state_out as above. record: NULL, or srnl_gated_delta_record_bytes of memory
  * that the call fills for srnl_gated_delta_bwd (errors and states of every chunk).
- * With bf16 inputs, what the call forms between is kept to 2^-17 (pairs of bf16
- * words); sums are fp32, in a fixed order (bitwise reproducible).
+ * With bf16 inputs, what the call forms between is kept to 2^-26 (three bf16 words)
+ * where states and fp32 gradients depend on it, to 2^-18 (two) where bf16 outputs
+ * alone do; sums are fp32, in a fixed order (bitwise reproducible).
  * Workspace: srnl_gated_delta_fwd_workspace_bytes. Errors: as the step, plus
  * SRNL_ERR_WORKSPACE (workspace or record).
  */

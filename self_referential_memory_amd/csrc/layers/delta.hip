@@ -39,6 +39,9 @@ srnl_status check_delta(const srnl_gated_delta_params *p)
         if (static_cast<__int128>(p->B) * p->T * s >= (static_cast<__int128>(1) << 60))
             return fail(SRNL_ERR_ARG, "tensors too large");
     }
+    // so are those of the parts of dq and dk that heads which share them write
+    if (static_cast<long long>(p->H) * p->Dk > 1 << 22)
+        return fail(SRNL_ERR_ARG, "a token's heads exceed 2^22 elements");
     // a block (of 512 threads at most) per 16 columns or per 64 tokens of a head
     const __int128 bh = static_cast<__int128>(p->B) * p->H;
     if (bh * ((p->Dv + 15) / 16) > MAX_BLOCKS || bh * ((p->T + 63LL) / 64) > MAX_BLOCKS)

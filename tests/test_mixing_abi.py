@@ -85,7 +85,7 @@ BAD = [(dict(params=False), PTR), (dict(B=-1), ARG), (dict(T=-1), ARG), (dict(Hk
        (dict(H=3), ARG), (dict(H=-4), ARG), (dict(Dk=0), ARG), (dict(Dk=12), ARG), (dict(Dk=136), ARG),
        (dict(Dv=4), ARG), (dict(Dv=264), ARG), (dict(Dv=-8), ARG), (dict(H=1 << 21), ARG), (dict(q_stride=24), ARG),
        (dict(k_stride=33), ARG), (dict(v_stride=88), ARG), (dict(v_stride=100), ARG), (dict(q_stride=-32), ARG),
-       (dict(q_stride=(1 << 22) + 8), ARG), (dict(B=1 << 30), ARG), (dict(T=(1 << 31) - 1, B=4), ARG),
+       (dict(H=1 << 18, Dk=24, Dv=8), ARG), (dict(q_stride=(1 << 22) + 8), ARG), (dict(B=1 << 30), ARG), (dict(T=(1 << 31) - 1, B=4), ARG),
        (dict(dtype=2), DTYPE), (dict(scale=NAN), ARG), (dict(scale=INF), ARG), (dict(norm_eps=-1e-9), ARG),
        (dict(norm_eps=NAN), ARG), (dict(norm_eps=INF), ARG)]
 
