@@ -161,11 +161,12 @@ namespace srnl_i {
 
 srnl_status launch_delta_step(const DeltaArgs &a, hipStream_t st)
 {
-    // 64 columns a block; 32 where that leaves compute units idle
-    if (static_cast<long long>(a.B) * a.H * ((a.Dv + 63) / 64) >= 256)
-        launch_step<16>(a, st);
-    else
+    // 64 columns a block, 32 where v has no more: 256 x 16 heads of 128 x 32 take 25 us
+    // with 32, 27 with 64; 64 x 16 of 128 x 128, 5 tokens, 68 and 44
+    if (a.Dv <= 32)
         launch_step<8>(a, st);
+    else
+        launch_step<16>(a, st);
     return launched("delta_step_kernel");
 }
 

@@ -13,6 +13,10 @@
 // into slabs of cells whose sums a second kernel joins and a third applies. A thread
 // keeps a column of V channels and walks the cells, threads side by side along the
 // channels, so every access is a wide piece of a row.
+//
+// 64 x 3136 x 64 bf16, slices: forward 25 us (51 MB, 2.1 TB/s), back 31 (77 MB read and
+// written once, 2.5 TB/s): a slice's accesses are 16 or 32 bytes of each row. 5 x 1551 x
+// 210 fp32, slabs: 5 + 7 + 7 us and 8 + 5 + 8 + 5, seven short kernels.
 #include "linear.h"
 
 namespace {
