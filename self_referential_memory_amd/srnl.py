@@ -999,11 +999,11 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
 
 def _delta_shapes(q, k, v, g, beta, state, lengths):
     """(B, T, Hk, H, Dk, Dv) of a call whose shapes and types agree."""
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dim() != 4:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [B, T, heads, D]")
+    if q.dim() != 4 or v.dim() != 4:
+        t, name = (q, "q") if q.dim() != 4 else (v, "v")
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [B, T, heads, D]")
     B, T, Hk, Dk = q.shape
-    H, Dv = v.shape[2:]
+    _, _, H, Dv = v.shape
     _expect(k, (B, T, Hk, Dk), q.dtype, "k")
     _expect(v, (B, T, H, Dv), q.dtype, "v")
     _expect(g, (B, T, H), torch.float32, "g")
@@ -1035,7 +1035,7 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
         p = _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
         state_out = state if state_out is None else _new(state_out, state.shape, torch.float32,
                                                          q.device, "state_out")
-        out = _new(out, v.shape, q.dtype, q.device)
+        out = _new(out, v.shape, q.dtype, q.device, like=v if v.is_contiguous() else None)
         _check(lib().srnl_gated_delta_step(ctypes.byref(p), _ptr(out), _ptr(state_out)),
                "srnl_gated_delta_step")
     return out, state_out
@@ -1056,7 +1056,7 @@ def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
     with _on(q, k, v, g, beta, state, lengths):
         p = _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
         state_out = _new(state_out, (B, H, Dk, Dv), torch.float32, q.device, "state_out")
-        out = _new(out, v.shape, q.dtype, q.device)
+        out = _new(out, v.shape, q.dtype, q.device, like=v if v.is_contiguous() else None)
         rec = None
         if record:
             rec = torch.empty(L.srnl_gated_delta_record_bytes(ctypes.byref(p)), dtype=torch.uint8,
