@@ -130,6 +130,17 @@ def test_forward_and_backward(B, S, C, G, x_t, y_t, kind):
     check(B, S, C, G, x_t, y_t, kind)
 
 
+@pytest.mark.parametrize("B,S,C,G", [
+    # slices of 64, 32 and 16 channels, each pass's and type's own
+    (64, 196, 256, 16), (64, 784, 128, 16), (300, 100, 64, 8), (64, 1568, 64, 16),
+    # few groups of many slabs and channels; few slices, just short and just long enough for slabs
+    (3, 2149, 366, 2), (1, 9, 20000, 2), (1, 3584, 256, 32), (1, 3585, 256, 32)])
+@pytest.mark.parametrize("x_t,y_t", [(F32, F32), (BF16, BF16), (BF16, F32)])
+def test_where_a_map_is_cut(B, S, C, G, x_t, y_t):
+    print("[gnorm cut]", B, S, C, G, x_t, y_t, flush=True)
+    check(B, S, C, G, x_t, y_t, "silu")
+
+
 def test_constant_maps_and_large_offsets():
     """A constant group has variance 0: y = act(bias). An offset of 1e4 keeps
     its digits. An infinity makes NaN of its item's group alone."""
