@@ -180,21 +180,7 @@ __device__ __forceinline__ u32x4 buf16(const Buf &b, unsigned o)
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.r, o, 0, 0));
 }
 
-// bf16 words or fp32 values as they come
-template <bool BF> struct Raw { uint16_t v; };
-template <> struct Raw<false> { float v; };
-__device__ __forceinline__ float value(Raw<true> r) { return bf16_one(r.v); }
-__device__ __forceinline__ float value(Raw<false> r) { return r.v; }
-// o in elements
-template <bool BF> __device__ __forceinline__ Raw<BF> raw_load(const Buf &b, int o, bool live)
-{
-    Raw<BF> v;
-    if constexpr (BF)
-        v.v = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(b.r, live ? 2u * o : NOWHERE, 0, 0));
-    else
-        v.v = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b.r, live ? 4u * o : NOWHERE, 0, 0));
-    return v;
-}
+// a value at element o
 template <bool BF> __device__ __forceinline__ void put_value(const Buf &b, int o, bool live, float v)
 {
     if constexpr (BF)
