@@ -300,3 +300,27 @@ def test_offsets_past_32_bits():
                                    norm_eps=1e-6)
     assert torch.equal(o[-2:], o1[-2:]) and torch.equal(st[-2:], s1[-2:])
     assert not st[:-2].any()
+
+
+@pytest.mark.parametrize("Dv", [16, 40])
+def test_a_large_call_as_its_parts(Dv):
+    """More chunks than the caches hold, and more blocks than compute units, are stored
+    and cut in their own ways: the same values, bit for bit, as two calls of half of it."""
+    B, T, H = 200, 900, 1
+    assert B * H * 15 * 2 * 64 * 64 * 6 > 128 << 20 > B // 2 * H * 15 * 2 * 64 * 64 * 6
+    g = torch.Generator(DEV).manual_seed(Dv)
+    lengths = torch.randint(0, T + 1, (B,), generator=g, device=DEV).int()
+    q, k, v, dout = (torch.randn(B, T, H, n, generator=g, device=DEV).bfloat16() for n in (16, 16, Dv, Dv))
+    gate, beta = -torch.rand(B, T, H, generator=g, device=DEV), torch.rand(B, T, H, generator=g, device=DEV)
+    dstate = torch.randn(B, H, 16, Dv, generator=g, device=DEV)
+
+    def both(s):
+        part = dict(q=q[s], k=k[s], v=v[s], g=gate[s], beta=beta[s], state=None, lengths=lengths[s])
+        out, S, rec = call(part, record=True)
+        return [out, S] + [t for t in back(part, dout[s], rec, dstate=dstate[s]) if t is not None]
+
+    whole = both(slice(0, B))
+    for s in (slice(0, B // 2), slice(B // 2, B)):
+        for a, b in zip(whole, both(s)):
+            assert torch.equal(a[s], b)
+            assert b.isfinite().all()
