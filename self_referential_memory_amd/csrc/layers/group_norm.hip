@@ -16,7 +16,7 @@
 //
 // 64 x 3136 x 64 bf16, slices: forward 25 us (51 MB, 2.1 TB/s), back 31 (77 MB read and
 // written once, 2.5 TB/s): a slice's accesses are 16 or 32 bytes of each row. 5 x 1551 x
-// 210 fp32, slabs: 5 + 7 + 7 us and 8 + 5 + 8 + 5, seven short kernels.
+// 210 fp32, slabs: 5 + 7 + 6 us and 7 + 5 + 7 + 5, seven short kernels.
 #include "linear.h"
 
 namespace {
@@ -79,6 +79,64 @@ template <int V> __device__ __forceinline__ void store_piece(void *p, bool bf, l
     }
 }
 
+// A piece as it lies in memory, at most 16 bytes: 8 channels are bf16 words, fewer
+// either type's. Loads and conversions are apart, so that many loads are in flight.
+template <int V> struct Held {
+    uint32_t w[V == 8 ? 4 : V];
+    __device__ __forceinline__ void load(const void *p, bool bf, long long o)
+    {
+        if (V == 8 || bf) {
+            const uint16_t *q = static_cast<const uint16_t *>(p) + o;
+            if constexpr (V == 8) {
+                const u32x4 t = *reinterpret_cast<const u32x4 *>(q);
+                w[0] = t[0], w[1] = t[1], w[2] = t[2], w[3] = t[3];
+            } else if constexpr (V == 4) {
+                const u32x2 t = *reinterpret_cast<const u32x2 *>(q);
+                w[0] = t[0], w[1] = t[1];
+            } else if constexpr (V == 2) {
+                w[0] = *reinterpret_cast<const uint32_t *>(q);
+            } else {
+                w[0] = *q;
+            }
+        } else if constexpr (V < 8) {
+            float v[V];
+            load_piece<V>(p, false, o, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                w[e] = __float_as_uint(v[e]);
+        }
+    }
+    __device__ __forceinline__ void get(bool bf, float (&v)[V]) const
+    {
+        if (V == 8 || bf) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                v[e] = __uint_as_float(w[V == 8 ? 0 : e]);
+        }
+    }
+};
+// f(k, s) for s = first, first + step and so on below last, U at a time (k = 0 .. U - 1),
+// after load(k, s) of all U: in a loop over single cells the branches on type and
+// activation keep each one's load behind the one before (2 x 12544 x 128 bf16 19 us
+// forward and 25 back, 17 and 21 so; 64 x 3136 x 64 fp32 forward 40, 34 so).
+template <int U, class L, class F>
+__device__ __forceinline__ void in_batches(long long first, long long step, long long last, L load, F f)
+{
+    for (long long s0 = first; s0 < last; s0 += U * step) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            load(k, s0 + k * step < last ? s0 + k * step : s0);
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            if (s0 + k * step < last)
+                f(k, s0 + k * step);
+    }
+}
+
 // A thread's place: its channels, and the cells it walks.
 template <int V> struct Place {
     int b, c, lanes, lane;          // channel c .. c + V - 1; every lanes-th cell from lane
@@ -136,17 +194,20 @@ template <int V> __global__ __launch_bounds__(256) void gn_stats_kernel(GnArgs a
             from[e] = s1[e] = s2[e] = 0.0f;
         if (mine)
             load_piece<V>(a.x, a.xbf, pl.at(a, pl.first + pl.lane), from);
-#pragma unroll 4
-        for (long long i = 1; i < mine; ++i) {
-            float v[V];
-            load_piece<V>(a.x, a.xbf, pl.at(a, pl.first + pl.lane + i * pl.lanes), v);
+        Held<V> x[4];
+        in_batches<4>(
+            pl.first + pl.lane + pl.lanes, pl.lanes, pl.last,
+            [&](int k, long long s) __attribute__((always_inline)) { x[k].load(a.x, a.xbf, pl.at(a, s)); },
+            [&](int k, long long) __attribute__((always_inline)) {
+                float v[V];
+                x[k].get(a.xbf, v);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float d = v[e] - from[e];
-                s1[e] += d;
-                s2[e] = fmaf(d, d, s2[e]);
-            }
-        }
+                for (int e = 0; e < V; ++e) {
+                    const float d = v[e] - from[e];
+                    s1[e] += d;
+                    s2[e] = fmaf(d, d, s2[e]);
+                }
+            });
         const float n = static_cast<float>(mine);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -324,16 +385,19 @@ template <int V> __global__ __launch_bounds__(256) void gn_apply_kernel(GnArgs a
     if (!pl.live)
         return;
     const Channels<V> ch(a, pl);
-#pragma unroll 4
-    for (long long s = pl.first + pl.lane; s < pl.last; s += pl.lanes) {
-        float v[V];
-        load_piece<V>(a.x, a.xbf, pl.at(a, s), v);
+    Held<V> x[4];
+    in_batches<4>(
+        pl.first + pl.lane, pl.lanes, pl.last,
+        [&](int k, long long s) __attribute__((always_inline)) { x[k].load(a.x, a.xbf, pl.at(a, s)); },
+        [&](int k, long long s) __attribute__((always_inline)) {
+            float v[V];
+            x[k].get(a.xbf, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            v[e] = fmaf((v[e] - ch.mean[e]) * ch.rstd[e], ch.gain[e], ch.bias[e]);
-        act_piece<V>(v, a.act);
-        store_piece<V>(a.out, a.obf, pl.at(a, s), v);
-    }
+            for (int e = 0; e < V; ++e)
+                v[e] = fmaf((v[e] - ch.mean[e]) * ch.rstd[e], ch.gain[e], ch.bias[e]);
+            act_piece<V>(v, a.act);
+            store_piece<V>(a.out, a.obf, pl.at(a, s), v);
+        });
 }
 
 // Sums of dz n and of dz, per channel of a slab.
@@ -347,23 +411,29 @@ template <int V> __global__ __launch_bounds__(256) void gn_bwd_sums_kernel(GnArg
 #pragma unroll
         for (int e = 0; e < V; ++e)
             s0[e] = s1[e] = 0.0f;
-#pragma unroll 4
-        for (long long s = pl.first + pl.lane; s < pl.last; s += pl.lanes) {
-            float v[V], d[V], z[V];
-            load_piece<V>(a.x, a.xbf, pl.at(a, s), v);
-            load_piece<V>(a.dout, a.dbf, pl.at(a, s), d);
+        Held<V> x[4], dy[4];
+        in_batches<4>(
+            pl.first + pl.lane, pl.lanes, pl.last,
+            [&](int k, long long s) __attribute__((always_inline)) {
+                x[k].load(a.x, a.xbf, pl.at(a, s));
+                dy[k].load(a.dout, a.dbf, pl.at(a, s));
+            },
+            [&](int k, long long) __attribute__((always_inline)) {
+                float v[V], d[V], z[V];
+                x[k].get(a.xbf, v);
+                dy[k].get(a.dbf, d);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[e] = (v[e] - ch.mean[e]) * ch.rstd[e];
-                z[e] = fmaf(v[e], ch.gain[e], ch.bias[e]);
-            }
-            slope_piece<V>(z, a.act, d);
+                for (int e = 0; e < V; ++e) {
+                    v[e] = (v[e] - ch.mean[e]) * ch.rstd[e];
+                    z[e] = fmaf(v[e], ch.gain[e], ch.bias[e]);
+                }
+                slope_piece<V>(z, a.act, d);
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                s0[e] = fmaf(d[e], v[e], s0[e]);
-                s1[e] += d[e];
-            }
-        }
+                for (int e = 0; e < V; ++e) {
+                    s0[e] = fmaf(d[e], v[e], s0[e]);
+                    s1[e] += d[e];
+                }
+            });
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             lds[threadIdx.x][e] = s0[e];
@@ -420,27 +490,35 @@ template <int V> __global__ __launch_bounds__(256) void gn_bwd_apply_kernel(GnAr
         md[e] = a.means[2LL * group];
         mn[e] = a.means[2LL * group + 1];
     }
-#pragma unroll 4
-    for (long long s = pl.first + pl.lane; s < pl.last; s += pl.lanes) {
-        float v[V], d[V], z[V], w[V];
-        load_piece<V>(a.x, a.xbf, pl.at(a, s), v);
-        load_piece<V>(a.dout, a.dbf, pl.at(a, s), d);
-        if (a.add)
-            load_piece<V>(a.add, a.xbf, pl.at(a, s), w);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            v[e] = (v[e] - ch.mean[e]) * ch.rstd[e];
-            z[e] = fmaf(v[e], ch.gain[e], ch.bias[e]);
-        }
-        slope_piece<V>(z, a.act, d);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            v[e] = ch.rstd[e] * (d[e] * ch.gain[e] - md[e] - v[e] * mn[e]);
+    Held<V> x[4], dy[4], add[4];
+    in_batches<4>(
+        pl.first + pl.lane, pl.lanes, pl.last,
+        [&](int k, long long s) __attribute__((always_inline)) {
+            x[k].load(a.x, a.xbf, pl.at(a, s));
+            dy[k].load(a.dout, a.dbf, pl.at(a, s));
             if (a.add)
-                v[e] += w[e];
-        }
-        store_piece<V>(a.out, a.obf, pl.at(a, s), v);
-    }
+                add[k].load(a.add, a.xbf, pl.at(a, s));
+        },
+        [&](int k, long long s) __attribute__((always_inline)) {
+            float v[V], d[V], z[V], w[V];
+            x[k].get(a.xbf, v);
+            dy[k].get(a.dbf, d);
+            if (a.add)
+                add[k].get(a.xbf, w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                v[e] = (v[e] - ch.mean[e]) * ch.rstd[e];
+                z[e] = fmaf(v[e], ch.gain[e], ch.bias[e]);
+            }
+            slope_piece<V>(z, a.act, d);
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                v[e] = ch.rstd[e] * (d[e] * ch.gain[e] - md[e] - v[e] * mn[e]);
+                if (a.add)
+                    v[e] += w[e];
+            }
+            store_piece<V>(a.out, a.obf, pl.at(a, s), v);
+        });
 }
 
 // ------------------------------------------------------------------ slices
@@ -467,47 +545,6 @@ template <int V> struct Slice {
         live = lane < used;
     }
     __device__ __forceinline__ long long at(const GnArgs &a, long long s) const { return (b * a.S + s) * a.C + c; }
-};
-
-// A piece as it lies in memory, at most 16 bytes: 8 channels are bf16 words, fewer
-// either type's.
-template <int V> struct Held {
-    uint32_t w[V == 8 ? 4 : V];
-    __device__ __forceinline__ void load(const void *p, bool bf, long long o)
-    {
-        if (V == 8 || bf) {
-            const uint16_t *q = static_cast<const uint16_t *>(p) + o;
-            if constexpr (V == 8) {
-                const u32x4 t = *reinterpret_cast<const u32x4 *>(q);
-                w[0] = t[0], w[1] = t[1], w[2] = t[2], w[3] = t[3];
-            } else if constexpr (V == 4) {
-                const u32x2 t = *reinterpret_cast<const u32x2 *>(q);
-                w[0] = t[0], w[1] = t[1];
-            } else if constexpr (V == 2) {
-                w[0] = *reinterpret_cast<const uint32_t *>(q);
-            } else {
-                w[0] = *q;
-            }
-        } else if constexpr (V < 8) {
-            float v[V];
-            load_piece<V>(p, false, o, v);
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                w[e] = __float_as_uint(v[e]);
-        }
-    }
-    __device__ __forceinline__ void get(bool bf, float (&v)[V]) const
-    {
-        if (V == 8 || bf) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                v[e] = e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                v[e] = __uint_as_float(w[V == 8 ? 0 : e]);
-        }
-    }
 };
 
 // The slice's cells as a thread walks them: its NV pieces are held, or (NV = 0) each
@@ -539,11 +576,14 @@ __device__ __forceinline__ void each_cell(const GnArgs &a, const Slice<V> &sl, c
             }
         }
     } else if (sl.live) {
-#pragma unroll 4
-        for (long long s = sl.lane; s < a.S; s += sl.lanes) {
-            load_piece<V>(a.x, V == 8 || a.xbf, sl.at(a, s), v);
-            f(v, s);
-        }
+        Held<V> h[4];
+        in_batches<4>(
+            sl.lane, sl.lanes, a.S,
+            [&](int k, long long s) __attribute__((always_inline)) { h[k].load(a.x, a.xbf, sl.at(a, s)); },
+            [&](int k, long long s) __attribute__((always_inline)) {
+                h[k].get(a.xbf, v);
+                f(v, s);
+            });
     }
 }
 template <int V, int NV, class F>
@@ -562,12 +602,18 @@ __device__ __forceinline__ void each_cell(const GnArgs &a, const Slice<V> &sl, c
             }
         }
     } else if (sl.live) {
-#pragma unroll 2
-        for (long long s = sl.lane; s < a.S; s += sl.lanes) {
-            load_piece<V>(a.x, V == 8 || a.xbf, sl.at(a, s), v);
-            load_piece<V>(a.dout, V == 8 || a.dbf, sl.at(a, s), w);
-            f(v, w, s);
-        }
+        Held<V> h[2], g[2];
+        in_batches<2>(
+            sl.lane, sl.lanes, a.S,
+            [&](int k, long long s) __attribute__((always_inline)) {
+                h[k].load(a.x, a.xbf, sl.at(a, s));
+                g[k].load(a.dout, a.dbf, sl.at(a, s));
+            },
+            [&](int k, long long s) __attribute__((always_inline)) {
+                h[k].get(a.xbf, v);
+                g[k].get(a.dbf, w);
+                f(v, w, s);
+            });
     }
 }
 
@@ -770,8 +816,8 @@ template <int V, int NV> __global__ __launch_bounds__(SLICE_THREADS) void gn_sli
 // The widest piece that divides a row.
 int piece_of(int C) { return C % 8 == 0 ? 8 : C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1; }
 
-// A slice's pieces are 16 bytes at most of the wider type that it holds.
-int slice_piece(const GnArgs &a)
+// The kernels' pieces are 16 bytes at most of the wider type that they read.
+int read_piece(const GnArgs &a)
 {
     const int v = piece_of(a.C);
     return v == 8 && !(a.xbf && (!a.dout || a.dbf)) ? 4 : v;
@@ -808,7 +854,7 @@ void cut_slices(GnArgs &a)
 // forward, of 32 20.
 void widen_slices(GnArgs &a)
 {
-    const int v = slice_piece(a);
+    const int v = read_piece(a);
     while (a.C % (2 * a.slice) == 0 && static_cast<long long>(a.B) * (a.C / (2 * a.slice)) >= 256 &&
            2 * a.slice <= 64 && (a.dout || held(a.S, 2 * a.slice, v) || !held(a.S, a.slice, v)))
         a.slice *= 2;
@@ -818,10 +864,9 @@ void widen_slices(GnArgs &a)
 void cut_map(GnArgs &a)
 {
     const int pieces = a.C / piece_of(a.C);
-    a.tiles = (pieces + 255) / 256;
     const int lanes = pieces < 256 ? 256 / pieces : 1;
     const long long most = (a.S + 8LL * lanes - 1) / (8LL * lanes);
-    const long long items = static_cast<long long>(a.B) * a.tiles;
+    const long long items = static_cast<long long>(a.B) * ((pieces + 255) / 256);
     long long slabs = (1024 + items - 1) / items;
     slabs = slabs < most ? slabs : most;
     a.rows = (a.S + slabs - 1) / slabs;
@@ -834,8 +879,9 @@ size_t group_floats(const GnArgs &a) { return 2 * static_cast<size_t>(a.B) * a.G
 
 #define SRNL_GN_LAUNCH(kernel, a, st)                                                                  \
     do {                                                                                               \
+        (a).tiles = ((a).C / read_piece(a) + 255) / 256;                                               \
         const dim3 grid(static_cast<unsigned>(static_cast<long long>((a).B) * (a).slabs * (a).tiles)); \
-        switch (piece_of((a).C)) {                                                                     \
+        switch (read_piece(a)) {                                                                       \
         case 8: hipLaunchKernelGGL(kernel<8>, grid, dim3(256), 0, st, a); break;                       \
         case 4: hipLaunchKernelGGL(kernel<4>, grid, dim3(256), 0, st, a); break;                       \
         case 2: hipLaunchKernelGGL(kernel<2>, grid, dim3(256), 0, st, a); break;                       \
@@ -855,7 +901,7 @@ size_t group_floats(const GnArgs &a) { return 2 * static_cast<size_t>(a.B) * a.G
             hipLaunchKernelGGL((kernel<V, 0>), grid, dim3(SLICE_THREADS), 0, st, a);                   \
     } while (0)
 #define SRNL_GN_SLICE(kernel, MORE, a, st)                    \
-    switch (slice_piece(a)) {                                 \
+    switch (read_piece(a)) {                                 \
     case 8: SRNL_GN_SLICE_NV(kernel, 8, MORE, a, st); break;  \
     case 4: SRNL_GN_SLICE_NV(kernel, 4, MORE, a, st); break;  \
     case 2: SRNL_GN_SLICE_NV(kernel, 2, MORE, a, st); break;  \
