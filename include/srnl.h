@@ -626,9 +626,8 @@ srnl_status srnl_gated_delta_step(const srnl_gated_delta_params *params, void *o
  * srnl_gated_delta_fwd -- the rule over whole sequences, 64 tokens at a time.
  * state_out as above. record: NULL, or srnl_gated_delta_record_bytes of memory
  * that the call fills for srnl_gated_delta_bwd (errors and states of every chunk).
- * With bf16 inputs, what the call forms between is kept to 2^-26 (three bf16 words)
- * where states and fp32 gradients depend on it, to 2^-18 (two) where bf16 outputs
- * alone do; sums are fp32, in a fixed order (bitwise reproducible).
+ * With bf16 inputs, what the call forms between is kept to 2^-26 (three bf16 words);
+ * sums are fp32, in a fixed order (bitwise reproducible).
  * Workspace: srnl_gated_delta_fwd_workspace_bytes. Errors: as the step, plus
  * SRNL_ERR_WORKSPACE (workspace or record).
  */

@@ -296,8 +296,7 @@ template <class P> __device__ __forceinline__ void store_rows(const DeltaArgs &a
 template <bool BF, int KD, int NV, bool RECORD> struct FwdShared {
     __attribute__((aligned(16))) Rows<BF, KD> k;
     Split<BF, 3, NV, KD> S;                            // the state, transposed
-    Split<BF, 3, NV, 64> R, W;
-    Split<BF, 2, NV, 64> U;
+    Split<BF, 3, NV, 64> R, W, U;
     v4f e[RECORD ? 4 : 1][NV / 16][64];                // E as result tiles, for the helpers to record
     Factors w[2];
 };
@@ -321,13 +320,13 @@ template <bool BF, int KF, int NT, bool BACK> struct ChainIn {
 };
 template <bool BF, int KF> struct OutIn {
     In<BF> q[KF];
-    Mid<BF, 2> p[2];
+    Mid<BF, 3> p[2];
     Vec vec;                          // the next chunk's
     template <class P> __device__ __forceinline__ void load(const DeltaArgs &a, const P &pl, int c)
     {
         const int last = pl.chunks - 1;
         load_rows<BF, KF>(a, pl, a.q, a.qs, c < last ? c : last, q);
-        load_square<BF, 2, false>(a, pl, a.P, c < last ? c : last, p);
+        load_square<BF, 3, false>(a, pl, a.P, c < last ? c : last, p);
         vec.load(a, pl, c + 1 < last ? c + 1 : last);
     }
 };
@@ -426,12 +425,12 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
             store_state<KD, NV>(a, pl, sl, a.state_out, pl.bh, S);
     } else {
         const auto chunk = [&](const OutIn<BF, KF> &in, OutIn<BF, KF> &next, int c) __attribute__((always_inline)) {
-            Sum<BF, 2> qS[NT];
+            Sum<BF, 3> qS[NT];
 #pragma unroll
             for (int f = 0; f < KF; ++f)
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    qS[j].add(in.q[f], sh.S.template get<2>(16 * j + pl.l15, 4 * f + pl.quad));
+                    qS[j].add(in.q[f], sh.S.get(16 * j + pl.l15, 4 * f + pl.quad));
             const v4f read = sh.w[c & 1].rows(VEC_READQ, pl.rows);
             lds_barrier();
             next.load(a, pl, c + 1);
@@ -439,11 +438,11 @@ template <bool BF, int KD, int NV, bool RECORD> __global__ __launch_bounds__(512
                 store_words<BF, KD, NV>(a, pl, sh.S, a.S0, pl.at(a, c));
             lds_barrier();
             in.vec.store(sh.w[(c + 1) & 1], pl.wave);
-            Mid<BF, 2> us[2][NT];
+            Mid<BF, 3> us[2][NT];
             read_columns(sh.U, 0, pl.quad, pl.l15, us);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                Sum<BF, 2> pU;
+                Sum<BF, 3> pU;
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
                     if (half_live<false>(pl.wave, f))

@@ -41,7 +41,7 @@ template <bool BF, int KD> struct GradShared {
             Split<BF, 3, 64, 32> E, V;
         } in[2];
         struct {
-            Split<BF, 2, 64, 64> A, At, Z;
+            Split<BF, 3, 64, 64> A, At, Z;
         } out;
     };
     // a chunk's row factors, as they lie in memory from VEC_BETA on

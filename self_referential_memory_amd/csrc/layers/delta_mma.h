@@ -6,11 +6,10 @@
 // whose reduction order is the same for both operands.
 //
 // Inputs (In) are bf16 words or fp32 values. What the kernels form between (Mid) is
-// fp32, or with bf16 inputs a sum of PL bf16 words: two are right to 2^-18 and go
-// where only bf16 outputs depend on them; three, right to 2^-26, where states and
-// fp32 gradients do (with two those were off by 4e-6 to 7e-6, with three by 2e-7 to
-// 5e-7, as the fp32 path). A product of two leaves out the pairs of words below its
-// smallest kept one.
+// fp32, or with bf16 inputs a sum of PL bf16 words: three, right to 2^-27, so that
+// results are off by what fp32 sums lose. With two (2^-18) states and gradients were
+// off by 2e-6 to 7e-6, and a bf16 output in 400 rounded to the other side. A product
+// of two leaves out the pairs of words below its smallest kept one.
 #ifndef SRNL_LAYERS_DELTA_MMA_H
 #define SRNL_LAYERS_DELTA_MMA_H
 
@@ -304,14 +303,14 @@ template <bool BF, int PL, int ROWS, int K> struct Split {
     static constexpr int PLANES = BF ? PL : 1, ROW = K * (BF ? 2 : 4) + 32;
     __attribute__((aligned(16))) char b[PLANES][ROWS][ROW];
 
-    // 8 values of row r from piece g on, the first N words of them
-    template <int N = PL> __device__ __forceinline__ Mid<BF, N> get(int r, int g) const
+    // 8 values of row r from piece g on
+    __device__ __forceinline__ Mid<BF, PL> get(int r, int g) const
     {
-        Mid<BF, N> f;
-        u32x4 t[BF ? N : 2];
+        Mid<BF, PL> f;
+        u32x4 t[BF ? PL : 2];
         if constexpr (BF) {
 #pragma unroll
-            for (int p = 0; p < N; ++p)
+            for (int p = 0; p < PL; ++p)
                 t[p] = *reinterpret_cast<const u32x4 *>(&b[p][r][16 * g]);
         } else {
             t[0] = *reinterpret_cast<const u32x4 *>(&b[0][r][32 * g]);

@@ -194,9 +194,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, bool past)
         for (int r = 0; r < 4; ++r)
             L[16 * wave + 4 * quad + r][16 * j + l15] = p[j][r];
     __syncthreads();
-    // P itself meets outputs alone, its transpose the states' gradients. The half of a
-    // row that is zero is not written: nobody reads it.
-    constexpr int PP = TRANSPOSED ? 3 : 2;
+    // The half of a row that is zero is not written: nobody reads it.
     const long long square = static_cast<long long>(blockIdx.x) * DELTA_SQUARE;
     const Buf xo(a.X, square), po(a.P, square);
 #pragma unroll
@@ -211,7 +209,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, bool past)
             y[e] = TRANSPOSED ? L[k + e][row] : L[row][k + e];
         }
         frag_store<BF, 3>(xo, 2 * wave + f, x, past);
-        frag_store<BF, PP>(po, 2 * wave + f, y, past);
+        frag_store<BF, 3>(po, 2 * wave + f, y, past);
     }
 }
 
