@@ -1,0 +1,32 @@
+"""Calls of the gated delta rule that a program may come to make without meaning
+to, through every entry point."""
+import pytest
+import torch
+
+from self_referential_memory_amd import srnl
+from tests import delta_oracle
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def inputs(B, T, seed=70):
+    d = delta_oracle.inputs(seed, B, T, 2, 2, 16, 16, torch.float32, state=True)
+    return {n: None if t is None else t.to(DEV) for n, t in d.items()}
+
+
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+@pytest.mark.parametrize("B,T", [(1, 5), (3, 1), (3, 5)])
+def test_broadcast_inputs_are_refused(B, T, name):
+    x = inputs(B, T)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    out, _, rec = srnl.gated_delta_fwd(*args, record=True)
+    i = "qkv".index(name)
+    args[i] = args[i][:1, :1].expand(args[i].shape)
+    for call in (lambda: srnl.gated_delta_step(*args, x["state"]), lambda: srnl.gated_delta_fwd(*args),
+                 lambda: srnl.gated_delta_bwd(out, *args, rec),
+                 lambda: srnl.gated_delta(*args[:4], x["beta"].clone().requires_grad_())):
+        with pytest.raises(ValueError, match=f"{name} must be contiguous"):
+            call()
+    args[i] = args[i].contiguous()
+    assert srnl.gated_delta_fwd(*args)[0].isfinite().all()
