@@ -528,8 +528,9 @@ srnl_status srnl_dwconv_bwd(const void *dout, srnl_dtype out_dtype, const void *
  *   x [B][S][C] in in_dtype; out [B][S][C] in out_dtype; gain, bias [C] fp32,
  *   either NULL for 1 and 0; mean, rstd [B][groups] fp32, written unless NULL
  *   (the backward pass reads them; 0 over no cells). C a multiple of groups,
- *   C <= 2^20, B C <= 2^23. The variance is taken about the mean. Activations as
- *   in srnl_linear_fwd. A NaN or infinity makes NaN of its item's group alone.
+ *   C <= 2^20, B C <= 2^23 (below it where C = 1). The variance is taken about the
+ *   mean. Activations as in srnl_linear_fwd. A NaN or infinity makes NaN of its
+ *   item's group alone.
  * Workspace: srnl_group_norm_fwd_workspace_bytes.
  * Errors: SRNL_ERR_ARG, SRNL_ERR_DTYPE, SRNL_ERR_PTR, SRNL_ERR_WORKSPACE,
  * SRNL_ERR_HIP.

@@ -921,8 +921,9 @@ srnl_status check_gn(int B, long long S, int C, int G, srnl_dtype x, srnl_dtype 
         return fail(SRNL_ERR_ARG, "C must be >= 1 and a multiple of groups");
     if (C > 1 << 20 || static_cast<__int128>(B) * S * C >= (static_cast<__int128>(1) << 60) || S >= 1LL << 40)
         return fail(SRNL_ERR_ARG, "map too large");
-    // an item and tile of channels is a block, and so is a group
-    if (static_cast<__int128>(B) * C > 1 << 23)
+    // an item and tile of channels is a block, and so is a group; a slice is one of 512
+    // threads, of which a launch takes 2^32 - 1: maps of one channel have 2^23 slices
+    if (static_cast<__int128>(B) * C > (C == 1 ? (1 << 23) - 1 : 1 << 23))
         return fail(SRNL_ERR_ARG, "B x C is too large");
     if (!valid_dtype(x) || !valid_dtype(out))
         return fail(SRNL_ERR_DTYPE, "dtype must be SRNL_F32 or SRNL_BF16");
