@@ -1030,7 +1030,17 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     Hk, Dk], v [B, T, H, Dv], g, beta [B, T, H], lengths [B] int32 or None.
     Returns (out [B, T, H, Dv] in q's dtype, the states after the last token):
     state [B, H, Dk, Dv] itself, updated in place, unless state_out is given.
-    scale: 1 / sqrt(Dk) when None."""
+    scale: 1 / sqrt(Dk) when None. It has no gradient, and raises where autograd
+    wants one: gated_delta has."""
+    # (_tracked, without its loop's 1.5 us on the host)
+    if (torch.is_grad_enabled()
+            and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
+                 or beta.requires_grad or state.requires_grad
+                 or (state_out is not None and state_out.requires_grad)
+                 or (out is not None and out.requires_grad))
+            or forward_ad._current_level >= 0 and _tracked(q, k, v, g, beta, state, state_out, out)):
+        raise RuntimeError("gated_delta_step has no gradient: call it under torch.no_grad(), on detached "
+                           "tensors, or use gated_delta")
     sizes = _delta_shapes(q, k, v, g, beta, state, lengths)
     with _on(q, k, v, g, beta, state, lengths):
         p = _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stream)
