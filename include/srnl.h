@@ -600,8 +600,17 @@ srnl_status srnl_dropout_bwd(const void *dout, srnl_dtype out_dtype, long long c
  *   at most 2^22.
  *   lengths [B] or NULL: tokens at or past an item's length (held to 0..T) are
  *   not read and change nothing; their outputs and gradients are zero.
- * g is at most 0 in use and may be -infinity (the state starts anew); beta is
+ * g is at most 0 in use and may be -infinity (a finite state starts anew); beta is
  * any number. States, sums and norms are fp32; the layers' conventions hold.
+ * A NaN or infinity goes where the formulas take it in the step. Over whole sequences
+ * it goes further, as NaN, for products run over the tokens of a chunk (64, counted
+ * from an item's first), with zeros for those that a token does not see: one in k, v, g,
+ * beta or the state (with bf16 inputs, a value between above 3.39e38 too) reaches the
+ * outputs of its head from its chunk's first token on, tokens before its own among
+ * them, one in v or the state those of its column of v alone; one in q reaches its
+ * token's alone. Back, one in v reaches the gradients of its head from its chunk on, one
+ * in q or dout those from its chunk to the first, any other all of its head's. Other
+ * heads and items are as without it (dq and dk are sums over the heads that share them).
  */
 typedef struct {
     const void *q, *k, *v;
