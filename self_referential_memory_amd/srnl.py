@@ -992,7 +992,7 @@ def _token_stride(t: torch.Tensor, name: str) -> int:
     s = t.stride()
     step = s[1] if T > 1 else s[0]
     # a broadcast token has step 0, which is dense to the library
-    if s[3] != 1 or s[2] != d or step < h * d or (T > 1 and B > 1 and s[0] != T * step):
+    if s[3] != 1 or (h > 1 and s[2] != d) or step < h * d or (T > 1 and B > 1 and s[0] != T * step):
         raise ValueError(f"{name} must be contiguous, or a slice of the last axis of a contiguous "
                          "[B, T, ...] tensor (a broadcast one is neither)")
     return step

@@ -32,3 +32,13 @@ def test_slices_and_dense_tensors_are_taken(B, T):
     assert srnl._token_stride(p, "v") == (0 if B * T == 1 else 40)
     dense = torch.zeros(B * T * 32).as_strided((B, T, 2, 16), (T * 32, 32, 16, 1))
     assert srnl._token_stride(dense, "v") == 0
+
+
+def test_one_head_of_a_wider_row_is_taken():
+    """A single head's stride to the next one says nothing."""
+    p = torch.zeros(3, 5, 1, 40)
+    assert srnl._token_stride(p[..., 8:24], "q") == 40
+    assert srnl._token_stride(p[:, :1].contiguous()[..., 8:24], "q") == 40
+    assert srnl._token_stride(torch.zeros(3, 5, 4, 16)[:, :, 1:2], "q") == 64
+    with pytest.raises(ValueError, match="q must be contiguous"):
+        srnl._token_stride(torch.zeros(3, 5, 2, 40)[..., 8:24], "q")

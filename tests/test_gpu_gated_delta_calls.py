@@ -30,3 +30,22 @@ def test_broadcast_inputs_are_refused(B, T, name):
             call()
     args[i] = args[i].contiguous()
     assert srnl.gated_delta_fwd(*args)[0].isfinite().all()
+
+
+def test_one_head_of_a_wider_row():
+    x = inputs(3, 70)
+    one = {n: t[:, :, :1].contiguous() if n != "state" else t[:, :1].contiguous() for n, t in x.items() if t is not None}
+    wide = dict(one)
+    for n in ("q", "k", "v"):
+        p = torch.full((3, 70, 1, 40), float("nan"), device=DEV)
+        p[..., 8:24] = one[n]
+        wide[n] = p[..., 8:24]
+    args, same = ([u[n] for n in ("q", "k", "v", "g", "beta")] for u in (one, wide))
+    dout = torch.randn(3, 70, 1, 16, device=DEV)
+    o, s, r = srnl.gated_delta_fwd(*args, record=True)
+    o2, s2, r2 = srnl.gated_delta_fwd(*same, record=True)
+    assert torch.equal(o, o2) and torch.equal(s, s2)
+    for a, b in zip(srnl.gated_delta_bwd(dout, *args, r)[:5], srnl.gated_delta_bwd(dout, *same, r2)[:5]):
+        assert torch.equal(a, b)
+    for a, b in zip(srnl.gated_delta_step(*args, one["state"].clone()), srnl.gated_delta_step(*same, one["state"].clone())):
+        assert torch.equal(a, b)
