@@ -142,3 +142,18 @@ def on_other_sides(got, ref, tol):
     step = 2.0 ** -7 * torch.exp2(torch.floor(torch.log2(ref.abs().clamp(min=1e-30))))
     mean = (e / step).clamp(max=1.0).sum().item()
     return count, mean + 4 * mean ** 0.5 + 1
+
+
+# fp32 results, in norm over an item's and head's values, by the same counting. With
+# fp32 inputs a product of K = 128 is a sum of 32 instructions' results of 4 products:
+# 3.5 u in the mean; a chunk 6 u, gradients with what they carry 9 u. Four times these.
+FINE = {torch.bfloat16: {"out": 16 * U, "grad": 24 * U}, torch.float32: {"out": 24 * U, "grad": 36 * U}}
+
+
+def off(got, ref, heads):
+    """|got - ref| in norm per item and head (axis `heads`), relative to the larger of
+    the reference's norm there and its mean over them: the largest."""
+    ref = ref.detach()
+    dims = [i for i in range(ref.dim()) if i not in (0, heads)]
+    err, norm = ((t.square().sum(dims)).sqrt() for t in (got.detach().cpu().double() - ref, ref))
+    return (err / torch.maximum(norm, norm.mean())).max().item()
