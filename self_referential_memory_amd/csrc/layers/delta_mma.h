@@ -92,16 +92,6 @@ template <bool BF, int PL> struct Sum {
             part[0] = mma16(a.v, b.v, part[0]);
         }
     }
-    __device__ __forceinline__ void add(const Mid<BF, PL> &a, const In<BF> &b)
-    {
-        if constexpr (BF) {
-#pragma unroll
-            for (int j = PL - 1; j >= 0; --j)
-                part[j] = mma16(a.p[j], b.v, part[j]);
-        } else {
-            part[0] = mma16(a.v, b.v, part[0]);
-        }
-    }
     __device__ __forceinline__ void add(const Mid<BF, PL> &a, const Mid<BF, PL> &b)
     {
         if constexpr (BF) {
