@@ -9,10 +9,11 @@
 //
 // Two ways. Where items and groups make enough blocks, a block takes all the cells of
 // a slice of whole groups: one kernel each way, which holds the slice in registers if
-// it fits and otherwise reads it again, from the L2 cache. Else an item's map is cut
-// into slabs of cells whose sums a second kernel joins and a third applies. A thread
-// keeps a column of V channels and walks the cells, threads side by side along the
-// channels, so every access is a wide piece of a row.
+// it fits and otherwise reads it again, from the L2 as far as that holds the eight items
+// an XCD works on, else from the cache behind it. Else an item's map is cut into slabs of
+// cells whose sums a second kernel joins and a third applies. A thread keeps a column of
+// V channels and walks the cells, threads side by side along the channels, so every
+// access is a wide piece of a row.
 //
 // 64 x 3136 x 64 bf16, slices: forward 25 us (51 MB, 2.1 TB/s), back 31 (77 MB read and
 // written once, 2.5 TB/s): a slice's accesses are 16 or 32 bytes of each row. 5 x 1551 x
@@ -286,7 +287,7 @@ template <class F> __device__ __forceinline__ void each_of_group(int i, int n, i
                 f(r, c);
 }
 // A block joins one group's channels and slabs. There may be few groups and much of
-// each: with 256 threads 3 x 2 groups of 268 slabs x 183 channels take JOIN256 us, with
+// each: with 256 threads 3 x 2 groups of 268 slabs x 183 channels take 37 us, with
 // 1024 20 (5 x 7 of 97 x 30: 7.3 and 6.8).
 constexpr int JOIN_THREADS = 1024;
 // the sum over such a block
@@ -845,8 +846,9 @@ int read_piece(const GnArgs &a)
     return v == 8 && !(a.xbf && (!a.dout || a.dbf)) ? 4 : v;
 }
 // The pieces of V channels that a thread holds of a slice of w, 0: it reads them again.
-// Backward there are two arrays to hold: eight pieces of each leave two waves a SIMD,
-// and reading again is faster (64 x 3136 x 64 bf16 30.9 us, 39.8 held).
+// Backward there are two arrays to hold: eight pieces of each are slower than reading
+// again in slices of 8 channels (64 x 3136 x 64 bf16 39.8 us, 30.9), and as fast in the
+// wider ones chosen (64 x 1568 x 64 18.5 and 18.6, 64 x 784 x 128 21.2 and 20.6).
 int held(long long S, int w, int v, bool backward = false)
 {
     const int lanes = SLICE_THREADS / (w / v);
