@@ -1021,6 +1021,12 @@ def _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stre
         _dtype_code(q), sizes[4] ** -0.5 if scale is None else scale, norm_eps, _stream(stream, q))
 
 
+def _written(state: torch.Tensor) -> None:
+    """States go from call to call in one tensor: a graph that holds what was in it
+    has to notice, as of torch's own in-place operations."""
+    torch._C._increment_version((state,))
+
+
 def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                      beta: torch.Tensor, state: torch.Tensor, *, lengths: Optional[torch.Tensor] = None,
                      scale: Optional[float] = None, norm_eps: float = 0.0,
@@ -1049,6 +1055,7 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
         out = _new(out, v.shape, q.dtype, q.device, like=v if v.is_contiguous() else None)
         _check(lib().srnl_gated_delta_step(ctypes.byref(p), _ptr(out), _ptr(state_out)),
                "srnl_gated_delta_step")
+    _written(state_out)
     return out, state_out
 
 
@@ -1077,6 +1084,7 @@ def gated_delta_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.
                                       0 if rec is None else rec.numel(), _ptr(ws),
                                       0 if ws is None else ws.numel()), "srnl_gated_delta_fwd")
         _keep_for_stream(p.stream, ws)
+    _written(state_out)
     return (out, state_out, rec) if record else (out, state_out)
 
 

@@ -49,3 +49,32 @@ def test_one_head_of_a_wider_row():
         assert torch.equal(a, b)
     for a, b in zip(srnl.gated_delta_step(*args, one["state"].clone()), srnl.gated_delta_step(*same, one["state"].clone())):
         assert torch.equal(a, b)
+
+
+def test_states_written_in_place_are_noticed_by_autograd():
+    """A graph that holds the states from before an in-place call raises, as it does
+    for torch's own in-place operations, and does not use what it finds there."""
+    x = inputs(2, 5)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+
+    def step():
+        srnl.gated_delta_step(*args, x["state"])
+
+    def forward():
+        srnl.gated_delta_fwd(*args, state=x["state"], state_out=x["state"])
+
+    for call in (step, forward):
+        w = torch.ones_like(x["state"]).requires_grad_()
+        loss = (w * x["state"]).sum()
+        with torch.no_grad():
+            call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        loss = (w * x["state"]).sum()
+        with torch.no_grad():                     # into another tensor
+            srnl.gated_delta_step(*args, x["state"], state_out=torch.empty_like(x["state"]))
+        loss.backward()
+        assert torch.equal(w.grad, x["state"])
+    with torch.inference_mode():
+        y = {n: t.clone() for n, t in x.items() if t is not None}
+        srnl.gated_delta_step(*(y[n] for n in ("q", "k", "v", "g", "beta")), y["state"])
