@@ -52,3 +52,36 @@ def test_first_cell_far_out(B, S, C, G, dtype, offset, far):
             assert abs(mean[b, g].item() - m.item()) <= chain * U * d.mean().item() + 4 * U * slab, "mean"
             assert abs(rstd[b, g].item() / r.item() - 1) <= (chain + 4) * U, "rstd"
     assert y.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_slabs_of_constant_offset_and_infinite_items(dtype):
+    """What holds for a slice holds for a map cut into slabs: a constant group's
+    variance is 0, an offset keeps its digits, an infinity stays in its group."""
+    gen = torch.Generator("cuda:0").manual_seed(5)
+    B, S, C, G = 5, 9001, 64, 16                       # 8 slices an item, of more than 14 cells a thread
+    x = torch.randn(B, S, C, generator=gen, device="cuda:0")
+    gain, bias = (torch.randn(C, generator=gen, device="cuda:0") for _ in range(2))
+    x[0] = 7.25
+    x[1] += 1e4 if dtype == F32 else 100.0
+    x = x.to(dtype)
+    x[2, 0, 5] = float("inf")                          # a thread's first cell
+    x[3, 8999, 5] = float("-inf")
+    x[4, 4500, 9] = float("nan")
+    y, mean, rstd = srnl.group_norm_fwd(x, G, gain, bias, stats=True, out_dtype=F32)
+    assert torch.equal(y[0], bias.expand(S, C)) and bool((mean[0] == 7.25).all())
+    X = x[1].double().reshape(S, G, 4)
+    m = X.mean((0, 2), keepdim=True)
+    r = (X.sub(m).square().mean((0, 2), keepdim=True) + 1e-5).rsqrt()
+    # joins: 8 cells and a batch's steps a thread, 32 lanes, slabs of 4 channels by 1024
+    assert ((rstd[1].double() / r[0, :, 0] - 1).abs() <= 100 * U).all()
+    assert ((mean[1].double() - m[0, :, 0]).abs() <= 4 * U * m[0, :, 0].abs() + 100 * U).all()
+    clean = x.clone()
+    for b, s, c, g in ((2, 0, 5, 1), (3, 8999, 5, 1), (4, 4500, 9, 2)):
+        clean[b, s, c] = 0.0
+        rest = [j for j in range(C) if j // 4 != g]
+        assert y[b, :, 4 * g:4 * g + 4].isnan().all() and y[b][:, rest].isfinite().all()
+    y2 = srnl.group_norm_fwd(clean, G, gain, bias, out_dtype=F32)
+    bad = torch.zeros(B, C, dtype=torch.bool, device="cuda:0")
+    bad[2, 4:8], bad[3, 4:8], bad[4, 8:12] = True, True, True
+    assert torch.equal(torch.where(bad[:, None], 0.0, y), torch.where(bad[:, None], 0.0, y2))
