@@ -12,11 +12,12 @@
 // come straight from memory in the layout the matrix units want, a chunk ahead. Three
 // barriers a chunk.
 //
-// Measured: 16384 tokens, 16 heads of 128, 1.6 us a chunk (410 us, 128 blocks); 4 x
-// 4096 x 8 heads 107 us, with the record 147 us (201 MB of it) and back 153 to 175 us.
+// Measured: 16384 tokens, 16 heads of 128, 1.75 us a chunk (450 us, 128 blocks); 4 x
+// 4096 x 8 heads 120 us, with the record 145 us (201 MB of it) and back 155 to 172 us.
 // The steps' latency bounds it: a barrier, reads of LDS, 12 dependent products, a split,
 // three times a chunk. Four waves that shared a state's rows and added partial products
-// instead of reading the whole state took 20 % longer, k and v through the helpers 10 %.
+// instead of reading the whole state took 20 % longer, k and v through the helpers 10 %,
+// U formed by the helpers from E's tiles 18 %.
 #include "delta_mma.h"
 
 namespace {
@@ -169,7 +170,8 @@ __device__ __forceinline__ v4f values(const Column<true> &c)
 }
 __device__ __forceinline__ v4f values(const Column<false> &c) { return v4f{c.v[0], c.v[1], c.v[2], c.v[3]}; }
 // ... and its outputs; tokens past the item's length get zeros. bf16 ones pass the
-// caches, as what is recorded does (16384 tokens x 16 heads of 128: 423 -> 411 us).
+// caches, as what is recorded does (4 x 4096 x 8 heads with the record: 145 us, 153 not
+// so; alone no difference).
 template <bool BF, class P>
 __device__ __forceinline__ void store_values(const DeltaArgs &a, const P &pl, void *p, int c, int j, v4f v)
 {
@@ -685,7 +687,7 @@ namespace srnl_i {
 srnl_status launch_delta_chain(const DeltaArgs &a, bool backward, hipStream_t st)
 {
     // 32 columns a block; 16 where that leaves compute units idle: 16 chunks of 128 with
-    // the record take 64 us with 256 blocks of 32 (16: 80), 54 with 128 of 32 (16: 39)
+    // the record take 64 us with 256 blocks of 32 (16: 79), 58 with 128 of 32 (16: 39)
     const bool narrow = a.Dv <= 16 || static_cast<long long>(a.B) * a.H * ((a.Dv + 31) / 32) < 256;
 #define SRNL_DELTA_CHAIN(BF, KD)                   \
     if (narrow)                                    \

@@ -23,7 +23,7 @@
 // Heads that share q and k write their parts in fp32, and a second kernel adds them
 // in order.
 //
-// 2048 chunks of 128 x 128 take 192 us, eight rounds of one block a CU: of a block's 24
+// 2048 chunks of 128 x 128 take 202 us, eight rounds of one block a CU: of a block's 25
 // us half goes to the walk, where a step's products (2500 cycles) and LDS reads (2400)
 // only partly overlap with two waves a SIMD, 2 us each to the first loads, the 64 x 64
 // parts, the states' terms and the norms, 1 us to the last products and the stores.
@@ -180,7 +180,8 @@ template <bool BF, int KD> __global__ __launch_bounds__(512) void delta_grads_ke
                 Y[x] = mma(y, e, Y[x]);
             }
         }
-        // a tile's operands are read while the one before is multiplied (205 us without, 200)
+        // a tile's operands are read while the one before is multiplied (with matrices of
+        // two words below 200 us, 205 without; with three no difference is left)
         In<BF> ro[2];
         Mid<BF, 3> rv[2], re[2];
         ro[0] = in.O.get_in(16 * rt0 + l15, quad), rv[0] = in.V.get(16 * rt0 + l15, quad), re[0] = in.E.get(16 * rt0 + l15, quad);

@@ -181,8 +181,8 @@ template <bool BF> __device__ __forceinline__ void put_value(const Buf &b, int o
 // columns: element of a row and column, of rows rows.
 __device__ __forceinline__ int record_at(int row, int col, int rows) { return ((col >> 3) * rows + row) * 8 + (col & 7); }
 // They are stored past the caches (the nt bit): written as others are, they put q, k, X
-// and P, which a head's blocks share, out of the L2, and the chain takes 168 us forward
-// and 196 back at 4 x 4096 x 8 heads of 128, not 149 and 174.
+// and P, which a head's blocks share, out of the L2, and the chain takes 167 us forward
+// and 192 back at 4 x 4096 x 8 heads of 128, not 145 and 172.
 constexpr int NT_STORE = 2;
 // four or eight fp32 values from o on, a multiple of 4
 __device__ __forceinline__ void put4(const Buf &b, int o, bool live, v4f v)
@@ -288,7 +288,7 @@ template <bool BF, int PL> __device__ __forceinline__ void frag_store(const Buf 
 // ROWS rows of K split values in LDS, a plane for each word. Rows are 32 bytes longer
 // than their values, so that 16 rows' reads of one piece of 16 bytes meet no bank
 // twice (16 bytes suit writes of 8 bytes a lane better, 73 cycles and not 82, but the
-// kernels read more: with them the gradient kernel takes 235 us, not 230).
+// kernels read more: the gradient kernel takes as long with either).
 template <bool BF, int PL, int ROWS, int K> struct Split {
     static constexpr int PLANES = BF ? PL : 1, ROW = K * (BF ? 2 : 4) + 32;
     __attribute__((aligned(16))) char b[PLANES][ROWS][ROW];

@@ -7,8 +7,9 @@
 // matrix products whose result is the next one's operand without a move (its rows
 // 4 quad + s serve as the reduction elements of step s).
 //
-// 2048 chunks of 128 take 32 us: 67 MB of q and k in, 68 MB out, 4.2 TB/s. Four blocks
-// a CU; one chunk alone takes 8 us, a chain of loads, sums, substitution and blocks.
+// 2048 chunks of 128 take 32 to 34 us: 67 MB of q and k in, 81 MB out, 4.5 TB/s. Four
+// blocks a CU; one chunk alone takes 8 us, a chain of loads, sums, substitution and
+// blocks, so that 6272 chunks of 32 (61 us) are bound by their latency as much.
 #include "delta_mma.h"
 
 namespace {
@@ -222,8 +223,8 @@ srnl_status launch_delta_prep(const DeltaArgs &a, bool transposed, hipStream_t s
     const long long chunks = static_cast<long long>(a.B) * a.H * a.N;
     const dim3 grid(static_cast<unsigned>(chunks));
     // X and P stay in the caches for the chain only while they fit. Written past them,
-    // this kernel and the chain take 139 us for 2048 chunks with k and v of 128 (137
-    // not so), 231 for 3584 (243) and 132 for 6272 with 32 (152).
+    // this kernel and the chain take 197 us for 2048 chunks of a record with k and v of
+    // 128 (180 not so), 292 for 3584 without (310) and 135 for 6272 with 32 (165).
     const bool past = chunks * 2 * DELTA_SQUARE > 128ll << 20;
 #define SRNL_DELTA_PREP(BF, KD)                                                                    \
     if (transposed)                                                                                \
