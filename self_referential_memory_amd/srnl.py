@@ -1021,10 +1021,11 @@ def _delta_params(sizes, q, k, v, g, beta, state, lengths, scale, norm_eps, stre
         _dtype_code(q), sizes[4] ** -0.5 if scale is None else scale, norm_eps, _stream(stream, q))
 
 
-def _written(state: torch.Tensor) -> None:
+def _written(state: Optional[torch.Tensor]) -> None:
     """States go from call to call in one tensor: a graph that holds what was in it
     has to notice, as of torch's own in-place operations."""
-    torch._C._increment_version((state,))
+    if state is not None:
+        torch._C._increment_version((state,))
 
 
 def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
@@ -1041,7 +1042,7 @@ def gated_delta_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch
     # (_tracked, without its loop's 1.5 us on the host)
     if (torch.is_grad_enabled()
             and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad
-                 or beta.requires_grad or state.requires_grad
+                 or beta.requires_grad or (state is not None and state.requires_grad)
                  or (state_out is not None and state_out.requires_grad)
                  or (out is not None and out.requires_grad))
             or forward_ad._current_level >= 0 and _tracked(q, k, v, g, beta, state, state_out, out)):

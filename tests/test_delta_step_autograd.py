@@ -48,3 +48,12 @@ def test_a_tracked_buffer_raises():
         next(iter(kw.values())).requires_grad_()
         with pytest.raises(RuntimeError, match="no gradient"):
             srnl.gated_delta_step(*a, **kw)
+
+
+def test_no_states_at_all():
+    a = args()
+    with pytest.raises(ValueError, match="GPU"):
+        srnl.gated_delta_step(*a[:5], None)
+    a[0].requires_grad_()
+    with pytest.raises(RuntimeError, match="no gradient"):
+        srnl.gated_delta_step(*a[:5], None)

@@ -78,3 +78,12 @@ def test_states_written_in_place_are_noticed_by_autograd():
     with torch.inference_mode():
         y = {n: t.clone() for n, t in x.items() if t is not None}
         srnl.gated_delta_step(*(y[n] for n in ("q", "k", "v", "g", "beta")), y["state"])
+
+
+def test_a_step_without_states():
+    """None: zeros before, none after."""
+    x = inputs(2, 3)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    out, state = srnl.gated_delta_step(*args, None)
+    want, _ = srnl.gated_delta_step(*args, torch.zeros_like(x["state"]))
+    assert state is None and torch.equal(out, want)
